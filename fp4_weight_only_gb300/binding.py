@@ -49,6 +49,27 @@ class PlanInfo(ctypes.Structure):
                 ("units", ctypes.c_int64), ("workspace_bytes", ctypes.c_uint64)]
 
 
+class KvCacheInfo(ctypes.Structure):
+    """petit_kv_cache_t"""
+    _fields_ = [("data", _c_p), ("scales", _c_p), ("num_pages", _c_i64), ("page_stride", _c_i64),
+                ("page_size", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("fmt", ctypes.c_int32)]
+
+
+class Rows(ctypes.Structure):
+    """petit_rows_t"""
+    _fields_ = [("data", _c_p), ("token_stride", _c_i64), ("head_stride", _c_i64)]
+
+
+class KvAttentionArgs(ctypes.Structure):
+    """petit_kv_attention_t"""
+    _fields_ = [("q", Rows), ("out", Rows), ("lse", _c_p), ("block_table", _c_p), ("seq_lens", _c_p),
+                ("q_offsets", _c_p), ("batch", _c_i64), ("total_q", _c_i64), ("max_q", _c_i64),
+                ("max_pages", _c_i64), ("table_stride", _c_i64), ("num_q_heads", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("scale", ctypes.c_float), ("causal", ctypes.c_int32),
+                ("window", _c_i64)]
+
+
 # name -> (restype, argtypes)
 SIGNATURES = {
     "petit_layout_version": (ctypes.c_int, []),
@@ -89,6 +110,11 @@ SIGNATURES = {
                                        ctypes.POINTER(PlanInfo), _c_p, _c_i64]),
     "petit_plan_moe": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_i64, ctypes.c_int, ctypes.c_int,
                                       ctypes.c_int, ctypes.POINTER(PlanInfo), _c_p, _c_i64]),
+    "petit_kv_page_bytes": (_c_sz, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int]),
+    "petit_kv_append": (ctypes.c_int, [_c_p, _c_p, _c_p, ctypes.c_int, _c_p, _c_i64, _c_p, _c_sz, _c_p]),
+    "petit_kv_read": (ctypes.c_int, [_c_p, _c_p, _c_i64, _c_p, _c_p, ctypes.c_int, _c_p, _c_sz, _c_p]),
+    "petit_kv_attention_workspace_bytes": (_c_sz, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int]),
+    "petit_kv_attention": (ctypes.c_int, [_c_p, _c_p, _c_p, _c_sz, _c_p]),
     "petit_device_limits": (ctypes.c_int, [ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int)]),
 }
 
@@ -390,6 +416,164 @@ def device_limits():
 def selftest_timeout(workspace, timeout_us=1000):
     _check(load().petit_selftest_timeout(_ptr(workspace.buf), workspace.buf.numel(), timeout_us, _stream()),
            "selftest_timeout")
+
+
+# ------------------------------------------------------------ 4-bit K/V cache
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+
+
+@functools.lru_cache(maxsize=64)
+def _kv_workspace_bytes(device, heads, dim, fmt):
+    return int(load().petit_kv_attention_workspace_bytes(heads, dim, FORMATS[fmt]))
+
+
+class KVCache:
+    """A paged cache of attention keys and values in 4 bits (petit.h gives its
+    memory order): `num_pages` pages of `page_size` tokens of `num_kv_heads`
+    heads.  NVFP4 scales are relative to an FP32 scale per head, for K and for
+    V: `scales`, an FP32 CUDA tensor [2, num_kv_heads] (by default ones).
+    `data` takes over existing memory, uint8 [num_pages, >= page bytes] with
+    contiguous rows; by default it is allocated and zero-filled."""
+
+    def __init__(self, num_pages, page_size, num_kv_heads, head_dim, fmt="nvfp4", scales=None, data=None,
+                 device=None):
+        if fmt not in ("nvfp4", "mxfp4"):
+            raise ValueError("fmt: need 'nvfp4' or 'mxfp4'")
+        page = load().petit_kv_page_bytes(page_size, num_kv_heads, head_dim, FORMATS[fmt])
+        if page == 0 or num_pages < 1:
+            raise PetitError(2, "kv cache geometry")
+        if data is None:
+            data = torch.zeros((num_pages, page), dtype=torch.uint8, device=torch.device(device or "cuda"))
+        elif (not data.is_cuda or data.dtype != torch.uint8 or data.dim() != 2 or data.shape[0] != num_pages
+              or data.shape[1] < page or data.stride(1) != 1 or (num_pages > 1 and data.stride(0) < page)):
+            raise ValueError(f"data: need a CUDA uint8 tensor [{num_pages}, >= {page}] with contiguous rows")
+        if scales is not None:
+            if fmt == "mxfp4":
+                raise ValueError("scales: MXFP4 has none")
+            _need(scales, torch.float32, "scales")
+            if tuple(scales.shape) != (2, num_kv_heads):
+                raise ValueError(f"scales: need shape (2, {num_kv_heads})")
+            if scales.device != data.device:
+                raise ValueError("scales: need the cache's device")
+        self.data, self.scales, self.fmt = data, scales, fmt
+        self.num_pages, self.page_size = num_pages, page_size
+        self.num_kv_heads, self.head_dim = num_kv_heads, head_dim
+        self.page_bytes = page
+        self.info = KvCacheInfo(_ptr(data), _ptr(scales) if scales is not None else None, num_pages,
+                                data.stride(0) if num_pages > 1 else page, page_size, num_kv_heads, head_dim,
+                                FORMATS[fmt])
+        self._ref = ctypes.addressof(self.info)
+
+    def append(self, k, v, slots, workspace=None):
+        return kv_append(self, k, v, slots, workspace)
+
+    def read(self, slots, dtype=torch.bfloat16, workspace=None, out=None):
+        return kv_read(self, slots, dtype, workspace, out)
+
+    def attention(self, q, block_table, seq_lens, q_offsets=None, max_q=1, **kwargs):
+        return kv_attention(self, q, block_table, seq_lens, q_offsets, max_q, **kwargs)
+
+
+def _rows(t, cache, heads, dtype, name, tokens=None):
+    """petit_rows_t of a [tokens, heads, D] tensor whose last dimension is contiguous."""
+    if (t.dim() != 3 or t.dtype != dtype or t.device != cache.data.device or t.shape[1] != heads
+            or t.shape[2] != cache.head_dim or t.stride(2) != 1):
+        raise ValueError(f"{name}: need a {dtype} tensor [tokens, {heads}, {cache.head_dim}] on the cache's device, "
+                         "contiguous in its last dimension")
+    if tokens is not None and t.shape[0] != tokens:
+        raise ValueError(f"{name}: need {tokens} tokens")
+    return Rows(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def _indices(t, cache, dtype, shape, name):
+    if t.dtype != dtype or t.device != cache.data.device or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: need a contiguous {dtype} tensor {list(shape)} on the cache's device")
+    return t.data_ptr()
+
+
+def _status_buf(workspace):
+    return (None, 0) if workspace is None else (_ptr(workspace.buf), workspace.buf.numel())
+
+
+def kv_append(cache, k, v, slots, workspace=None):
+    """Quantise rows k and v ([tokens, num_kv_heads, head_dim], BF16 or FP16,
+    any token and head stride that is a multiple of 8) and write token i to
+    slot slots[i] (int64; slot = page * page_size + offset).  Negative slots
+    are skipped; a slot past the cache is skipped and recorded in `workspace`
+    (see :meth:`Workspace.status`) if one is given."""
+    if k.dtype not in _DTYPES:
+        raise ValueError("k: need BF16 or FP16")
+    n = k.shape[0]
+    rk = _rows(k, cache, cache.num_kv_heads, k.dtype, "k")
+    rv = _rows(v, cache, cache.num_kv_heads, k.dtype, "v", n)
+    buf, nbytes = _status_buf(workspace)
+    _check(load().petit_kv_append(cache._ref, ctypes.byref(rk), ctypes.byref(rv), _DTYPES[k.dtype],
+                                  _indices(slots, cache, torch.int64, (n,), "slots"), n, buf, nbytes, _stream()),
+           "kv_append")
+
+
+def kv_read(cache, slots, dtype=torch.bfloat16, workspace=None, out=None):
+    """The values of the tokens in `slots` as (K, V), each [tokens,
+    num_kv_heads, head_dim] in `dtype`; a negative slot (or one past the
+    cache, which is recorded in `workspace`) gives zeros."""
+    if dtype not in _DTYPES:
+        raise ValueError("dtype: need torch.bfloat16 or torch.float16")
+    n = slots.numel()
+    if out is None:
+        shape = (n, cache.num_kv_heads, cache.head_dim)
+        out = (torch.empty(shape, dtype=dtype, device=cache.data.device),
+               torch.empty(shape, dtype=dtype, device=cache.data.device))
+    rk = _rows(out[0], cache, cache.num_kv_heads, dtype, "out[0]", n)
+    rv = _rows(out[1], cache, cache.num_kv_heads, dtype, "out[1]", n)
+    buf, nbytes = _status_buf(workspace)
+    _check(load().petit_kv_read(cache._ref, _indices(slots, cache, torch.int64, (n,), "slots"), n, ctypes.byref(rk),
+                                ctypes.byref(rv), _DTYPES[dtype], buf, nbytes, _stream()), "kv_read")
+    return out
+
+
+def kv_attention(cache, q, block_table, seq_lens, q_offsets=None, max_q=1, scale=None, causal=True, window=0,
+                 workspace=None, out=None, lse=None):
+    """softmax(scale * q k^T + mask) v over the cached sequences.
+
+    q: BF16 or FP16 [total_q, num_q_heads, head_dim], the queries of all
+    sequences one after the other; block_table: int32 [batch, max_pages];
+    seq_lens: int32 [batch], the cached tokens of each sequence, its queries'
+    own among them.  q_offsets: int32 [batch + 1], where each sequence's
+    queries begin; None: max_q queries for every sequence.  max_q: the most
+    queries of a sequence.  scale: by default head_dim ** -0.5.  causal: the
+    last query sees every key, the one before it all but the last, and so on;
+    window > 0 keeps the nearest `window` of them.  lse: an FP32 tensor
+    [total_q, num_q_heads] that receives the log of the softmax's sum.  A
+    query that sees no key gives zeros (and an lse of -inf)."""
+    if q.dtype not in _DTYPES or q.dim() != 3:
+        raise ValueError("q: need a BF16 or FP16 tensor [total_q, num_q_heads, head_dim]")
+    total_q, heads = q.shape[0], q.shape[1]
+    if heads < 1 or heads % cache.num_kv_heads:
+        raise ValueError(f"q: need a multiple of {cache.num_kv_heads} heads")
+    if block_table.dim() != 2 or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("block_table: need [batch, max_pages] with contiguous rows")
+    batch, max_pages = block_table.shape
+    if block_table.dtype != torch.int32 or block_table.device != cache.data.device:
+        raise ValueError("block_table: need int32 on the cache's device")
+    if out is None:
+        out = torch.empty((total_q, heads, cache.head_dim), dtype=q.dtype, device=q.device)
+    args = KvAttentionArgs(
+        _rows(q, cache, heads, q.dtype, "q"), _rows(out, cache, heads, q.dtype, "out", total_q),
+        None if lse is None else _ptr(lse), _ptr(block_table),
+        _indices(seq_lens, cache, torch.int32, (batch,), "seq_lens"),
+        None if q_offsets is None else _indices(q_offsets, cache, torch.int32, (batch + 1,), "q_offsets"),
+        batch, total_q, int(max_q), max_pages, max(block_table.stride(0), max_pages) if batch > 1 else max_pages,
+        heads, _DTYPES[q.dtype], cache.head_dim ** -0.5 if scale is None else float(scale), int(bool(causal)),
+        int(window))
+    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (total_q, heads)
+                            or not lse.is_contiguous() or lse.device != cache.data.device):
+        raise ValueError(f"lse: need a contiguous FP32 tensor [{total_q}, {heads}] on the cache's device")
+    ws = workspace or Workspace(q.device)
+    need = _kv_workspace_bytes(torch.cuda.current_device(), cache.num_kv_heads, cache.head_dim, cache.fmt)
+    buf = ws.ensure(need)
+    _check(load().petit_kv_attention(cache._ref, ctypes.byref(args), _ptr(buf), buf.numel(), _stream()),
+           "kv_attention")
+    return out
 
 
 class FP4Weight:

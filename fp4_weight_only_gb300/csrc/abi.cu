@@ -268,6 +268,8 @@ petit_status_t describe_plan(const petit::GemmPlan& pl, petit_plan_info_t* info,
 
 }  // namespace
 
+int petit::usable_device(int* sms, int* dev) { return current_device(sms, dev); }
+
 extern "C" {
 
 int petit_layout_version(void) { return petit::kLayoutVersion; }

@@ -74,6 +74,9 @@ int tile_override();   // bn | ku << 16, or 0
 // normal build.
 bool bounds_checking();
 bool set_check_limits(int64_t weight_bytes, int64_t c_elems);
+// Checks that the current device can run this library's kernels and gives its
+// SM count and index; returns a petit_status_t.
+int usable_device(int* sms, int* dev = nullptr);
 // row_off: num_groups + 1 non-decreasing offsets starting at 0
 GemmPlan plan_grouped(const int64_t* row_off, int num_groups, int64_t n, int64_t k, int fmt,
                       int num_sms, int pair_cap);

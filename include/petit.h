@@ -69,7 +69,7 @@ typedef enum petit_status {
   PETIT_ERR_ARCH = 5,              /* current device is not sm_103 */
   PETIT_ERR_CUDA = 6,              /* a CUDA runtime call failed */
   PETIT_ERR_TIMEOUT = 7,           /* a bounded device-side wait ran out */
-  PETIT_ERR_BOUNDS = 8             /* an index check failed (bounds-checking build only) */
+  PETIT_ERR_BOUNDS = 8             /* an index check failed (bounds-checking build; cache indices) */
 } petit_status_t;
 
 typedef enum petit_format {
@@ -292,6 +292,126 @@ petit_status_t petit_gemm_bf16_nvfp4_noalloc(const void* A, const uint8_t* rep,
                                              int64_t m, int64_t n, int64_t k,
                                              petit_stream_t stream);
 
+/* ------------------------------------------------------- 4-bit K/V cache */
+
+/* A paged cache of attention keys and values held in the two FP4 formats,
+ * and the attention that reads it.  For every token and K/V head the cache
+ * holds D = head_dim codes of K and of V, with one scale per block along D:
+ *
+ *   NVFP4: value = code * e4m3 scale * g   (16 elements; g: FP32, one for K
+ *          and one for V of every head, `scales`)
+ *   MXFP4: value = code * e8m0 scale       (32 elements; `scales` NULL)
+ *
+ * quantised as petit_quantize_nvfp4 / _mxfp4 do (MXFP4 scales stop at 2^125,
+ * so that every value is a finite BF16 number).
+ *
+ * Memory order.  Page p begins at byte p * page_stride of `data`; a page
+ * holds its heads one after the other; a head's part of a page is
+ * page_size / 16 groups of 16 consecutive tokens; a group is
+ *   K codes [16][D/2] | K scales [16][D/B] | V codes [16][D/2] | V scales
+ *   [16][D/B]                       (bytes; B = 16 or 32, the block)
+ * with element 2j of a row in the low nibble of byte j.  So any run of whole
+ * groups of a head's page is contiguous and is fetched with one bulk copy.
+ * Token slot s is token s % page_size of page s / page_size. */
+typedef struct petit_kv_cache {
+  void* data;           /* (device) num_pages * page_stride bytes, 16-byte aligned */
+  const float* scales;  /* (device) FP32 [2][num_kv_heads]: K's, then V's; NULL: 1.0 */
+  int64_t num_pages;
+  int64_t page_stride;  /* bytes between pages: >= petit_kv_page_bytes, a multiple of 16 */
+  int32_t page_size;    /* tokens a page: 16, 32, 64, 128 or 256 */
+  int32_t num_kv_heads; /* 1..1024 */
+  int32_t head_dim;     /* 64 or 128 */
+  int32_t fmt;          /* PETIT_FMT_NVFP4 or PETIT_FMT_MXFP4 */
+} petit_kv_cache_t;
+
+/* 16-bit element types of rows that enter or leave the cache. */
+typedef enum petit_dtype { PETIT_BF16 = 0, PETIT_F16 = 1 } petit_dtype_t;
+
+/* Rows [tokens][heads][D] of 16-bit elements, D contiguous; the strides, in
+ * elements, are multiples of 8 and `data` is 16-byte aligned. */
+typedef struct petit_rows {
+  void* data;
+  int64_t token_stride;
+  int64_t head_stride;
+} petit_rows_t;
+
+/* Bytes of one page without padding; 0 if the arguments are not valid. */
+size_t petit_kv_page_bytes(int32_t page_size, int32_t num_kv_heads, int32_t head_dim, int fmt);
+
+/* Quantises num_tokens rows of K and of V and writes token i to slot
+ * slots[i] (device int64).  Negative slots are skipped (padding).  A slot at
+ * or past num_pages * page_size is skipped too, and PETIT_ERR_BOUNDS is
+ * recorded in `workspace` (device, >= 256 bytes, zero-filled once; or NULL:
+ * not recorded).  Slots of one call must be distinct.  NaN becomes code 0
+ * and infinities saturate, so that no written value is NaN or infinite.
+ * num_tokens = 0 is valid and enqueues nothing.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE (cache geometry, more than 2^24
+ * tokens or 2^31 rows), MISALIGNED (data, rows or strides), WORKSPACE, ARCH,
+ * CUDA. */
+petit_status_t petit_kv_append(const petit_kv_cache_t* cache, const petit_rows_t* k,
+                               const petit_rows_t* v, int dtype, const int64_t* slots,
+                               int64_t num_tokens, void* workspace, size_t workspace_bytes,
+                               petit_stream_t stream);
+
+/* Writes the values of the tokens in `slots` to rows k_out and v_out, rounded
+ * to dtype (nearest even).  A negative slot gives a row of zeros, and so does
+ * a slot past the cache (recorded as above).  Errors as petit_kv_append. */
+petit_status_t petit_kv_read(const petit_kv_cache_t* cache, const int64_t* slots,
+                             int64_t num_tokens, const petit_rows_t* k_out,
+                             const petit_rows_t* v_out, int dtype, void* workspace,
+                             size_t workspace_bytes, petit_stream_t stream);
+
+/* Attention of packed query rows over cached sequences.  Sequence b has
+ * len = seq_lens[b] cached tokens (its own queries' tokens among them), the
+ * j-th in page block_table[b * table_stride + j / page_size], and nq
+ * consecutive query rows from row q_offsets[b] on (nq = q_offsets[b + 1] -
+ * q_offsets[b]; q_offsets NULL: nq = max_q for every sequence).  Query head a
+ * reads K/V head a / (num_q_heads / num_kv_heads).  Query i of a sequence is
+ * the token at position p = len - nq + i and sees the keys
+ *     j < len;  causal: j <= p;  window > 0 (causal only): j > p - window
+ *     x_j = scale * q . k_j,  out = sum_j softmax(x)_j v_j,
+ *     lse = log(sum_j exp(x_j))        (natural logarithm, FP32)
+ * A query that sees no key (len = 0, or p < 0) gets out = 0 and lse = -inf.
+ * Products are FP16 by FP16 in FP32 (MXFP4 values of long prompts: BF16);
+ * scores, the softmax's maximum and sum, and the output's sums are FP32.
+ *
+ * A length past max_pages * page_size, a page outside the cache and query
+ * offsets outside 0..total_q are recorded as PETIT_ERR_BOUNDS in the
+ * workspace; the length is cut, the page's keys are left out, the sequence
+ * is left out.  Rows of `out` that no sequence covers are not written. */
+typedef struct petit_kv_attention {
+  petit_rows_t q;             /* [total_q][num_q_heads][D] */
+  petit_rows_t out;           /* [total_q][num_q_heads][D], not overlapping q */
+  float* lse;                 /* (device) [total_q][num_q_heads], or NULL */
+  const int32_t* block_table; /* (device) [batch][max_pages] */
+  const int32_t* seq_lens;    /* (device) [batch] */
+  const int32_t* q_offsets;   /* (device) [batch + 1], or NULL */
+  int64_t batch;              /* 0..2^20; 0 enqueues nothing */
+  int64_t total_q;            /* query rows; batch * max_q if q_offsets is NULL */
+  int64_t max_q;              /* most query rows of a sequence (chooses the kernel;
+                                 longer sequences are still right) */
+  int64_t max_pages;          /* max_pages * page_size <= 2^30 */
+  int64_t table_stride;       /* entries between rows of block_table, >= max_pages */
+  int32_t num_q_heads;        /* a multiple of num_kv_heads */
+  int32_t dtype;              /* of q and out */
+  float scale;
+  int32_t causal;             /* 0 or 1 */
+  int64_t window;             /* 0: none */
+} petit_kv_attention_t;
+
+/* Bytes of workspace petit_kv_attention needs on the current device for this
+ * cache geometry: a size that holds for any batch and lengths.  0 if the
+ * arguments are not valid or no device is usable.  The workspace is used and
+ * kept as a GEMM's (zero-filled once; may be shared with GEMMs on the same
+ * stream). */
+size_t petit_kv_attention_workspace_bytes(int32_t num_kv_heads, int32_t head_dim, int fmt);
+
+/* Runs it.  Nothing about the sequences is read on the host, so a captured
+ * graph follows changed lengths, tables and offsets.  Errors: INVALID_ARG,
+ * UNSUPPORTED_SHAPE, MISALIGNED, WORKSPACE, ARCH, CUDA. */
+petit_status_t petit_kv_attention(const petit_kv_cache_t* cache, const petit_kv_attention_t* args,
+                                  void* workspace, size_t workspace_bytes, petit_stream_t stream);
+
 /* ------------------------------------------------------------------ tuning */
 
 /* Forces the tile shape of every later GEMM plan in this process, for tile
@@ -401,7 +521,8 @@ petit_status_t petit_check_set_limits(int64_t weight_bytes, int64_t c_elems);
  * PETIT_ERR_TIMEOUT (a bounded wait ran out in some earlier call on this
  * workspace), PETIT_ERR_BOUNDS (in the bounds-checking build of the
  * library, _petit_check.so: a kernel found an index outside its buffer,
- * skipped that access and stopped) or PETIT_ERR_CUDA.  When the word is not
+ * skipped that access and stopped; in both builds: a K/V cache call met a
+ * slot, page, length or offset outside its range) or PETIT_ERR_CUDA.  When the word is not
  * zero it is cleared,
  * together with the split-tile arrival counters (bytes 256..4351, when
  * workspace_bytes covers them) that a kernel which stopped early may have
