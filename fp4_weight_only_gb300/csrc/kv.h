@@ -71,6 +71,12 @@ cudaError_t launch_kv_read(const KvCacheArgs& c, const int64_t* slots, int64_t n
 // Workspace of the attention kernels on a device with num_sms SMs: the
 // header and counters of a GEMM's workspace, then partial results.
 size_t kv_attention_workspace(int head_dim, int num_sms);
+// The kernel for many query rows (kv_prompt.cu), for groups of at most
+// kKvPromptGroup query heads, and its share of the workspace.
+constexpr int kKvPromptGroup = 128;
+constexpr int kKvPromptCtas = 160;
+size_t kv_prompt_partials(int head_dim, int num_sms);
+cudaError_t launch_kv_prompt(const KvAttnArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_kv_attention(const KvAttnArgs& a, int num_sms, cudaStream_t stream);
 
 }  // namespace petit

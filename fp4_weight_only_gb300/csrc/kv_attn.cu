@@ -24,7 +24,7 @@
 //    transposes (movmatrix), with no shared memory.
 // Both products are FP16: codes times NVFP4 scales are exact in FP16, q is
 // brought into FP16's range by a power of two per row (exact but for elements
-// 2^37 below the row's largest), and p is rounded to 11 bits, which adds less
+// 2^26 below the row's largest), and p is rounded to 11 bits, which adds less
 // than the rounding of a 16-bit output.  MXFP4 scales exceed FP16's range:
 // K's are taken relative to the token's largest and V's relative to the
 // largest seen in the dimension block, and the difference is applied in FP32
@@ -43,6 +43,7 @@
 #include "internal.h"
 #include "kv.h"
 #include "kv_layout.cuh"
+#include "kv_math.cuh"
 #include "ptx.cuh"
 
 namespace petit {
@@ -72,29 +73,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   uint32_t d;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
-}
-
-__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-// FP16 bits of 2^n, n <= 15: subnormal below 2^-14, zero below 2^-24.
-__device__ __forceinline__ uint32_t f16_power(int n) {
-  return n >= -14 ? static_cast<uint32_t>(n + 15) << 10 : 0x400u >> min(-14 - n, 31);
 }
 
 __device__ __forceinline__ void consumers_sync() {
@@ -128,7 +106,7 @@ __device__ __forceinline__ Seq load_seq(const KvAttnArgs& a, int b, int rows_per
     s.q0 = static_cast<int>(b * a.max_q);
     s.nq = static_cast<int>(a.max_q);
   }
-  if (bad && threadIdx.x == 0) atomicOr(status, kStatusBounds);
+  if (bad) atomicOr(status, kStatusBounds);
   s.lo = 0;
   if (a.window > 0) {
     const int64_t first = static_cast<int64_t>(s.len) - s.nq - a.window + 1;
@@ -292,13 +270,7 @@ __device__ __forceinline__ void store_row(const KvAttnArgs& a, const Seq& s, int
   const float inv = L == 0.0f ? 0.0f : gv / L;   // no key: zeros
   uint32_t w[D / 64];
 #pragma unroll
-  for (int i = 0; i < D / 64; ++i) {
-    const float x = acc[2 * i] * inv, y = acc[2 * i + 1] * inv;
-    if (a.bf16)
-      *reinterpret_cast<__nv_bfloat162*>(&w[i]) = __floats2bfloat162_rn(x, y);
-    else
-      *reinterpret_cast<__half2*>(&w[i]) = __floats2half2_rn(x, y);
-  }
+  for (int i = 0; i < D / 64; ++i) w[i] = pack2(acc[2 * i] * inv, acc[2 * i + 1] * inv, a.bf16);
   uint16_t* dst = static_cast<uint16_t*>(a.out.data) + tok * a.out.token_stride + head * a.out.head_stride +
                   lane * (D / 32);
   if constexpr (D == 128)
@@ -451,11 +423,7 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv_attn_kernel(cons
           const uint32_t wd[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            float2 f;
-            if (a.bf16)
-              f = make_float2(__uint_as_float(wd[j] << 16), __uint_as_float(wd[j] & 0xFFFF0000u));
-            else
-              f = __half22float2(*reinterpret_cast<const __half2*>(&wd[j]));
+            const float2 f = unpack2(wd[j], a.bf16);
             x[8 * i + 2 * j] = f.x;
             x[8 * i + 2 * j + 1] = f.y;
           }
@@ -466,10 +434,7 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv_attn_kernel(cons
       for (int i = 0; i < D / 4; ++i) amax = fmaxf(amax, fabsf(x[i]));
       amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-      // the largest element to 2^12..2^13: products with values up to 6 * 2^12 and
-      // sums over D stay far inside FP32, small elements far above FP16's least
-      const int e = static_cast<int>(__float_as_uint(amax) >> 23);
-      const int shift = amax == 0.0f ? 0 : min(139 - e, 127);
+      const int shift = row_shift(amax);
       const float up = ldexpf(1.0f, shift);
 #pragma unroll
       for (int kk = 0; kk < kK; ++kk)
@@ -848,11 +813,14 @@ cudaError_t launch_as(const KvAttnArgs& a, int num_sms, cudaStream_t stream) {
 
 size_t kv_attention_workspace(int head_dim, int num_sms) {
   const int ctas = 2 * num_sms < kMaxCtas_ ? 2 * num_sms : kMaxCtas_;
-  return kWsHeaderBytes + kWsCountersBytes + sizeof(float) * 2 * ctas * Partials<4>::floats(head_dim);
+  const size_t own = sizeof(float) * 2 * ctas * Partials<4>::floats(head_dim);
+  const size_t prompt = kv_prompt_partials(head_dim, num_sms);
+  return kWsHeaderBytes + kWsCountersBytes + (own > prompt ? own : prompt);
 }
 
 cudaError_t launch_kv_attention(const KvAttnArgs& a, int num_sms, cudaStream_t stream) {
   const int64_t rows = a.max_q * a.group;
+  if (rows > 16 && a.group <= kKvPromptGroup) return launch_kv_prompt(a, num_sms, stream);
   return kv_dispatch(a.cache.head_dim, a.cache.fmt, true, [&](auto d, auto f, auto) {
     if (rows <= 8) return launch_as<d, f, 1>(a, num_sms, stream);
     if (rows <= 16) return launch_as<d, f, 2>(a, num_sms, stream);

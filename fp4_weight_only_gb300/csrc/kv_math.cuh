@@ -1,0 +1,58 @@
+// Small conversions and products of the K/V attention kernels.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+namespace petit {
+
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// FP16 bits of 2^n, n <= 15: subnormal below 2^-14, zero below 2^-24.
+__device__ __forceinline__ uint32_t f16_power(int n) {
+  return n >= -14 ? static_cast<uint32_t>(n + 15) << 10 : 0x400u >> min(-14 - n, 31);
+}
+
+// Two 16-bit elements of a query row in FP32.
+__device__ __forceinline__ float2 unpack2(uint32_t w, bool bf16) {
+  if (bf16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+// The same, rounded, for an output row.
+__device__ __forceinline__ uint32_t pack2(float x, float y, bool bf16) {
+  uint32_t w;
+  if (bf16)
+    *reinterpret_cast<__nv_bfloat162*>(&w) = __floats2bfloat162_rn(x, y);
+  else
+    *reinterpret_cast<__half2*>(&w) = __floats2half2_rn(x, y);
+  return w;
+}
+
+// The power of two that brings a row's largest magnitude to 2^12..2^13 (at
+// most 2^127), as an exponent: the row is then exact in FP16 but for elements
+// 2^26 below its largest, which lose bits, and products with values up to
+// 6 * 2^12 and their sums stay far inside FP32.
+__device__ __forceinline__ int row_shift(float amax) {
+  const int e = static_cast<int>(__float_as_uint(amax) >> 23);
+  return amax == 0.0f ? 0 : min(139 - e, 127);
+}
+
+}  // namespace petit

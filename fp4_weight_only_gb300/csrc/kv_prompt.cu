@@ -1,0 +1,808 @@
+// Attention over the 4-bit K/V cache for many query rows a sequence (prompts
+// and long drafts), on the 5th-generation tensor cores.
+//
+// The rows of a K/V head (query tokens x heads of the group, token by token)
+// are cut into items of up to two 128-row MMA tiles; an item meets its keys
+// 128 at a time:
+//     S_q = Q_q K^T (shared x shared memory -> tensor memory),
+//     P_q = 2^(S_q f - m) (registers, back into S_q's columns as FP16),
+//     O_q += P_q V (tensor x shared memory -> tensor memory),  q = 0, 1.
+// With both formats in FP16 the products are those of kv_attn.cu; what bounds
+// the kernel is the two MMAs (4 D FLOP a row and key) next to the 128 x 128
+// exponentials and the conversion of a 128-key tile of K and V, which two row
+// tiles share.  Warps by role, each with its own barriers:
+//   0-3, 4-7   softmax of row tile 0 and 1: a thread holds a row, so maximum
+//              and sum need no exchange; while one tile's scores are in the
+//              registers the tensor cores work on the other tile
+//   8-11       K: a thread converts a token's row (codes -> FP16, swizzled)
+//   12-15      V: a thread converts 8 tokens by D / 8 dimensions and writes
+//              them transposed (contraction along the tokens)
+//   16         issues the MMAs
+// Codes go from global memory to registers a tile ahead; the converted tiles
+// are double-buffered.  Tensor memory: O_0, O_1, S_0, S_1 (all 512 columns at
+// D = 128).
+//
+// The key tiles of all items are cut into equal ranges as in kv_attn.cu; an
+// item cut between CTAs leaves FP32 partials that the last arriver adds.
+#include <cfloat>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "internal.h"
+#include "kv.h"
+#include "kv_layout.cuh"
+#include "kv_math.cuh"
+#include "ptx.cuh"
+
+namespace petit {
+namespace {
+
+constexpr int kKeys = 128;        // keys of a tile
+constexpr int kRowTile = 128;     // rows of an MMA tile
+constexpr int kRows = 2 * kRowTile;
+constexpr int kKWarp = 8, kVWarp = 12, kMmaWarp = 16;
+constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kRing = 4;          // per-tile facts: written at most two tiles ahead of their last reader
+
+// ------------------------------------------------------------ work split
+struct Seq {
+  int len, nq, q0;
+  int tokens;     // query tokens of an item (whole tokens)
+  int row_tiles;  // items along the rows, per head
+};
+
+__device__ __forceinline__ Seq load_seq(const KvAttnArgs& a, int b, uint32_t* status) {
+  Seq s;
+  const int64_t cap = a.max_pages << a.cache.page_shift;
+  s.len = a.seq_lens[b];
+  bool bad = s.len < 0 || s.len > cap;
+  s.len = s.len < 0 ? 0 : static_cast<int>(s.len < cap ? s.len : cap);
+  if (a.q_offsets) {
+    const int q0 = a.q_offsets[b], q1 = a.q_offsets[b + 1];
+    const bool ok = q0 >= 0 && q1 >= q0 && q1 <= a.total_q;
+    bad = bad || !ok;
+    s.q0 = ok ? q0 : 0;
+    s.nq = ok ? q1 - q0 : 0;
+  } else {
+    s.q0 = static_cast<int>(b * a.max_q);
+    s.nq = static_cast<int>(a.max_q);
+  }
+  if (bad) atomicOr(status, kStatusBounds);
+  s.tokens = kRows / a.group;
+  s.row_tiles = (s.nq + s.tokens - 1) / s.tokens;
+  return s;
+}
+
+struct Keys {
+  int lo;      // first key of tile 0, a multiple of kKeys
+  int tiles;   // at least 1, so that rows without keys are written
+};
+
+__device__ __forceinline__ Keys item_keys(const KvAttnArgs& a, const Seq& s, int rt) {
+  const int t0 = rt * s.tokens, t1 = min(s.nq, t0 + s.tokens) - 1;
+  const int64_t hi = a.causal ? static_cast<int64_t>(s.len) - s.nq + t1 : s.len - 1;
+  const int64_t first = a.window > 0 ? static_cast<int64_t>(s.len) - s.nq + t0 - a.window + 1 : 0;
+  Keys k;
+  k.lo = first > 0 ? static_cast<int>(first) & ~(kKeys - 1) : 0;
+  k.tiles = hi >= k.lo ? static_cast<int>(hi - k.lo) / kKeys + 1 : 1;
+  return k;
+}
+
+// Tiles of a sequence over all its items; every lane of the warp calls it.
+__device__ __forceinline__ int64_t seq_tiles(const KvAttnArgs& a, int b, uint32_t* status) {
+  const Seq s = load_seq(a, b, status);
+  int64_t sum = 0;
+  for (int rt = threadIdx.x & 31; rt < s.row_tiles; rt += 32) sum += item_keys(a, s, rt).tiles;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+  return sum * a.cache.heads;
+}
+
+__device__ __forceinline__ int64_t range_begin(int64_t total, int ctas, int64_t c) { return total * c / ctas; }
+__device__ __forceinline__ int cta_of_tile(int64_t total, int ctas, int64_t x) {
+  return static_cast<int>(((x + 1) * ctas + total - 1) / total) - 1;
+}
+
+// Items in order: sequence, row tile, head.
+struct Walk {
+  int64_t total, pos, end;
+  int ctas;
+  int b, rt, h;
+  Seq s;
+  Keys k;
+  int ta, tb;   // tiles of the item in this range
+
+  __device__ __forceinline__ bool done() const { return pos >= end; }
+  __device__ __forceinline__ void cut() {
+    const int64_t left = end - pos;
+    tb = left < k.tiles - ta ? ta + static_cast<int>(left) : k.tiles;
+  }
+  __device__ __forceinline__ void next(const KvAttnArgs& a, uint32_t* status) {
+    pos += tb - ta;
+    if (pos >= end) return;
+    if (tb == k.tiles) {
+      if (++h == static_cast<int>(a.cache.heads)) {
+        h = 0;
+        if (++rt == s.row_tiles) {
+          rt = 0;
+          do {
+            s = load_seq(a, ++b, status);
+          } while (s.row_tiles == 0 && b + 1 < a.batch);
+        }
+        k = item_keys(a, s, rt);
+      }
+      ta = 0;
+    } else {
+      ta = tb;
+    }
+    cut();
+  }
+};
+
+constexpr int kSeqChunk = 64;
+
+// Every thread of the CTA calls this; sh holds kSeqChunk values.
+__device__ Walk find_range(const KvAttnArgs& a, int64_t* sh, uint32_t* status) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kW = kThreads / 32;
+  auto chunk = [&](int b0) {   // totals of the sequences b0.. into sh; returns their sum
+    __syncthreads();
+    for (int i = warp; i < kSeqChunk; i += kW) {
+      const int64_t t = b0 + i < a.batch ? seq_tiles(a, b0 + i, status) : 0;
+      if (lane == 0) sh[i] = t;
+    }
+    __syncthreads();
+    int64_t sum = sh[lane] + sh[lane + 32];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    return sum;
+  };
+  Walk w{};
+  for (int b0 = 0; b0 < a.batch; b0 += kSeqChunk) w.total += chunk(b0);
+  w.ctas = w.total < gridDim.x ? static_cast<int>(w.total) : static_cast<int>(gridDim.x);
+  if (static_cast<int>(blockIdx.x) >= w.ctas) return w;
+  w.pos = range_begin(w.total, w.ctas, blockIdx.x);
+  w.end = range_begin(w.total, w.ctas, blockIdx.x + 1);
+  int64_t before = 0;
+  int b0 = 0;
+  for (;; b0 += kSeqChunk) {
+    const int64_t sum = a.batch > kSeqChunk ? chunk(b0) : w.total;
+    if (before + sum > w.pos) break;
+    before += sum;
+  }
+  w.b = b0;
+  while (before + sh[w.b - b0] <= w.pos) before += sh[w.b++ - b0];
+  w.s = load_seq(a, w.b, status);
+  // the row tile: prefix sums of 32 at a time
+  for (int rt0 = 0;; rt0 += 32) {
+    const int64_t mine =
+        rt0 + lane < w.s.row_tiles ? static_cast<int64_t>(item_keys(a, w.s, rt0 + lane).tiles) * a.cache.heads : 0;
+    int64_t pre = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xFFFFFFFFu, pre, o);
+      if (lane >= o) pre += v;
+    }
+    const unsigned over = __ballot_sync(0xFFFFFFFFu, before + pre > w.pos);
+    if (over) {
+      const int l = __ffs(over) - 1;
+      w.rt = rt0 + l;
+      before += __shfl_sync(0xFFFFFFFFu, pre - mine, l);
+      break;
+    }
+    before += __shfl_sync(0xFFFFFFFFu, pre, 31);
+  }
+  w.k = item_keys(a, w.s, w.rt);
+  const int64_t in = w.pos - before;
+  w.h = static_cast<int>(in / w.k.tiles);
+  w.ta = static_cast<int>(in - static_cast<int64_t>(w.h) * w.k.tiles);
+  w.cut();
+  return w;
+}
+
+// ------------------------------------------------------------ the kernel
+template <int D>
+struct Smem {
+  alignas(1024) uint8_t q[2][D / 64][kRowTile * 128];   // 64 dimensions a slab, 128-byte swizzle
+  uint8_t k[2][D / 64][kKeys * 128];
+  uint8_t v[2][kKeys / 64][D * 128];                    // 64 tokens a slab
+  uint64_t qfull[2], sfull[2], pfull[2], ofull[2], kfull[2], kfree[2], vfull[2], vfree[2], fin;
+  int64_t scan[kSeqChunk];
+  float kfac[kRing][4];       // MXFP4: factor of the scores of 32 keys
+  float vfac[kRing];          // MXFP4: factor of O before this tile
+  uint32_t valid[kRing][4];   // of 32 keys: bit 0, 1: the 16-key group's page is in the cache
+  int vtop;                   // MXFP4: largest V scale of the tile
+  float vscale[kRing];        // MXFP4: what O needs if the item ends with this tile
+  uint32_t tmem;
+  int abort;
+  int last;
+};
+
+template <int D>
+__host__ __device__ constexpr size_t partial_floats() { return static_cast<size_t>(kRows) * (D + 2); }
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_constant__ KvAttnArgs a) {
+  using S = Smem<D>;
+  using G = KvGroup<D, FMT>;
+  constexpr uint32_t kO = 0, kS = 2 * D;                 // tensor-memory columns
+  constexpr uint32_t kColumns = 512;                     // (384 used at D = 64: sizes are powers of two)
+  constexpr uint32_t kIdescS = idesc_f16_f32(kRowTile, kKeys), kIdescO = idesc_f16_f32(kRowTile, D);
+  extern __shared__ __align__(1024) uint8_t raw[];
+  S& sm = *reinterpret_cast<S*>(raw);
+  uint32_t* status = reinterpret_cast<uint32_t*>(a.workspace);
+  uint32_t* counters = reinterpret_cast<uint32_t*>(a.workspace + kWsHeaderBytes);
+  float* partials = reinterpret_cast<float*>(a.workspace + kWsHeaderBytes + kWsCountersBytes);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // waits never end the CTA: one that runs out raises the flag, later ones
+  // return at once, and every role walks on to its end
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (!mbar_wait_bounded(smem_u32(bar), parity, a.timeout_ns, &sm.abort)) *(volatile int*)&sm.abort = 1;
+    __syncwarp();
+  };
+
+  if (tid == 0) {
+    sm.abort = 0;
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&sm.qfull[i]), 4);
+      mbar_init(smem_u32(&sm.sfull[i]), 1);
+      mbar_init(smem_u32(&sm.pfull[i]), 4);
+      mbar_init(smem_u32(&sm.ofull[i]), 1);
+      mbar_init(smem_u32(&sm.kfull[i]), 4);
+      mbar_init(smem_u32(&sm.kfree[i]), 1);
+      mbar_init(smem_u32(&sm.vfull[i]), 4);
+      mbar_init(smem_u32(&sm.vfree[i]), 1);
+    }
+    mbar_init(smem_u32(&sm.fin), 1);
+    mbar_fence_init();
+  }
+  Walk w = find_range(a, sm.scan, status);   // (synchronises the CTA)
+  if (w.done()) return;
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(&sm.tmem), kColumns);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+  const int64_t head_stride = static_cast<int64_t>(G::kBytes) << (a.cache.page_shift - 4);
+  // 16-token group of `key` in sequence w.b, or null
+  auto group_of = [&](int key) -> const uint8_t* {
+    if (key >= w.s.len) return nullptr;
+    const int64_t page = a.block_table[w.b * a.table_stride + (key >> a.cache.page_shift)];
+    if (page < 0 || page >= a.cache.num_pages) {
+      atomicOr(status, kStatusBounds);
+      return nullptr;
+    }
+    return a.cache.data + page * a.cache.page_stride + w.h * head_stride +
+           ((key & ((1 << a.cache.page_shift) - 1)) / kKvGroup) * G::kBytes;
+  };
+  uint32_t n = 0;   // tiles before the item in this CTA
+
+  if (warp == kMmaWarp) {
+    // ---------------------------------------------------------- MMA issue
+    uint32_t items[2] = {0, 0}, ptiles[2] = {0, 0};
+    auto scores = [&](int q, uint32_t num) {
+      if (elect_one()) {
+        const uint32_t qa = smem_u32(sm.q[q]), ka = smem_u32(sm.k[num & 1]);
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j)
+          mma_ss_f16(tmem + kS + q * kKeys,
+                     smem_desc_kmajor_sw128(qa + (j >> 2) * (kRowTile * 128)) + (j & 3) * 2,
+                     smem_desc_kmajor_sw128(ka + (j >> 2) * (kKeys * 128)) + (j & 3) * 2, kIdescS, j > 0);
+        mma_commit(smem_u32(&sm.sfull[q]));
+      }
+      __syncwarp();
+    };
+    auto commit = [&](uint64_t* bar) {
+      if (elect_one()) mma_commit(smem_u32(bar));
+      __syncwarp();
+    };
+    for (; !w.done(); w.next(a, status)) {
+      const int tiles = w.tb - w.ta;
+      const int rows = min(w.s.tokens, w.s.nq - w.rt * w.s.tokens) * a.group;
+      const int nt = rows > kRowTile ? 2 : 1;
+      for (int q = 0; q < nt; ++q) {
+        wait(&sm.qfull[q], items[q] & 1);
+        if (q == 0) wait(&sm.kfull[n & 1], (n >> 1) & 1);
+        tc_fence_after();
+        scores(q, n);
+      }
+      commit(&sm.kfree[n & 1]);
+      for (int i = 0; i < tiles; ++i) {
+        const uint32_t num = n + i;
+        for (int q = 0; q < nt; ++q) {
+          wait(&sm.pfull[q], ptiles[q]++ & 1);
+          if (q == 0) wait(&sm.vfull[num & 1], (num >> 1) & 1);
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t va = smem_u32(sm.v[num & 1]);
+#pragma unroll
+            for (int j = 0; j < kKeys / 16; ++j)
+              mma_ts_f16(tmem + kO + q * D, tmem + kS + q * kKeys + j * 8,
+                         smem_desc_kmajor_sw128(va + (j >> 2) * (D * 128)) + (j & 3) * 2, kIdescO, i > 0 || j > 0);
+          }
+          __syncwarp();
+          if (i + 1 < tiles) {
+            if (q == 0) {
+              wait(&sm.kfull[(num + 1) & 1], ((num + 1) >> 1) & 1);
+              tc_fence_after();
+            }
+            scores(q, num + 1);
+          } else {
+            commit(&sm.ofull[q]);
+          }
+        }
+        commit(&sm.vfree[num & 1]);
+        if (i + 1 < tiles) commit(&sm.kfree[(num + 1) & 1]);
+      }
+      for (int q = 0; q < nt; ++q) ++items[q];
+      n += tiles;
+    }
+    commit(&sm.fin);
+    mbar_wait_bounded(smem_u32(&sm.fin), 0, a.timeout_ns, nullptr);
+  } else if (warp >= kVWarp) {
+    // ------------------------------------------------------------------ V
+    constexpr int kD = D / 8;          // dimensions of a thread
+    constexpr int kW = kD / 8;         // code words of a token
+    const int vw = warp - kVWarp;
+    const int slab = vw & 1, kg = lane & 7;
+    const int d0 = (vw >> 1) * (D / 2) + (lane >> 3) * kD;
+    const int key_in = slab * 64 + kg * 8;
+    uint32_t wd[8][kW];
+    uint32_t sc[8];
+    auto load = [&](int tile) {
+      const int key = w.k.lo + tile * kKeys + key_in;
+      const uint8_t* grp = group_of(key);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int t = (kg & 1) * 8 + i;
+#pragma unroll
+        for (int j = 0; j < kW; ++j) wd[i][j] = 0;
+        sc[i] = 0;
+        // a token past the end may hold anything, NaN scales among it: zeros
+        if (grp && key + i < w.s.len) {
+          const uint8_t* p = grp + G::kVCodes + t * G::kRow + d0 / 2;
+          if constexpr (kW == 2) {
+            const uint2 v = *reinterpret_cast<const uint2*>(p);
+            wd[i][0] = v.x;
+            wd[i][1] = v.y;
+          } else {
+            wd[i][0] = *reinterpret_cast<const uint32_t*>(p);
+          }
+          sc[i] = grp[G::kVScales + t * G::kScales + d0 / G::kBlock];
+        }
+      }
+    };
+    if (!w.done()) load(w.ta);
+    while (!w.done()) {
+      const int tiles = w.tb - w.ta;
+      int vref = 0;
+      for (int i = 0; i < tiles; ++i) {
+        const uint32_t num = n + i;
+        if (num >= 2) wait(&sm.vfree[num & 1], ((num >> 1) - 1) & 1);
+        uint32_t s2[4];
+        if constexpr (FMT == kNVFP4) {
+#pragma unroll
+          for (int p = 0; p < 4; ++p) s2[p] = e4m3x2_to_f16x2(sc[2 * p] | sc[2 * p + 1] << 8);
+        } else {
+          // the scales are taken relative to the largest so far in the item
+          uint32_t top = 0;
+#pragma unroll
+          for (int p = 0; p < 8; ++p) top = max(top, sc[p]);
+          top = __reduce_max_sync(0xFFFFFFFFu, top);
+          if (warp == kVWarp && lane == 0) sm.vtop = 0;
+          asm volatile("bar.sync 2, 128;" ::: "memory");
+          if (lane == 0) atomicMax(&sm.vtop, static_cast<int>(top));
+          asm volatile("bar.sync 2, 128;" ::: "memory");
+          const int t = max(vref, sm.vtop);
+          asm volatile("bar.sync 2, 128;" ::: "memory");
+          if (warp == kVWarp && lane == 0) {
+            sm.vfac[num % kRing] = t == vref ? 1.0f : ex2(static_cast<float>(vref - t));
+            sm.vscale[num % kRing] = ldexpf(1.0f, t - 127 - 12);
+          }
+          vref = t;
+#pragma unroll
+          for (int p = 0; p < 4; ++p)
+            s2[p] = f16_power(static_cast<int>(sc[2 * p]) - vref + 12) |
+                    f16_power(static_cast<int>(sc[2 * p + 1]) - vref + 12) << 16;
+        }
+        uint8_t* dst = sm.v[num & 1][slab];
+        auto put = [&](int d, uint32_t x0, uint32_t x1, uint32_t x2, uint32_t x3) {
+          *reinterpret_cast<uint4*>(dst + d * 128 + ((kg ^ (d & 7)) << 4)) = make_uint4(x0, x1, x2, x3);
+        };
+#pragma unroll
+        for (int j = 0; j < kW; ++j) {
+          uint32_t lo[4], hi[4];   // dimension pairs of two tokens side by side
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            const uint32_t x = wd[2 * p][j], y = wd[2 * p + 1][j];
+            lo[p] = (x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u);
+            hi[p] = ((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u);
+          }
+          const int d = d0 + 8 * j;
+          put(d + 0, mul2(e2m1x2_to_f16x2<0>(lo[0]), s2[0]), mul2(e2m1x2_to_f16x2<0>(lo[1]), s2[1]),
+              mul2(e2m1x2_to_f16x2<0>(lo[2]), s2[2]), mul2(e2m1x2_to_f16x2<0>(lo[3]), s2[3]));
+          put(d + 1, mul2(e2m1x2_to_f16x2<0>(hi[0]), s2[0]), mul2(e2m1x2_to_f16x2<0>(hi[1]), s2[1]),
+              mul2(e2m1x2_to_f16x2<0>(hi[2]), s2[2]), mul2(e2m1x2_to_f16x2<0>(hi[3]), s2[3]));
+          put(d + 2, mul2(e2m1x2_to_f16x2<1>(lo[0]), s2[0]), mul2(e2m1x2_to_f16x2<1>(lo[1]), s2[1]),
+              mul2(e2m1x2_to_f16x2<1>(lo[2]), s2[2]), mul2(e2m1x2_to_f16x2<1>(lo[3]), s2[3]));
+          put(d + 3, mul2(e2m1x2_to_f16x2<1>(hi[0]), s2[0]), mul2(e2m1x2_to_f16x2<1>(hi[1]), s2[1]),
+              mul2(e2m1x2_to_f16x2<1>(hi[2]), s2[2]), mul2(e2m1x2_to_f16x2<1>(hi[3]), s2[3]));
+          put(d + 4, mul2(e2m1x2_to_f16x2<2>(lo[0]), s2[0]), mul2(e2m1x2_to_f16x2<2>(lo[1]), s2[1]),
+              mul2(e2m1x2_to_f16x2<2>(lo[2]), s2[2]), mul2(e2m1x2_to_f16x2<2>(lo[3]), s2[3]));
+          put(d + 5, mul2(e2m1x2_to_f16x2<2>(hi[0]), s2[0]), mul2(e2m1x2_to_f16x2<2>(hi[1]), s2[1]),
+              mul2(e2m1x2_to_f16x2<2>(hi[2]), s2[2]), mul2(e2m1x2_to_f16x2<2>(hi[3]), s2[3]));
+          put(d + 6, mul2(e2m1x2_to_f16x2<3>(lo[0]), s2[0]), mul2(e2m1x2_to_f16x2<3>(lo[1]), s2[1]),
+              mul2(e2m1x2_to_f16x2<3>(lo[2]), s2[2]), mul2(e2m1x2_to_f16x2<3>(lo[3]), s2[3]));
+          put(d + 7, mul2(e2m1x2_to_f16x2<3>(hi[0]), s2[0]), mul2(e2m1x2_to_f16x2<3>(hi[1]), s2[1]),
+              mul2(e2m1x2_to_f16x2<3>(hi[2]), s2[2]), mul2(e2m1x2_to_f16x2<3>(hi[3]), s2[3]));
+        }
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.vfull[num & 1]));
+        if (i + 1 < tiles) load(w.ta + i + 1);
+      }
+      n += tiles;
+      w.next(a, status);
+      if (!w.done()) load(w.ta);
+    }
+  } else if (warp >= kKWarp) {
+    // ------------------------------------------------------------------ K
+    constexpr int kW = D / 8;          // code words of a token
+    const int kw = warp - kKWarp;
+    const int key_in = kw * 32 + lane;
+    uint32_t wd[kW];
+    uint32_t sc[(G::kScales + 3) / 4];
+    bool have = false;
+    auto load = [&](int tile) {
+      const int key = w.k.lo + tile * kKeys + key_in;
+      const uint8_t* grp = group_of(key);
+      have = grp != nullptr;
+#pragma unroll
+      for (int j = 0; j < kW; ++j) wd[j] = 0;
+#pragma unroll
+      for (int j = 0; j < (G::kScales + 3) / 4; ++j) sc[j] = 0;
+      if (have) {
+        const int t = key % kKvGroup;
+        const uint4* p = reinterpret_cast<const uint4*>(grp + G::kKCodes + t * G::kRow);
+#pragma unroll
+        for (int j = 0; j < kW / 4; ++j) {
+          const uint4 v = p[j];
+          wd[4 * j] = v.x, wd[4 * j + 1] = v.y, wd[4 * j + 2] = v.z, wd[4 * j + 3] = v.w;
+        }
+        const uint8_t* ps = grp + G::kKScales + t * G::kScales;
+        if constexpr (G::kScales == 8) {
+          const uint2 v = *reinterpret_cast<const uint2*>(ps);
+          sc[0] = v.x, sc[1] = v.y;
+        } else if constexpr (G::kScales == 4) {
+          sc[0] = *reinterpret_cast<const uint32_t*>(ps);
+        } else {
+          sc[0] = *reinterpret_cast<const uint16_t*>(ps);
+        }
+      }
+    };
+    if (!w.done()) load(w.ta);
+    while (!w.done()) {
+      const int tiles = w.tb - w.ta;
+      for (int i = 0; i < tiles; ++i) {
+        const uint32_t num = n + i;
+        if (num >= 2) wait(&sm.kfree[num & 1], ((num >> 1) - 1) & 1);
+        const unsigned held = __ballot_sync(0xFFFFFFFFu, have);
+        int top = 0;
+        if constexpr (FMT == kMXFP4) {
+#pragma unroll
+          for (int p = 0; p < G::kScales; ++p) top = max(top, static_cast<int>((sc[0] >> (8 * p)) & 0xFFu));
+          top = static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(top)));
+        }
+        if (lane == 0) {
+          sm.valid[num % kRing][kw] = (held & 0xFFFFu ? 1u : 0u) | (held >> 16 ? 2u : 0u);
+          if constexpr (FMT == kMXFP4) sm.kfac[num % kRing][kw] = e8m0_to_f32(top) * 0.000244140625f;
+        }
+        uint8_t* dst = &sm.k[num & 1][0][key_in * 128];
+        uint32_t s2 = 0;
+#pragma unroll
+        for (int j = 0; j < kW; ++j) {
+          if (j % (G::kBlock / 8) == 0) {   // this word begins a block
+            const int blk = j / (G::kBlock / 8);
+            const uint32_t b = (sc[blk / 4] >> (8 * (blk % 4))) & 0xFFu;
+            if constexpr (FMT == kNVFP4)
+              s2 = e4m3x2_to_f16x2(b * 0x0101u);
+            else
+              s2 = f16_power(static_cast<int>(b) - top + 12) * 0x10001u;
+          }
+          *reinterpret_cast<uint4*>(dst + (j >> 3) * (kKeys * 128) + (((j & 7) ^ (key_in & 7)) << 4)) =
+              make_uint4(mul2(e2m1x2_to_f16x2<0>(wd[j]), s2), mul2(e2m1x2_to_f16x2<1>(wd[j]), s2),
+                         mul2(e2m1x2_to_f16x2<2>(wd[j]), s2), mul2(e2m1x2_to_f16x2<3>(wd[j]), s2));
+        }
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.kfull[num & 1]));
+        if (i + 1 < tiles) load(w.ta + i + 1);
+      }
+      n += tiles;
+      w.next(a, status);
+      if (!w.done()) load(w.ta);
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int q = warp >> 2;
+    const int row_in = (warp & 3) * 32 + lane;            // row of the MMA tile = tensor-memory lane
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_tmem = tmem + lanes + kS + q * kKeys, o_tmem = tmem + lanes + kO + q * D;
+    uint32_t my_items = 0, my_tiles = 0;
+    for (; !w.done(); w.next(a, status)) {
+      const int tiles = w.tb - w.ta;
+      const int tok0 = w.rt * w.s.tokens;
+      const int rows = min(w.s.tokens, w.s.nq - tok0) * a.group;
+      const bool whole = tiles == w.k.tiles;
+      const int row = q * kRowTile + row_in;
+      const bool mine = row < rows;
+      const int tok = tok0 + min(row, rows - 1) / a.group;   // (a row past the last masks like it)
+      const int64_t head = static_cast<int64_t>(w.h) * a.group + (mine ? row % a.group : 0);
+      const float gv = a.cache.scales ? a.cache.scales[a.cache.heads + w.h] : 1.0f;
+      float m = -INFINITY, l = 0.0f;
+      float vs = 1.0f;
+      if (q * kRowTile < rows) {
+        // ---- the row to FP16, swizzled; the sign of the scale goes with it
+        float f;
+        {
+          const float gk = a.cache.scales ? a.cache.scales[w.h] : 1.0f;
+          uint4 x[D / 8];
+#pragma unroll
+          for (int j = 0; j < D / 8; ++j) x[j] = make_uint4(0, 0, 0, 0);
+          if (mine) {
+            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q.data) +
+                                                              (w.s.q0 + static_cast<int64_t>(tok)) * a.q.token_stride +
+                                                              head * a.q.head_stride);
+#pragma unroll
+            for (int j = 0; j < D / 8; ++j) x[j] = src[j];
+          }
+          float amax = 0.0f;
+#pragma unroll
+          for (int j = 0; j < D / 8; ++j) {
+            const uint32_t wd[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 v = unpack2(wd[e], a.bf16);
+              amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
+            }
+          }
+          const int shift = row_shift(amax);
+          const float factor = a.scale_log2 * gk;
+          const float up = copysignf(ldexpf(1.0f, shift), factor);
+          f = ldexpf(fabsf(factor), -shift);
+#pragma unroll
+          for (int j = 0; j < D / 8; ++j) {
+            const uint32_t wd[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 v = unpack2(wd[e], a.bf16);
+              o[e] = pack_f16(v.x * up, v.y * up);
+            }
+            *reinterpret_cast<uint4*>(&sm.q[q][j >> 3][row_in * 128 + (((j & 7) ^ (row_in & 7)) << 4)]) =
+                make_uint4(o[0], o[1], o[2], o[3]);
+          }
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sm.qfull[q]));
+        }
+        // keys this row sees, and those every row of the tile sees
+        const int hi = a.causal ? w.s.len - w.s.nq + tok : w.s.len - 1;
+        const int64_t first = a.window > 0 ? static_cast<int64_t>(hi) - a.window + 1 : 0;
+        const int lo = first > 0 ? static_cast<int>(first) : 0;
+        const int tok_a = tok0 + q * kRowTile / a.group, tok_b = tok0 + (min(rows, (q + 1) * kRowTile) - 1) / a.group;
+        const int all_hi = a.causal ? w.s.len - w.s.nq + tok_a : w.s.len - 1;
+        const int64_t all_lo = a.window > 0 ? static_cast<int64_t>(w.s.len) - w.s.nq + tok_b - a.window + 1 : 0;
+
+        for (int i = 0; i < tiles; ++i) {
+          const uint32_t num = n + i;
+          const int key0 = w.k.lo + (w.ta + i) * kKeys;
+          wait(&sm.sfull[q], my_tiles++ & 1);
+          if constexpr (FMT == kMXFP4) wait(&sm.vfull[num & 1], (num >> 1) & 1);   // vfac, vscale
+          tc_fence_after();
+          uint32_t valid = 0;
+          float fc[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            valid |= sm.valid[num % kRing][c] << (2 * c);
+            fc[c] = FMT == kMXFP4 ? f * sm.kfac[num % kRing][c] : f;
+            // not zero, so that a masked score stays -inf (2^-126 of a score is nothing)
+            fc[c] = fc[c] < FLT_MIN ? FLT_MIN : fc[c];
+          }
+          if constexpr (FMT == kMXFP4) vs = sm.vscale[num % kRing];
+          const bool masked = valid != 0xFFu || key0 + kKeys - 1 > all_hi || key0 < all_lo;
+          auto load_scores = [&](int c, float(&x)[32]) {
+            uint32_t r[32];
+            tmem_ld_x32(s_tmem + 32 * c, r);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(r[e]);
+            if (masked) {
+              const int from = lo - key0 - 32 * c, to = hi - key0 - 32 * c;
+              const bool g0 = (valid >> (2 * c)) & 1, g1 = (valid >> (2 * c + 1)) & 1;
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (e < from || e > to || !(e < 16 ? g0 : g1)) x[e] = -INFINITY;
+            }
+          };
+          // ---- the reference maximum moves only when passed by 2^8
+          float top = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float x[32], t = -INFINITY;
+            load_scores(c, x);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) t = fmaxf(t, x[e]);
+            top = fmaxf(top, t * fc[c]);
+          }
+          const bool grow = top > m + 8.0f;
+          const float vf = FMT == kMXFP4 && i > 0 ? sm.vfac[num % kRing] : 1.0f;
+          if (__any_sync(0xFFFFFFFFu, grow || vf != 1.0f)) {
+            float r = 1.0f;
+            if (grow) {
+              r = ex2(m - top);
+              m = top;
+              l *= r;
+            }
+            if (i > 0) {
+              r *= vf;
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld_x32(o_tmem + 32 * c, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * r);
+                tmem_st_x16(o_tmem + 32 * c, *reinterpret_cast<uint32_t(*)[16]>(&o[0]));
+                tmem_st_x16(o_tmem + 32 * c + 16, *reinterpret_cast<uint32_t(*)[16]>(&o[16]));
+              }
+            }
+          }
+          const float ref = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float x[32];
+            load_scores(c, x);
+            uint32_t p[16];
+            float l0 = 0.0f, l1 = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float p0 = ex2(fmaf(x[2 * e], fc[c], -ref)), p1 = ex2(fmaf(x[2 * e + 1], fc[c], -ref));
+              l0 += p0;
+              l1 += p1;
+              p[e] = pack_f16(p0, p1);
+            }
+            l += l0 + l1;
+            tmem_st_x16(s_tmem + 16 * c, p);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sm.pfull[q]));
+        }
+        wait(&sm.ofull[q], my_items++ & 1);
+        tc_fence_after();
+      }
+      n += tiles;
+      // ---- O of the row: the output, or a partial
+      const int64_t out_row = w.s.q0 + static_cast<int64_t>(tok);
+      auto store_out = [&](int c, const float(&x)[32], float inv) {   // 32 dimensions from 32 c on
+        uint16_t* dst = static_cast<uint16_t*>(a.out.data) + out_row * a.out.token_stride + head * a.out.head_stride +
+                        32 * c;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          reinterpret_cast<uint4*>(dst)[e] =
+              make_uint4(pack2(x[8 * e] * inv, x[8 * e + 1] * inv, a.bf16), pack2(x[8 * e + 2] * inv, x[8 * e + 3] * inv, a.bf16),
+                         pack2(x[8 * e + 4] * inv, x[8 * e + 5] * inv, a.bf16),
+                         pack2(x[8 * e + 6] * inv, x[8 * e + 7] * inv, a.bf16));
+      };
+      auto store_lse = [&](float M, float L) {
+        if (a.lse)
+          a.lse[out_row * (static_cast<int64_t>(a.cache.heads) * a.group) + head] =
+              L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+      };
+      float* slot = partials + (2 * static_cast<size_t>(blockIdx.x) + (w.ta == 0 ? 1 : 0)) * partial_floats<D>();
+      if (q * kRowTile < rows) {
+        const float inv = l == 0.0f ? 0.0f : vs * gv / l;   // no key: zeros
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t r[32];
+          float x[32];
+          tmem_ld_x32(o_tmem + 32 * c, r);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(r[e]);
+          if (whole) {
+            if (mine) store_out(c, x, inv);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              reinterpret_cast<float4*>(slot)[(8 * c + e) * kRows + row] =
+                  make_float4(x[4 * e] * vs, x[4 * e + 1] * vs, x[4 * e + 2] * vs, x[4 * e + 3] * vs);
+          }
+        }
+        if (whole) {
+          if (mine) store_lse(m, l);
+        } else {
+          slot[kRows * D + row] = m;
+          slot[kRows * D + kRows + row] = l;
+        }
+        tc_fence_before();
+      }
+      if (!whole) {
+        const int64_t item0 = w.pos - w.ta;
+        const int c0 = cta_of_tile(w.total, w.ctas, item0), c1 = cta_of_tile(w.total, w.ctas, item0 + w.k.tiles - 1);
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (tid == 0) sm.last = atomic_add_acq_rel_gpu(&counters[c0], 1u) == static_cast<uint32_t>(c1 - c0);
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (sm.last) {
+          if (tid == 0) counters[c0] = 0;   // every CTA of the item has arrived
+          if (mine) {
+            auto part = [&](int c) { return partials + (2 * static_cast<size_t>(c) + (c == c0)) * partial_floats<D>(); };
+            float M = -INFINITY, L = 0.0f;
+            for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(part(c) + kRows * D + row));
+            auto weight = [&](int c, float lc) {
+              const float mc = __ldcg(part(c) + kRows * D + row);
+              return mc == -INFINITY ? (lc == 0.0f ? 0.0f : 1.0f) : ex2(mc - M);
+            };
+            for (int c = c0; c <= c1; ++c) {
+              const float lc = __ldcg(part(c) + kRows * D + kRows + row);
+              L += weight(c, lc) * lc;
+            }
+            const float inv2 = L == 0.0f ? 0.0f : gv / L;
+            for (int d = 0; d < D / 32; ++d) {
+              float x[32] = {};
+              for (int c = c0; c <= c1; ++c) {
+                const float wt = weight(c, __ldcg(part(c) + kRows * D + kRows + row));
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const float4 v = __ldcg(reinterpret_cast<const float4*>(part(c)) + (8 * d + e) * kRows + row);
+                  x[4 * e] += wt * v.x, x[4 * e + 1] += wt * v.y, x[4 * e + 2] += wt * v.z, x[4 * e + 3] += wt * v.w;
+                }
+              }
+              store_out(d, x, inv2);
+            }
+            store_lse(M, L);
+          }
+        }
+        asm volatile("bar.sync 1, 256;" ::: "memory");   // sm.last may be written again
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp) {
+    tmem_dealloc(tmem, kColumns);
+    if (lane == 0 && sm.abort) atomicOr(status, kStatusTimeout);
+  }
+}
+
+template <int D, int FMT>
+cudaError_t launch_as(const KvAttnArgs& a, int num_sms, cudaStream_t stream) {
+  // more than half of an SM's shared memory, whatever D is: one CTA an SM, and
+  // none of a GEMM's CTAs beside it (both allocate all of tensor memory)
+  constexpr size_t kSmem = sizeof(Smem<D>) > 120 * 1024 ? sizeof(Smem<D>) : 120 * 1024;
+  cudaError_t e = cudaFuncSetAttribute(kv_prompt_kernel<D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(kSmem));
+  if (e != cudaSuccess) return e;
+  kv_prompt_kernel<D, FMT><<<num_sms < kKvPromptCtas ? num_sms : kKvPromptCtas, kThreads, kSmem, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t kv_prompt_partials(int head_dim, int num_sms) {
+  const size_t ctas = num_sms < kKvPromptCtas ? num_sms : kKvPromptCtas;
+  return sizeof(float) * 2 * ctas * (head_dim == 128 ? partial_floats<128>() : partial_floats<64>());
+}
+
+cudaError_t launch_kv_prompt(const KvAttnArgs& a, int num_sms, cudaStream_t stream) {
+  return kv_dispatch(a.cache.head_dim, a.cache.fmt, true,
+                     [&](auto d, auto f, auto) { return launch_as<d, f>(a, num_sms, stream); });
+}
+
+}  // namespace petit

@@ -372,8 +372,9 @@ petit_status_t petit_kv_read(const petit_kv_cache_t* cache, const int64_t* slots
  *     x_j = scale * q . k_j,  out = sum_j softmax(x)_j v_j,
  *     lse = log(sum_j exp(x_j))        (natural logarithm, FP32)
  * A query that sees no key (len = 0, or p < 0) gets out = 0 and lse = -inf.
- * Products are FP16 by FP16 in FP32 (MXFP4 values of long prompts: BF16);
- * scores, the softmax's maximum and sum, and the output's sums are FP32.
+ * Products are FP16 by FP16 with FP32 sums (q by a power of two per row, the
+ * softmax's weights rounded to 11 bits); scores, the softmax's maximum and
+ * sum, and the output's sums are FP32.
  *
  * A length past max_pages * page_size, a page outside the cache and query
  * offsets outside 0..total_q are recorded as PETIT_ERR_BOUNDS in the

@@ -63,7 +63,7 @@ class Case:
         """Every row against the oracle, element by element.
 
         Error bound: with A the softmax average of |v|, each p_j is rounded to
-        11 bits (BF16's 8 for MXFP4 prompts) and carries its score's error d,
+        11 bits and carries its score's error d,
         e^d - 1 <= 2 d; FP32 sums over the keys add len * 2^-23; p below FP16's
         normal range have an absolute error of 2^-25 of the largest; the output
         is rounded once.  A score is an FP32 sum of dim products whose absolute
@@ -71,7 +71,6 @@ class Case:
         """
         scale = self.dim ** -0.5 if scale is None else scale
         u = NP[q.dtype]
-        group = q.shape[1] // self.heads
         at = 0
         qf, of = q.float().cpu().numpy().astype(np.float64), out.float().cpu().numpy().astype(np.float64)
         for b, (nq, n) in enumerate(zip(nqs, self.lens)):
@@ -79,7 +78,7 @@ class Case:
             got = of[at:at + nq]
             assert np.isfinite(got).all(), f"sequence {b}"
             d = ((self.dim + 16) * 2.0 ** -23 * score + 2.0 ** -22)[..., None]
-            pu = 2.0 ** -8 if self.fmt == "mxfp4" and max(nqs) * group > 16 else 2.0 ** -11
+            pu = 2.0 ** -11
             vmax = np.abs(self.v[b]).max(initial=0.0)
             bound = spread * (pu + 2 * d + (n + 64) * 2.0 ** -23) + u * np.abs(want) + n * 2.0 ** -25 * vmax + 1e-7
             bad = np.abs(got - want) > bound
