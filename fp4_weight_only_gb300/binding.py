@@ -422,11 +422,6 @@ def selftest_timeout(workspace, timeout_us=1000):
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1}
 
 
-@functools.lru_cache(maxsize=64)
-def _kv_workspace_bytes(device, heads, dim, fmt):
-    return int(load().petit_kv_attention_workspace_bytes(heads, dim, FORMATS[fmt]))
-
-
 class KVCache:
     """A paged cache of attention keys and values in 4 bits (petit.h gives its
     memory order): `num_pages` pages of `page_size` tokens of `num_kv_heads`
@@ -456,6 +451,7 @@ class KVCache:
             if scales.device != data.device:
                 raise ValueError("scales: need the cache's device")
         self.data, self.scales, self.fmt = data, scales, fmt
+        self.device, self.device_index = data.device, data.get_device()
         self.num_pages, self.page_size = num_pages, page_size
         self.num_kv_heads, self.head_dim = num_kv_heads, head_dim
         self.page_bytes = page
@@ -463,6 +459,14 @@ class KVCache:
                                 data.stride(0) if num_pages > 1 else page, page_size, num_kv_heads, head_dim,
                                 FORMATS[fmt])
         self._ref = ctypes.addressof(self.info)
+        self._workspace_bytes = 0
+
+    def workspace_bytes(self):
+        """Bytes of workspace :meth:`attention` needs on the current device."""
+        if not self._workspace_bytes:
+            self._workspace_bytes = int(load().petit_kv_attention_workspace_bytes(
+                self.num_kv_heads, self.head_dim, FORMATS[self.fmt]))
+        return self._workspace_bytes
 
     def append(self, k, v, slots, workspace=None):
         return kv_append(self, k, v, slots, workspace)
@@ -476,19 +480,25 @@ class KVCache:
 
 def _rows(t, cache, heads, dtype, name, tokens=None):
     """petit_rows_t of a [tokens, heads, D] tensor whose last dimension is contiguous."""
-    if (t.dim() != 3 or t.dtype != dtype or t.device != cache.data.device or t.shape[1] != heads
-            or t.shape[2] != cache.head_dim or t.stride(2) != 1):
-        raise ValueError(f"{name}: need a {dtype} tensor [tokens, {heads}, {cache.head_dim}] on the cache's device, "
-                         "contiguous in its last dimension")
-    if tokens is not None and t.shape[0] != tokens:
-        raise ValueError(f"{name}: need {tokens} tokens")
-    return Rows(t.data_ptr(), t.stride(0), t.stride(1))
+    if t.dim() == 3 and t.dtype is dtype and t.get_device() == cache.device_index:
+        n, h, d = t.shape
+        st, sh, sd = t.stride()
+        if h == heads and d == cache.head_dim and sd == 1 and (tokens is None or n == tokens):
+            return Rows(t.data_ptr(), st, sh)
+    raise ValueError(f"{name}: need a {dtype} tensor [{'tokens' if tokens is None else tokens}, {heads}, "
+                     f"{cache.head_dim}] on the cache's device, contiguous in its last dimension")
+
+
+def _new_rows(cache, tokens, heads, dtype):
+    """A new tensor [tokens, heads, D] and its petit_rows_t."""
+    t = torch.empty((tokens, heads, cache.head_dim), dtype=dtype, device=cache.device)
+    return t, Rows(t.data_ptr(), heads * cache.head_dim, cache.head_dim)
 
 
 def _indices(t, cache, dtype, shape, name):
-    if t.dtype != dtype or t.device != cache.data.device or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name}: need a contiguous {dtype} tensor {list(shape)} on the cache's device")
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.get_device() == cache.device_index and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name}: need a contiguous {dtype} tensor {list(shape)} on the cache's device")
 
 
 def _status_buf(workspace):
@@ -520,11 +530,12 @@ def kv_read(cache, slots, dtype=torch.bfloat16, workspace=None, out=None):
         raise ValueError("dtype: need torch.bfloat16 or torch.float16")
     n = slots.numel()
     if out is None:
-        shape = (n, cache.num_kv_heads, cache.head_dim)
-        out = (torch.empty(shape, dtype=dtype, device=cache.data.device),
-               torch.empty(shape, dtype=dtype, device=cache.data.device))
-    rk = _rows(out[0], cache, cache.num_kv_heads, dtype, "out[0]", n)
-    rv = _rows(out[1], cache, cache.num_kv_heads, dtype, "out[1]", n)
+        k, rk = _new_rows(cache, n, cache.num_kv_heads, dtype)
+        v, rv = _new_rows(cache, n, cache.num_kv_heads, dtype)
+        out = k, v
+    else:
+        rk = _rows(out[0], cache, cache.num_kv_heads, dtype, "out[0]", n)
+        rv = _rows(out[1], cache, cache.num_kv_heads, dtype, "out[1]", n)
     buf, nbytes = _status_buf(workspace)
     _check(load().petit_kv_read(cache._ref, _indices(slots, cache, torch.int64, (n,), "slots"), n, ctypes.byref(rk),
                                 ctypes.byref(rv), _DTYPES[dtype], buf, nbytes, _stream()), "kv_read")
@@ -553,24 +564,25 @@ def kv_attention(cache, q, block_table, seq_lens, q_offsets=None, max_q=1, scale
     if block_table.dim() != 2 or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
         raise ValueError("block_table: need [batch, max_pages] with contiguous rows")
     batch, max_pages = block_table.shape
-    if block_table.dtype != torch.int32 or block_table.device != cache.data.device:
+    if block_table.dtype is not torch.int32 or block_table.get_device() != cache.device_index:
         raise ValueError("block_table: need int32 on the cache's device")
+    rq = _rows(q, cache, heads, q.dtype, "q")
     if out is None:
-        out = torch.empty((total_q, heads, cache.head_dim), dtype=q.dtype, device=q.device)
+        out, ro = _new_rows(cache, total_q, heads, q.dtype)
+    else:
+        ro = _rows(out, cache, heads, q.dtype, "out", total_q)
     args = KvAttentionArgs(
-        _rows(q, cache, heads, q.dtype, "q"), _rows(out, cache, heads, q.dtype, "out", total_q),
-        None if lse is None else _ptr(lse), _ptr(block_table),
+        rq, ro, None if lse is None else _ptr(lse), _ptr(block_table),
         _indices(seq_lens, cache, torch.int32, (batch,), "seq_lens"),
         None if q_offsets is None else _indices(q_offsets, cache, torch.int32, (batch + 1,), "q_offsets"),
         batch, total_q, int(max_q), max_pages, max(block_table.stride(0), max_pages) if batch > 1 else max_pages,
         heads, _DTYPES[q.dtype], cache.head_dim ** -0.5 if scale is None else float(scale), int(bool(causal)),
         int(window))
     if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (total_q, heads)
-                            or not lse.is_contiguous() or lse.device != cache.data.device):
+                            or not lse.is_contiguous() or lse.get_device() != cache.device_index):
         raise ValueError(f"lse: need a contiguous FP32 tensor [{total_q}, {heads}] on the cache's device")
-    ws = workspace or Workspace(q.device)
-    need = _kv_workspace_bytes(torch.cuda.current_device(), cache.num_kv_heads, cache.head_dim, cache.fmt)
-    buf = ws.ensure(need)
+    ws = workspace or Workspace(cache.device)
+    buf = ws.ensure(cache.workspace_bytes())
     _check(load().petit_kv_attention(cache._ref, ctypes.byref(args), _ptr(buf), buf.numel(), _stream()),
            "kv_attention")
     return out

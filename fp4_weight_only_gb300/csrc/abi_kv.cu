@@ -135,7 +135,7 @@ petit_status_t petit_kv_attention(const petit_kv_cache_t* cache, const petit_kv_
   if (!workspace) return PETIT_ERR_WORKSPACE;
   if (!aligned(workspace, 16)) return PETIT_ERR_MISALIGNED;
   int sms = 0;
-  if (int st = petit::usable_device(&sms)) return static_cast<petit_status_t>(st);
+  if (int st = petit::usable_device(&sms, &a.device)) return static_cast<petit_status_t>(st);
   if (workspace_bytes < petit::kv_attention_workspace(cache->head_dim, sms)) return PETIT_ERR_WORKSPACE;
   a.lse = args->lse;
   a.block_table = args->block_table;

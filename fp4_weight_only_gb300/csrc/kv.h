@@ -2,6 +2,7 @@
 // the kernels (kv_cache.cu, kv_attn.cu).
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -47,6 +48,7 @@ struct KvAttnArgs {
   int64_t window;             // 0: none
   uint8_t* workspace;
   uint64_t timeout_ns;
+  int device;
 };
 
 // Calls f with head_dim, format and type as integral constants.
@@ -71,6 +73,20 @@ cudaError_t launch_kv_read(const KvCacheArgs& c, const int64_t* slots, int64_t n
 // Workspace of the attention kernels on a device with num_sms SMs: the
 // header and counters of a GEMM's workspace, then partial results.
 size_t kv_attention_workspace(int head_dim, int num_sms);
+// Allows a kernel its dynamic shared memory, once per device.
+template <auto KERNEL>
+cudaError_t kv_allow_smem(int device, size_t bytes) {
+  static std::atomic<bool> done[64];
+  if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
+  if (!done[device].load(std::memory_order_acquire)) {
+    const cudaError_t e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(bytes));
+    if (e != cudaSuccess) return e;
+    done[device].store(true, std::memory_order_release);
+  }
+  return cudaSuccess;
+}
+
 // The kernel for many query rows (kv_prompt.cu), for groups of at most
 // kKvPromptGroup query heads, and its share of the workspace.
 constexpr int kKvPromptGroup = 128;

@@ -800,12 +800,11 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv_attn_kernel(cons
 template <int D, int FMT, int NB>
 cudaError_t launch_as(const KvAttnArgs& a, int num_sms, cudaStream_t stream) {
   auto* kernel = kv_attn_kernel<D, FMT, NB>;
-  constexpr size_t smem = sizeof(Smem<D, FMT, NB>);
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
+  constexpr size_t kSmem = sizeof(Smem<D, FMT, NB>);
+  if (cudaError_t e = kv_allow_smem<kv_attn_kernel<D, FMT, NB>>(a.device, kSmem)) return e;
   int grid = num_sms * (NB == 1 ? 2 : 1);
   if (grid > kMaxCtas_) grid = kMaxCtas_;
-  kernel<<<grid, kThreads, smem, stream>>>(a);
+  kernel<<<grid, kThreads, kSmem, stream>>>(a);
   return cudaGetLastError();
 }
 

@@ -786,9 +786,7 @@ cudaError_t launch_as(const KvAttnArgs& a, int num_sms, cudaStream_t stream) {
   // more than half of an SM's shared memory, whatever D is: one CTA an SM, and
   // none of a GEMM's CTAs beside it (both allocate all of tensor memory)
   constexpr size_t kSmem = sizeof(Smem<D>) > 120 * 1024 ? sizeof(Smem<D>) : 120 * 1024;
-  cudaError_t e = cudaFuncSetAttribute(kv_prompt_kernel<D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(kSmem));
-  if (e != cudaSuccess) return e;
+  if (cudaError_t e = kv_allow_smem<kv_prompt_kernel<D, FMT>>(a.device, kSmem)) return e;
   kv_prompt_kernel<D, FMT><<<num_sms < kKvPromptCtas ? num_sms : kKvPromptCtas, kThreads, kSmem, stream>>>(a);
   return cudaGetLastError();
 }
