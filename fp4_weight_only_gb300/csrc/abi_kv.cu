@@ -121,6 +121,7 @@ petit_status_t petit_kv_attention(const petit_kv_cache_t* cache, const petit_kv_
   if (args->num_q_heads % cache->num_kv_heads) return PETIT_ERR_INVALID_ARG;
   const int64_t group = args->num_q_heads / cache->num_kv_heads;
   if (args->batch > kMaxBatch || args->total_q > kMaxTokens || args->max_q > kMaxTokens || group > kMaxHeads ||
+      args->total_q * args->num_q_heads >= (int64_t(1) << 31) - 64 ||
       args->max_pages > (int64_t(1) << 30) / cache->page_size)
     return PETIT_ERR_UNSUPPORTED_SHAPE;
   if (!args->q_offsets && args->total_q != args->batch * args->max_q) return PETIT_ERR_INVALID_ARG;

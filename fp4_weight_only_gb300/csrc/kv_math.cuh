@@ -5,6 +5,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "ptx.cuh"
+
 namespace petit {
 
 __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
@@ -53,6 +55,25 @@ __device__ __forceinline__ uint32_t pack2(float x, float y, bool bf16) {
 __device__ __forceinline__ int row_shift(float amax) {
   const int e = static_cast<int>(__float_as_uint(amax) >> 23);
   return amax == 0.0f ? 0 : min(139 - e, 127);
+}
+
+// Waits for a phase of an mbarrier with the whole warp.  The loop is kept
+// short, because a kernel of many roles lives or dies by its instruction
+// cache: time and the abort flag are looked at every 1024 tries only.  A wait
+// that lasts `timeout_ns` raises the flag; with the flag up waits return
+// without their phase, so that every role still walks on to its end.
+__device__ __forceinline__ void wait_phase(uint64_t* bar, uint32_t parity, uint64_t timeout_ns, int* abort) {
+  const uint32_t b = smem_u32(bar);
+  uint64_t since = 0;
+  for (uint32_t tries = 1; !mbar_try_wait(b, parity & 1); ++tries) {
+    if ((tries & 1023u) == 0) {
+      const uint64_t now = global_timer_ns();
+      if (since == 0) since = now;
+      if (now - since > timeout_ns) *reinterpret_cast<volatile int*>(abort) = 1;
+      if (*reinterpret_cast<volatile int*>(abort)) break;
+    }
+  }
+  __syncwarp();
 }
 
 }  // namespace petit

@@ -59,8 +59,8 @@ class Case:
         off = torch.tensor([0] + list(np.cumsum(nqs)), dtype=torch.int32, device="cuda")
         return torch.from_numpy(q).to(dtype).cuda(), off
 
-    def check(self, q, nqs, out, lse=None, causal=True, window=0, scale=None):
-        """Every row against the oracle, element by element.
+    def check(self, q, nqs, out, lse=None, causal=True, window=0, scale=None, only=None):
+        """Every row (of the sequences `only`) against the oracle, element by element.
 
         Error bound: with A the softmax average of |v|, each p_j is rounded to
         11 bits and carries its score's error d,
@@ -74,6 +74,9 @@ class Case:
         at = 0
         qf, of = q.float().cpu().numpy().astype(np.float64), out.float().cpu().numpy().astype(np.float64)
         for b, (nq, n) in enumerate(zip(nqs, self.lens)):
+            if only is not None and b not in only:
+                at += nq
+                continue
             want, wl, spread, score = kv.attention(qf[at:at + nq], self.k[b], self.v[b], scale, causal, window)
             got = of[at:at + nq]
             assert np.isfinite(got).all(), f"sequence {b}"
