@@ -25,18 +25,19 @@
 // Both products are FP16: codes times NVFP4 scales are exact in FP16, q is
 // brought into FP16's range by a power of two per row (exact but for elements
 // 2^26 below the row's largest), and p is rounded to 11 bits, which adds less
-// than the rounding of a 16-bit output.  MXFP4 scales exceed FP16's range:
-// K's are taken relative to the token's largest and V's relative to the
-// largest seen in the dimension block, and the difference is applied in FP32
-// (exact for scales up to 2^32 below that largest).
+// than the rounding of a 16-bit output.  MXFP4 scales exceed FP16's range: they
+// are taken relative to the largest that the warp has met in the item, for K
+// and for V, and that is applied in FP32 (exact for scales up to 2^32 below it).
 //
 // Work split.  The keys of every (sequence, K/V head, block of 8 NB rows) are
-// cut into tiles of 32; the tiles of the whole call, numbered in that order,
-// are cut into equal ranges, one a CTA, so that ragged lengths balance without
-// the host knowing them.  A CTA's producer warp fetches tiles with bulk copies
-// into a ring; six consumer warps take them in turn, each with its own
-// running maximum, and meet when the CTA leaves an item.  Items cut between
-// CTAs leave FP32 partials, and the last CTA to arrive adds them in CTA order.
+// cut into tiles; the tiles of the whole call, numbered in that order, are cut
+// into equal ranges, one a CTA, so that ragged lengths balance without the host
+// knowing them.  A CTA's producer warp fetches tiles with bulk copies into a
+// ring; four consumer warps take them in turn, each with its own running
+// maximum, and meet when the CTA leaves an item.  Items cut between CTAs leave
+// FP32 partials, and the last CTA to arrive adds them in CTA order.
+#include <cfloat>
+#include <climits>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -49,26 +50,16 @@
 namespace petit {
 namespace {
 
-constexpr int kTile = 32;                    // keys of a tile
-#ifndef KVW
-#define KVW 4
-#define KVC 3
-#define KVS 3
-#endif
-constexpr int kWarps = KVW;                    // consumer warps
+constexpr int kWarps = 4;                    // consumer warps
 constexpr int kConsumers = kWarps * 32;
 constexpr int kThreads = kConsumers + 32;
 constexpr int kMostCtas = 480;               // partial slots are sized for this
-// What beginning and ending an item costs, in tiles: an item's first tile
-// weighs 1 + kItemCost in the split, so that short contexts, whose items are
-// mostly this, get no longer ranges than others.
-#ifndef KIC
-#define KIC 8
-#endif
-constexpr int kItemCost = KIC;
-// The least a CTA gets: more than an item's cost, so that every CTA with units
-// of an item has a tile of it, and about a tile a warp.
-constexpr int kMinUnits = kWarps + kItemCost;
+constexpr int kGroupCounters = kMostCtas;    // counters[kGroupCounters + ..]: arrivals of groups of partials
+constexpr int kJoinFlat = 48;                // partials joined in one step; more in groups
+
+// Keys of a tile: 4.5 KB of codes and scales in either head dimension.
+template <int D>
+constexpr int kTileOf = D == 64 ? 64 : 32;
 
 __device__ __forceinline__ int kv_key_of_row(int r) {   // r in 0..7; + 8 for the upper rows
   const int i = r >> 1;
@@ -104,7 +95,8 @@ struct Seq {
   int blocks;   // row blocks
 };
 
-__device__ __forceinline__ Seq load_seq(const KvAttnArgs& a, int b, int rows_per_block, uint32_t* status) {
+template <int TILE, int ROWS>
+__device__ __forceinline__ Seq load_seq(const KvAttnArgs& a, int b, uint32_t* status) {
   Seq s;
   const int64_t cap = a.max_pages << a.cache.page_shift;
   s.len = a.seq_lens[b];
@@ -124,66 +116,117 @@ __device__ __forceinline__ Seq load_seq(const KvAttnArgs& a, int b, int rows_per
   s.lo = 0;
   if (a.window > 0) {
     const int64_t first = static_cast<int64_t>(s.len) - s.nq - a.window + 1;
-    s.lo = first > 0 ? static_cast<int>(first) & ~(kTile - 1) : 0;
+    s.lo = first > 0 ? static_cast<int>(first) & ~(TILE - 1) : 0;
   }
-  s.tiles = s.len > s.lo ? (s.len - s.lo + kTile - 1) / kTile : 1;
-  s.blocks = (s.nq * a.group + rows_per_block - 1) / rows_per_block;
+  s.tiles = s.len > s.lo ? (s.len - s.lo + TILE - 1) / TILE : 1;
+  s.blocks = (s.nq * a.group + ROWS - 1) / ROWS;
   return s;
 }
 
-__device__ __forceinline__ int64_t seq_cost(const KvAttnArgs& a, const Seq& s) {
-  return static_cast<int64_t>(s.blocks) * a.cache.heads * (s.tiles + kItemCost);
-}
-
-// A CTA's range and where it begins, in units of tiles: tile 0 of an item
-// stands at the item's beginning, tile t > 0 kItemCost + t after it.
+// A CTA's range and where it begins.  Ranges are counted in units of tiles, and
+// an item weighs its tiles and `cost` more, for what beginning and ending one
+// takes: tile 0 stands at the item's beginning, tile t > 0 cost + t after it.
 struct Range {
-  int64_t total;   // of the whole call
+  int64_t total;   // units of the whole call
   int64_t begin, end;
+  int64_t rem;     // units of sequence b before `begin`
+  int cost;
   int ctas;        // CTAs with a range
   int b;           // sequence of `begin`
-  int64_t rem;     // units of it before `begin`
 };
 
-__device__ __forceinline__ int64_t range_begin(int64_t total, int ctas, int64_t c) { return total * c / ctas; }
+// The first unit of CTA c's range.
+__device__ __forceinline__ int64_t range_begin(int64_t total, int ctas, int c) {
+  if (total < (1 << 21)) return static_cast<uint32_t>(total) * c / ctas;   // (c < 2^10; 64-bit division is slow)
+  return total * c / ctas;
+}
 
 // The CTA whose range holds unit x.
 __device__ __forceinline__ int cta_of(int64_t total, int ctas, int64_t x) {
   return static_cast<int>(((x + 1) * ctas + total - 1) / total) - 1;
 }
 
-// Every thread of the CTA calls this; `sh` holds kThreads / 32 + 2 values.
-__device__ Range find_range(const KvAttnArgs& a, int rows_per_block, int64_t* sh, uint32_t* status) {
+// An item's cost.  With more items than CTAs to run them, ranges of equal tiles
+// would give a CTA of many short items a multiple of the others' time (16 tiles
+// was the best of 0 to 40 for 512 ragged items: 71 us, 94 at 0).  With few long
+// items it only makes ranges longer than need be; with few short ones it keeps
+// them whole.
+__device__ __forceinline__ int item_cost(int64_t tiles, int64_t items) {
+  return 2 * items > gridDim.x ? 16 : tiles >= 16 * items ? 0 : 4;
+}
+
+// Every thread of the CTA calls this (and it synchronises them); `sh` holds
+// 2 kThreads / 32 + 2 values.
+template <int TILE, int ROWS>
+__device__ Range find_range(const KvAttnArgs& a, int64_t* sh, uint32_t* status) {
   constexpr int kW = kThreads / 32;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  Range r{};
-  int64_t sum = 0;
-  for (int b = tid; b < a.batch; b += kThreads) sum += seq_cost(a, load_seq(a, b, rows_per_block, status));
+  auto measure = [&](int b, int64_t& tiles, int64_t& items) {
+    tiles = items = 0;
+    if (b >= a.batch) return;
+    const Seq s = load_seq<TILE, ROWS>(a, b, status);
+    items = static_cast<int64_t>(s.blocks) * a.cache.heads;
+    tiles = items * s.tiles;
+  };
+  int64_t tiles = 0, items = 0, my_tiles, my_items;
+  if (a.batch == 1) {
+    measure(0, tiles, items);
+    my_tiles = tid == 0 ? tiles : 0;
+    my_items = tid == 0 ? items : 0;
+    __syncthreads();
+  } else {
+    measure(tid, my_tiles, my_items);
+    int64_t t = my_tiles, n = my_items;
+    for (int b = tid + kThreads; b < a.batch; b += kThreads) {
+      int64_t x, y;
+      measure(b, x, y);
+      t += x;
+      n += y;
+    }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-  if (lane == 0) sh[warp] = sum;
-  __syncthreads();
-  for (int w = 0; w < kW; ++w) r.total += sh[w];
-  __syncthreads();
-  const int64_t most = r.total > kMinUnits ? r.total / kMinUnits : r.total > 0;
-  r.ctas = most < gridDim.x ? static_cast<int>(most) : static_cast<int>(gridDim.x);
-  if (static_cast<int>(blockIdx.x) >= r.ctas) {
-    r.begin = r.end = 0;
-    return r;
+    for (int o = 16; o > 0; o >>= 1) {
+      t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+      n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
+    }
+    if (lane == 0) {
+      sh[2 * warp] = t;
+      sh[2 * warp + 1] = n;
+    }
+    __syncthreads();
+    for (int w = 0; w < kW; ++w) {
+      tiles += sh[2 * w];
+      items += sh[2 * w + 1];
+    }
   }
+  Range r{};
+  r.cost = item_cost(tiles, items);
+  r.total = tiles + r.cost * items;
+  // at least a tile a warp, and more than an item's cost, so that every CTA
+  // with units of an item has a tile of it
+  const int least = kWarps + r.cost;
+  r.ctas = r.total >= static_cast<int64_t>(gridDim.x) * least ? static_cast<int>(gridDim.x)
+           : r.total >= least                                 ? static_cast<int>(r.total) / least
+                                                              : r.total > 0;
+  if (static_cast<int>(blockIdx.x) >= r.ctas) return r;
   r.begin = range_begin(r.total, r.ctas, blockIdx.x);
   r.end = range_begin(r.total, r.ctas, blockIdx.x + 1);
+  if (a.batch == 1) {
+    r.rem = r.begin;
+    return r;
+  }
   // find `begin`: prefix sums over sequences, a block of them at a time
   int64_t base = 0;
   for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
     const int b = b0 + tid;
-    const int64_t mine = b < a.batch ? seq_cost(a, load_seq(a, b, rows_per_block, status)) : 0;
+    if (b0 > 0) measure(b, my_tiles, my_items);
+    const int64_t mine = my_tiles + r.cost * my_items;
     int64_t pre = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t v = __shfl_up_sync(0xFFFFFFFFu, pre, o);
       if (lane >= o) pre += v;
     }
+    __syncthreads();   // (what sh held has been read)
     if (lane == 31) sh[warp] = pre;
     __syncthreads();
     int64_t before = base, all = 0;
@@ -193,23 +236,24 @@ __device__ Range find_range(const KvAttnArgs& a, int rows_per_block, int64_t* sh
     }
     before += pre - mine;
     if (mine > 0 && before <= r.begin && r.begin < before + mine) {
-      sh[kW] = b;
-      sh[kW + 1] = r.begin - before;
+      sh[2 * kW] = b;
+      sh[2 * kW + 1] = r.begin - before;
     }
     base += all;
-    __syncthreads();
     if (base > r.begin) break;
   }
-  r.b = static_cast<int>(sh[kW]);
-  r.rem = sh[kW + 1];
+  __syncthreads();
+  r.b = static_cast<int>(sh[2 * kW]);
+  r.rem = sh[2 * kW + 1];
   return r;
 }
 
 // Walks the items of a range; every role steps one of its own.  Positions are
 // relative to the range's beginning (a range of 2^31 tiles would take an hour).
-template <int N>
+template <int TILE, int ROWS>
 struct Walk {
   int span;        // the range's units
+  int cost;
   int at;          // the item's first unit
   int b;
   int item;        // of the sequence: heads, and row blocks inside them
@@ -220,14 +264,14 @@ struct Walk {
   int ta, tb;      // tiles of the item in this range
 
   __device__ __forceinline__ Walk(const KvAttnArgs& a, const Range& r, uint32_t* status)
-      : span(static_cast<int>(r.end - r.begin)), b(r.b) {
-    s = load_seq(a, b, N, status);
-    const int64_t i = r.rem / (s.tiles + kItemCost);
-    const int in = static_cast<int>(r.rem - i * (s.tiles + kItemCost));
+      : span(static_cast<int>(r.end - r.begin)), cost(r.cost), b(r.b) {
+    s = load_seq<TILE, ROWS>(a, b, status);
+    const int64_t i = r.rem < INT_MAX ? static_cast<int>(r.rem) / (s.tiles + cost) : r.rem / (s.tiles + cost);
+    const int in = static_cast<int>(r.rem - i * (s.tiles + cost));
     item = static_cast<int>(i);
     at = -in;
     // the first tile at or past the beginning
-    ta = in == 0 ? 0 : in <= kItemCost ? 1 : in - kItemCost;
+    ta = in == 0 ? 0 : in <= cost ? 1 : in - cost;
     if (ta < s.tiles)
       place(a);
     else   // the range begins between an item's only tile and the next item
@@ -235,19 +279,19 @@ struct Walk {
   }
   __device__ __forceinline__ bool done() const { return at >= span; }
   __device__ __forceinline__ void place(const KvAttnArgs& a) {
-    const int below = span - at - kItemCost;   // tiles below the range's end
+    const int below = span - at - cost;   // tiles below the range's end
     tb = below >= s.tiles ? s.tiles : below > ta ? below : ta + 1;
     h = item / s.blocks;
-    row0 = (item - h * s.blocks) * N;
-    rows = min(N, s.nq * a.group - row0);
+    row0 = (item - h * s.blocks) * ROWS;
+    rows = min(ROWS, s.nq * a.group - row0);
   }
   __device__ __forceinline__ void next_item(const KvAttnArgs& a, uint32_t* status) {
-    at += s.tiles + kItemCost;
+    at += s.tiles + cost;
     if (done()) return;
     if (++item == s.blocks * static_cast<int>(a.cache.heads)) {
       item = 0;
       do {
-        s = load_seq(a, ++b, N, status);
+        s = load_seq<TILE, ROWS>(a, ++b, status);
       } while (s.blocks == 0 && b + 1 < a.batch);
     }
     ta = 0;
@@ -318,9 +362,9 @@ __device__ __forceinline__ void store_part(float* p, const float (&v)[E]) {
 
 // Row `row` of (sequence, K/V head) to the output: lane's D / 32 dimensions.
 template <int D>
-__device__ __forceinline__ void store_row(const KvAttnArgs& a, const Seq& s, int row, int h, int lane, float M,
+__device__ __forceinline__ void store_row(const KvAttnArgs& a, int q0, int row, int h, int lane, float M,
                                           float L, const float (&acc)[D / 32], float gv) {
-  const int64_t tok = s.q0 + row / a.group;
+  const int64_t tok = q0 + row / a.group;
   const int64_t head = h * a.group + row % a.group;
   const float inv = L == 0.0f ? 0.0f : gv / L;   // no key: zeros
   uint32_t w[D / 64];
@@ -340,27 +384,31 @@ __device__ __forceinline__ void store_row(const KvAttnArgs& a, const Seq& s, int
 template <int D, int FMT, int NB>
 struct Smem {
   using G = KvGroup<D, FMT>;
-  static constexpr int kStage = (kTile / kKvGroup) * G::kBytes;
+  static constexpr int kTile = kTileOf<D>;
+  static constexpr int kGroups = kTile / kKvGroup;   // of a tile
+  static constexpr int kStage = kGroups * G::kBytes;
   // CTAs an SM, and stages a warp: as many as registers and shared memory give
-  static constexpr int kCtas = NB == 1 ? KVC : 2;
-  static constexpr int kSlots = NB == 1 ? KVS : 2;
+  static constexpr int kCtas = NB == 1 ? 3 : 2;
+  static constexpr int kSlots = 3;
   static constexpr int kStages = kSlots * kWarps;
   // a warp's eight rows of results fit the stage it used last
   static constexpr int kORow = D + 4;
   static_assert(8 * kORow * 4 <= kStage, "results in a stage");
+  static_assert(kWarps >= 4, "a warp a row where partials are joined");
   alignas(128) uint8_t ring[kStages][kStage];
   static constexpr int kQueries = NB == 1 ? 4 : 2;   // items whose queries are on chip
   static constexpr int kList = 64;          // tiles listed ahead
   static_assert(kStages <= 32, "a lane a stage");
   alignas(16) uint16_t raw[kQueries][8 * NB][D];   // queries as they come
-  const uint8_t* list[kList][2];            // where the groups of coming tiles lie
+  const uint8_t* list[kList][kGroups];      // where the groups of coming tiles lie
   uint4 q[NB][D / 32][32];                  // B operands, a lane's of two MMAs together
   float fq[8 * NB];                         // takes a row's scores to log2 units
   float m[kWarps][8], l[kWarps][8];
   uint64_t full[kStages], empty[kStages], qfull[kQueries], qfree[kQueries];
   int valid[kStages];                       // bit u: group u of the stage holds keys
   int held[kWarps];                         // the stage that holds a warp's results, or -1
-  int64_t scan[kThreads / 32 + 2];
+  int64_t scan[2 * kThreads / 32 + 2];
+  Range range;
   int abort;
   int last;
 };
@@ -369,16 +417,156 @@ struct Smem {
 template <int NB>
 __host__ __device__ constexpr size_t partial_floats(int D) { return static_cast<size_t>(NB) * 8 * (D + 2); }
 
+// The end of an item that CTAs share: its partial rows are written; the last
+// CTA to arrive joins them.
+template <int D, int FMT, int NB>
+__device__ __forceinline__ void finish_split(const KvAttnArgs& a, Smem<D, FMT, NB>& sm, int stage, int q0, int tiles, int at,
+                                          int h, int row0, int rows) {
+  using S = Smem<D, FMT, NB>;
+  constexpr int kRows = 8 * NB, kE = D / 32;
+  constexpr size_t kPart = partial_floats<NB>(D);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint32_t* counters = reinterpret_cast<uint32_t*>(a.workspace + kWsHeaderBytes);
+  float* partials = reinterpret_cast<float*>(a.workspace + kWsHeaderBytes + kWsCountersBytes);
+  const float gv = a.cache.scales ? a.cache.scales[a.cache.heads + h] : 1.0f;
+  auto results = [&](int v) { return reinterpret_cast<float(*)[S::kORow]>(sm.ring[v]); };   // [8]
+  const int64_t item0 = sm.range.begin + at;
+  const int c0 = cta_of(sm.range.total, sm.range.ctas, item0);
+  const int c1 = cta_of(sm.range.total, sm.range.ctas, item0 + (tiles > 1 ? tiles - 1 + sm.range.cost : 0));
+  const int parts = c1 - c0 + 1;   // contributor k of the item is CTA c0 + k
+  auto last_of = [&](uint32_t* counter, int of) {   // are this CTA's sums the last of `of`?
+    consumers_sync();
+    if (tid == 0) {
+      const bool last = atomic_add_acq_rel_gpu(counter, 1u) == static_cast<uint32_t>(of - 1);
+      if (last) *counter = 0;   // everyone has arrived
+      sm.last = last;
+    }
+    consumers_sync();
+    return sm.last != 0;
+  };
+  // Joins contributors from, from + step, ... below `to`, into the output or
+  // the first one's place.  Every warp finds all weights, with a contributor a
+  // lane; the warps that hold a stage then add the rows of every so-manieth.
+  auto join = [&](int from, int to, int step, bool out) {
+    int before = 0, holders = 0;
+    for (int v = 0; v < kWarps; ++v) {
+      before += v < warp && sm.held[v] >= 0;
+      holders += sm.held[v] >= 0;
+    }
+    const int n = (to - from + step - 1) / step;
+    auto part = [&](int i) {
+      const int k = from + i * step;
+      return partials + (2 * static_cast<size_t>(c0 + k) + (k == 0)) * kPart;
+    };
+    float* place = partials + (2 * static_cast<size_t>(c0 + from) + (from == 0)) * kPart;
+#pragma unroll 1
+    for (int half = 0; half < 2 * NB; ++half) {   // four rows at a time
+      consumers_sync();   // the stages are free
+      const int base = 4 * half;
+      float M[4], L[4] = {}, acc[4][kE] = {};
+#pragma unroll
+      for (int r = 0; r < 4; ++r) M[r] = -INFINITY;
+#pragma unroll 1
+      for (int i0 = 0; i0 < n; i0 += 32) {
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(part(min(i0 + lane, n - 1)) + kRows * D + base));
+        M[0] = fmaxf(M[0], x.x), M[1] = fmaxf(M[1], x.y), M[2] = fmaxf(M[2], x.z), M[3] = fmaxf(M[3], x.w);
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) M[r] = fmaxf(M[r], __shfl_xor_sync(0xFFFFFFFFu, M[r], off));
+#pragma unroll 1
+      for (int i0 = 0; i0 < n; i0 += 32) {
+        const float* p = part(min(i0 + lane, n - 1)) + kRows * D + base;
+        const float4 m4 = __ldcg(reinterpret_cast<const float4*>(p));
+        const float4 l4 = __ldcg(reinterpret_cast<const float4*>(p + kRows));
+        const bool here = i0 + lane < n;
+        float f[4] = {weight_of(m4.x, l4.x, M[0]), weight_of(m4.y, l4.y, M[1]), weight_of(m4.z, l4.z, M[2]),
+                      weight_of(m4.w, l4.w, M[3])};
+        const float l1[4] = {l4.x, l4.y, l4.z, l4.w};
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          if (!here) f[r] = 0.0f;
+          L[r] += here ? f[r] * l1[r] : 0.0f;
+        }
+        if (stage >= 0) {
+          const int most = min(32, n - i0);
+#pragma unroll 4
+          for (int j = before; j < most; j += holders) {
+            const float* q = part(i0 + j) + base * D + lane * kE;
+            float x[4][kE];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) load_part<kE>(q + r * D, x[r]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float fr = __shfl_sync(0xFFFFFFFFu, f[r], j);
+#pragma unroll
+              for (int e = 0; e < kE; ++e) acc[r][e] += fr * x[r][e];
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) L[r] += __shfl_xor_sync(0xFFFFFFFFu, L[r], off);
+      if (stage >= 0) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) store_part<kE>(&results(stage)[r][lane * kE], acc[r]);
+      }
+      consumers_sync();   // (also: all have read the first one's maxima and sums)
+      if (warp < 4) {     // warp r adds row r
+        float y[kE] = {};
+        for (int v = 0; v < kWarps; ++v) {
+          if (sm.held[v] < 0) continue;
+          float x[kE];
+          load_row<kE>(&results(sm.held[v])[warp][lane * kE], x);
+#pragma unroll
+          for (int e = 0; e < kE; ++e) y[e] += x[e];
+        }
+        const int row = base + warp;
+        const float Mr = warp == 0 ? M[0] : warp == 1 ? M[1] : warp == 2 ? M[2] : M[3];
+        const float Lr = warp == 0 ? L[0] : warp == 1 ? L[1] : warp == 2 ? L[2] : L[3];
+        if (out) {
+          if (row < rows) store_row<D>(a, q0, row0 + row, h, lane, Mr, Lr, y, gv);
+        } else {
+          store_part<kE>(place + row * D + lane * kE, y);
+          if (lane == 0) {
+            place[kRows * D + row] = Mr;
+            place[kRows * D + kRows + row] = Lr;
+          }
+        }
+      }
+    }
+  };
+  if (parts <= kJoinFlat) {
+    if (last_of(&counters[c0], parts)) join(0, parts, 1, true);
+  } else {
+    // groups of about the square root, each joined by its last arriver
+    int per = 7;
+    while (per * per < parts) ++per;
+    const int k = static_cast<int>(blockIdx.x) - c0;
+    const int first = k / per * per, groups = (parts + per - 1) / per;
+    const int size = min(per, parts - first);
+    // (a group of one is joined as it is, so that the leader of any later
+    // group than the first begins no other item: its counter is this item's)
+    if (size == 1 || last_of(&counters[kGroupCounters + c0 + first], size)) {
+      if (size > 1) join(first, first + size, 1, false);
+      if (last_of(&counters[c0], groups)) join(0, parts, per, true);
+    }
+  }
+}
+
 template <int D, int FMT, int NB>
 __global__ void __launch_bounds__(kThreads, Smem<D, FMT, NB>::kCtas) kv_attn_kernel(const __grid_constant__ KvAttnArgs a) {
   using S = Smem<D, FMT, NB>;
   using G = KvGroup<D, FMT>;
   constexpr int kRows = 8 * NB;
+  constexpr int kTile = S::kTile, kU = S::kGroups;
   constexpr int kK = D / 16;            // MMAs along D of the first product, row tiles of the second
   extern __shared__ __align__(128) uint8_t raw_smem[];
   S& sm = *reinterpret_cast<S*>(raw_smem);
   uint32_t* status = reinterpret_cast<uint32_t*>(a.workspace);
-  uint32_t* counters = reinterpret_cast<uint32_t*>(a.workspace + kWsHeaderBytes);
   float* partials = reinterpret_cast<float*>(a.workspace + kWsHeaderBytes + kWsCountersBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   auto wait = [&](uint64_t* bar, uint32_t phase) { wait_phase(bar, phase, a.timeout_ns, &sm.abort); };
@@ -395,9 +583,10 @@ __global__ void __launch_bounds__(kThreads, Smem<D, FMT, NB>::kCtas) kv_attn_ker
     sm.abort = 0;
     mbar_fence_init();
   }
-  const Range range = find_range(a, kRows, sm.scan, status);   // (synchronises the CTA)
+  const Range range = find_range<kTile, kRows>(a, sm.scan, status);
   if (range.begin >= range.end) return;
-  Walk<kRows> w(a, range, status);
+  if (tid == 0) sm.range = range;   // (for items that CTAs share)
+  Walk<kTile, kRows> w(a, range, status);
   uint32_t items = 0;   // items before this one
 
   if (warp == kWarps) {
@@ -437,10 +626,11 @@ __global__ void __launch_bounds__(kThreads, Smem<D, FMT, NB>::kCtas) kv_attn_ker
           // each lane finds the pages of one tile
           const int32_t* table = a.block_table + w.b * a.table_stride;
           const int key0 = w.s.lo + (t0 + lane) * kTile;
-          const uint8_t* src[2] = {nullptr, nullptr};
+          const uint8_t* src[kU];
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
+          for (int u = 0; u < kU; ++u) {
             const int key = key0 + u * kKvGroup;
+            src[u] = nullptr;
             if (t0 + lane < w.tb && key < w.s.len) {
               const int64_t page = table[key >> a.cache.page_shift];
               if (page >= 0 && page < a.cache.num_pages)
@@ -452,8 +642,8 @@ __global__ void __launch_bounds__(kThreads, Smem<D, FMT, NB>::kCtas) kv_attn_ker
           }
           const int count = min(32, w.tb - t0);
           if (lane < count) {
-            sm.list[(listed + lane) % S::kList][0] = src[0];
-            sm.list[(listed + lane) % S::kList][1] = src[1];
+#pragma unroll
+            for (int u = 0; u < kU; ++u) sm.list[(listed + lane) % S::kList][u] = src[u];
           }
           __syncwarp();
           listed += count;
@@ -471,16 +661,29 @@ __global__ void __launch_bounds__(kThreads, Smem<D, FMT, NB>::kCtas) kv_attn_ker
       const bool go = feeds && num < listed &&
                       (round == 0 || mbar_test_wait(smem_u32(&sm.empty[lane]), (round - 1) & 1));
       if (go) {
-        const uint8_t* src0 = sm.list[num % S::kList][0];
-        const uint8_t* src1 = sm.list[num % S::kList][1];
         const uint32_t bar = smem_u32(&sm.full[lane]), dst = smem_u32(sm.ring[lane]);
-        sm.valid[lane] = (src0 ? 1 : 0) | (src1 ? 2 : 0);
-        mbar_arrive_expect_tx(bar, (src0 ? G::kBytes : 0) + (src1 ? G::kBytes : 0));
-        if (src0 && src1 == src0 + G::kBytes) {
-          bulk_g2s(dst, src0, 2 * G::kBytes, bar, policy);
-        } else {
-          if (src0) bulk_g2s(dst, src0, G::kBytes, bar, policy);
-          if (src1) bulk_g2s(dst + G::kBytes, src1, G::kBytes, bar, policy);
+        const uint8_t* src[kU];
+        int valid = 0;
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          src[u] = sm.list[num % S::kList][u];
+          valid |= (src[u] != nullptr) << u;
+        }
+        sm.valid[lane] = valid;
+        mbar_arrive_expect_tx(bar, __popc(valid) * G::kBytes);
+        // groups that follow one another in a page go with one copy
+#pragma unroll
+        for (int u = 0; u < kU; u += 2) {
+          if (kU == 4 && u == 0 && valid == 15 && src[kU - 1] == src[0] + (kU - 1) * G::kBytes) {
+            bulk_g2s(dst, src[0], kU * G::kBytes, bar, policy);
+            break;
+          }
+          if (src[u] && src[u + 1] == src[u] + G::kBytes) {
+            bulk_g2s(dst + u * G::kBytes, src[u], 2 * G::kBytes, bar, policy);
+          } else {
+            if (src[u]) bulk_g2s(dst + u * G::kBytes, src[u], G::kBytes, bar, policy);
+            if (src[u + 1]) bulk_g2s(dst + (u + 1) * G::kBytes, src[u + 1], G::kBytes, bar, policy);
+          }
         }
         num += S::kStages;
       }
@@ -547,7 +750,9 @@ __global__ void __launch_bounds__(kThreads, Smem<D, FMT, NB>::kCtas) kv_attn_ker
       amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
       const int shift = row_shift(amax);
-      const float up = ldexpf(1.0f, shift);
+      // (the scale's sign goes with Q, so that the factors are not negative)
+      const float factor = a.scale_log2 * (a.cache.scales ? a.cache.scales[w.h] : 1.0f);
+      const float up = copysignf(ldexpf(1.0f, shift), factor);
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
         const uint32_t wd[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
@@ -559,7 +764,9 @@ __global__ void __launch_bounds__(kThreads, Smem<D, FMT, NB>::kCtas) kv_attn_ker
         }
         sm.q[warp][i][lane] = make_uint4(o2[0], o2[1], o2[2], o2[3]);
       }
-      if (t == 0) sm.fq[row] = ldexpf(a.scale_log2 * (a.cache.scales ? a.cache.scales[w.h] : 1.0f), -shift);
+      // (nor zero, so that a masked score stays -inf)
+      const float f = ldexpf(fabsf(factor), -shift);
+      if (t == 0) sm.fq[row] = f < FLT_MIN ? FLT_MIN : f;
     }
     consumers_sync();
     if (tid == 0) mbar_arrive(smem_u32(&sm.qfree[items % S::kQueries]));
@@ -571,23 +778,29 @@ __global__ void __launch_bounds__(kThreads, Smem<D, FMT, NB>::kCtas) kv_attn_ker
     }
 
     float o[NB][kK][4];
-    float m[NB][2], l[NB][2];
-    int vref = -1024;   // MXFP4: exponent code V is held relative to
+    // reference maxima in log2 units (ref: 0 while there is none), what a score
+    // has to pass to move one, and the sums (in [0] and [1])
+    float m[NB][2], ref[NB][2], pass[NB][2], l[NB][4];
+    // MXFP4: exponent codes K and V are held relative to, and the rows' factors
+    // for scores of such K
+    int kref = 0, vref = 0;
+    float fk[NB][2];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      m[nb][0] = m[nb][1] = -INFINITY;
-      l[nb][0] = l[nb][1] = 0.0f;
+      m[nb][0] = m[nb][1] = pass[nb][0] = pass[nb][1] = -INFINITY;
+      fk[nb][0] = fk[nb][1] = FLT_MIN;
+      ref[nb][0] = ref[nb][1] = 0.0f;
+      l[nb][0] = l[nb][1] = l[nb][2] = l[nb][3] = 0.0f;
 #pragma unroll
       for (int i = 0; i < kK; ++i) o[nb][i][0] = o[nb][i][1] = o[nb][i][2] = o[nb][i][3] = 0.0f;
     }
 
-    // S^T = K Q^T of a tile (two groups of 16 keys), in log2 units
-    auto scores = [&](const uint8_t* base, float (&sc)[2][NB][4]) {
+    // S^T = K Q^T of a tile (groups of 16 keys), short of the rows' factors
+    auto scores = [&](const uint8_t* base, float (&sc)[kU][NB][4]) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+      for (int u = 0; u < kU; ++u) {
         // [e]: key key_a + 8 e of group u
         uint32_t wk[2][kKWords], sk[2][FMT == kNVFP4 && D == 128 ? 2 : 1];
-        float fk[2];   // MXFP4: what the token's scores still need
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const uint8_t* p = base + u * G::kBytes + 8 * e * G::kRow + k_codes;
@@ -600,12 +813,7 @@ __global__ void __launch_bounds__(kThreads, Smem<D, FMT, NB>::kCtas) kv_attn_ker
           }
           const uint8_t* ps = base + u * G::kBytes + 8 * e * G::kScales + k_scales;
           if constexpr (FMT == kMXFP4) {
-            // a key's scales lie in the lanes t of its g
-            const int c = *ps;
-            int top = max(c, __shfl_xor_sync(0xFFFFFFFFu, c, 1));
-            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-            sk[e][0] = f16_power(c - top + 12) * 0x10001u;
-            fk[e] = e8m0_to_f32(top) * 0.000244140625f;   // 2^(largest - 127 - 12)
+            sk[e][0] = f16x2_power(*ps - kref, *ps - kref);
           } else if constexpr (D == 128) {   // two scales, 16 elements each
             const uint32_t h = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(ps));
             sk[e][0] = __byte_perm(h, 0, 0x1010);
@@ -614,8 +822,8 @@ __global__ void __launch_bounds__(kThreads, Smem<D, FMT, NB>::kCtas) kv_attn_ker
             sk[e][0] = e4m3x2_to_f16x2(*ps * 0x0101u);
           }
         }
-        // two chains of products, for their latency
-        float c0[NB][4] = {}, c1[NB][4] = {};
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) sc[u][nb][0] = sc[u][nb][1] = sc[u][nb][2] = sc[u][nb][3] = 0.0f;
 #pragma unroll
         for (int j = 0; j < kKWords; ++j) {
           const uint32_t wa = wk[0][j], wb = wk[1][j];
@@ -628,28 +836,23 @@ __global__ void __launch_bounds__(kThreads, Smem<D, FMT, NB>::kCtas) kv_attn_ker
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
             const uint4 b = sm.q[nb][j][lane];
-            mma_f16(c0[nb], a00, a01, a02, a03, b.x, b.y);
-            mma_f16(c1[nb], a10, a11, a12, a13, b.z, b.w);
+            mma_f16(sc[u][nb], a00, a01, a02, a03, b.x, b.y);
+            mma_f16(sc[u][nb], a10, a11, a12, a13, b.z, b.w);
           }
         }
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            sc[u][nb][e] = (c0[nb][e] + c1[nb][e]) * (FMT == kMXFP4 ? fq[nb][e & 1] * fk[e >> 1] : fq[nb][e & 1]);
       }
     };
 
     // tile `i`'s softmax weights and its part of O; base: its codes
-    auto weigh = [&](const uint8_t* base, int i, int valid, float (&sc)[2][NB][4]) {
+    auto weigh = [&](const uint8_t* base, int i, int valid, float (&sc)[kU][NB][4]) {
       const int key0 = s.lo + (w.ta + i) * kTile;
       // the tile needs masks: it passes the keys every row sees, begins before
       // the last row's window, or lacks a page
-      const bool masked = valid != 3 || key0 + kTile > (a.causal ? s.len - s.nq + 1 : s.len) ||
+      const bool masked = valid != (1 << kU) - 1 || key0 + kTile > (a.causal ? s.len - s.nq + 1 : s.len) ||
                           (a.window > 0 && key0 <= s.len - 1 - a.window);
       if (masked) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < kU; ++u) {
           const bool here = (valid >> u) & 1;
           const int j0 = key0 + u * kKvGroup;
 #pragma unroll
@@ -666,52 +869,60 @@ __global__ void __launch_bounds__(kThreads, Smem<D, FMT, NB>::kCtas) kv_attn_ker
         }
       }
 
+      float(&fac)[NB][2] = FMT == kMXFP4 ? fk : fq;
       // ---- softmax: the reference maximum moves only when a score passes it
       // by 2^8, so most tiles need no exchange between lanes (p <= 2^8 fits FP16)
-      uint32_t pb[2][NB][2];
+      uint32_t pb[kU][NB][2];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        float h0 = fmaxf(fmaxf(sc[0][nb][0], sc[0][nb][2]), fmaxf(sc[1][nb][0], sc[1][nb][2]));
-        float h1 = fmaxf(fmaxf(sc[0][nb][1], sc[0][nb][3]), fmaxf(sc[1][nb][1], sc[1][nb][3]));
-        if (__any_sync(0xFFFFFFFFu, h0 > m[nb][0] + 8.0f || h1 > m[nb][1] + 8.0f)) {
+        float h0 = fmaxf(sc[0][nb][0], sc[0][nb][2]), h1 = fmaxf(sc[0][nb][1], sc[0][nb][3]);
+#pragma unroll
+        for (int u = 1; u < kU; ++u) {
+          h0 = fmaxf(h0, fmaxf(sc[u][nb][0], sc[u][nb][2]));
+          h1 = fmaxf(h1, fmaxf(sc[u][nb][1], sc[u][nb][3]));
+        }
+        if (__any_sync(0xFFFFFFFFu, h0 > pass[nb][0] || h1 > pass[nb][1])) {
 #pragma unroll
           for (int off = 4; off < 32; off <<= 1) {
             h0 = fmaxf(h0, __shfl_xor_sync(0xFFFFFFFFu, h0, off));
             h1 = fmaxf(h1, __shfl_xor_sync(0xFFFFFFFFu, h1, off));
           }
-          h0 = fmaxf(h0, m[nb][0]);
-          h1 = fmaxf(h1, m[nb][1]);
-          const float f0 = h0 == m[nb][0] ? 1.0f : ex2(m[nb][0] - h0);
-          const float f1 = h1 == m[nb][1] ? 1.0f : ex2(m[nb][1] - h1);
-          m[nb][0] = h0;
-          m[nb][1] = h1;
-          l[nb][0] *= f0;
-          l[nb][1] *= f1;
+          const float h[2] = {h0, h1};
+          float f[2];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float top = fmaxf(h[c] * fac[nb][c], m[nb][c]);
+            f[c] = top == m[nb][c] ? 1.0f : ex2(m[nb][c] - top);
+            m[nb][c] = top;
+            // (a row with no key yet: its scores are all -inf, and p = 0)
+            ref[nb][c] = top == -INFINITY ? 0.0f : top;
+            pass[nb][c] = (top + 8.0f) / fac[nb][c];
+            l[nb][c] *= f[c];
+          }
 #pragma unroll
           for (int i2 = 0; i2 < kK; ++i2) {
-            o[nb][i2][0] *= f0;
-            o[nb][i2][1] *= f1;
-            o[nb][i2][2] *= f0;
-            o[nb][i2][3] *= f1;
+            o[nb][i2][0] *= f[0];
+            o[nb][i2][1] *= f[1];
+            o[nb][i2][2] *= f[0];
+            o[nb][i2][3] *= f[1];
           }
         }
-        // a row with no key yet: its scores are all -inf and p = 0
-        const float m0 = m[nb][0] == -INFINITY ? 0.0f : m[nb][0];
-        const float m1 = m[nb][1] == -INFINITY ? 0.0f : m[nb][1];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const float p0 = ex2(sc[u][nb][0] - m0), p1 = ex2(sc[u][nb][1] - m1);
-          const float p2 = ex2(sc[u][nb][2] - m0), p3 = ex2(sc[u][nb][3] - m1);
-          l[nb][0] += p0 + p2;
-          l[nb][1] += p1 + p3;
+        for (int u = 0; u < kU; ++u) {
+          const float p0 = ex2(fmaf(sc[u][nb][0], fac[nb][0], -ref[nb][0]));
+          const float p1 = ex2(fmaf(sc[u][nb][1], fac[nb][1], -ref[nb][1]));
+          const float p2 = ex2(fmaf(sc[u][nb][2], fac[nb][0], -ref[nb][0]));
+          const float p3 = ex2(fmaf(sc[u][nb][3], fac[nb][1], -ref[nb][1]));
           pb[u][nb][0] = transpose8x8(pack_f16(p0, p1));
           pb[u][nb][1] = transpose8x8(pack_f16(p2, p3));
+          // the sums: a product with ones
+          mma_f16(l[nb], 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, pb[u][nb][0], pb[u][nb][1]);
         }
       }
 
       // ---- O^T += V^T P^T
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+      for (int u = 0; u < kU; ++u) {
         uint32_t wv[4][kVWords], cv[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -738,27 +949,8 @@ __global__ void __launch_bounds__(kThreads, Smem<D, FMT, NB>::kCtas) kv_attn_ker
           s01 = e4m3x2_to_f16x2(cv[0] | cv[1] << 8);
           s23 = e4m3x2_to_f16x2(cv[2] | cv[3] << 8);
         } else {
-          int top = max(max(static_cast<int>(cv[0]), static_cast<int>(cv[1])), max(static_cast<int>(cv[2]), static_cast<int>(cv[3])));
-          if (__any_sync(0xFFFFFFFFu, top > vref + 3)) {
-            // the lanes of a dimension block share their reference
-            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-            top = max(top, vref);
-            const float f = top == vref ? 1.0f : ex2(static_cast<float>(vref - top));
-            vref = top;
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-              for (int i2 = 0; i2 < kK; ++i2) {
-                o[nb][i2][0] *= f;
-                o[nb][i2][1] *= f;
-                o[nb][i2][2] *= f;
-                o[nb][i2][3] *= f;
-              }
-          }
-          const int r = 9 - vref;
-          s01 = f16_power(static_cast<int>(cv[0]) + r) | f16_power(static_cast<int>(cv[1]) + r) << 16;
-          s23 = f16_power(static_cast<int>(cv[2]) + r) | f16_power(static_cast<int>(cv[3]) + r) << 16;
+          s01 = f16x2_power(static_cast<int>(cv[0]) - vref, static_cast<int>(cv[1]) - vref);
+          s23 = f16x2_power(static_cast<int>(cv[2]) - vref, static_cast<int>(cv[3]) - vref);
         }
 #pragma unroll
         for (int j = 0; j < kVWords; ++j) {
@@ -772,6 +964,55 @@ __global__ void __launch_bounds__(kThreads, Smem<D, FMT, NB>::kCtas) kv_attn_ker
           pv_step<1>(o, pb[u], 4 * j + 1, lo01, hi01, lo23, hi23, s01, s23);
           pv_step<2>(o, pb[u], 4 * j + 2, lo01, hi01, lo23, hi23, s01, s23);
           pv_step<3>(o, pb[u], 4 * j + 3, lo01, hi01, lo23, hi23, s01, s23);
+        }
+      }
+    };
+
+    // MXFP4: raises the references where a scale of the tile passes one by more
+    // than 2^3, up to which 6 times a scale stays inside FP16 (relative to a
+    // reference, scales are 2^9 and down to 2^-23 of it exact)
+    auto refer = [&](const uint8_t* base, int i, int valid) {
+      const int key0 = s.lo + (w.ta + i) * kTile;
+      int tk = 0, tv = 0;
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const uint8_t* grp = base + u * G::kBytes;
+        // the group's 16 tokens' scales, kScales bytes each for K and for V: a
+        // lane looks at the bytes of token lane / 2
+        const int tok = lane >> 1;
+        const bool here = ((valid >> u) & 1) && key0 + u * kKvGroup + tok < s.len;
+        constexpr int kB = G::kScales / 2;   // 1 or 2
+        const uint8_t* pk = grp + G::kKScales + tok * G::kScales + (lane & 1) * kB;
+        const uint8_t* pv = grp + G::kVScales + tok * G::kScales + (lane & 1) * kB;
+        if (here) {
+#pragma unroll
+          for (int e = 0; e < kB; ++e) {
+            tk = max(tk, static_cast<int>(pk[e]));
+            tv = max(tv, static_cast<int>(pv[e]));
+          }
+        }
+      }
+      if (__any_sync(0xFFFFFFFFu, tk > kref + 3 || tv > vref + 3)) {
+        tk = max(kref, static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, tk)));
+        tv = max(vref, static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, tv)));
+        const float f = tv == vref ? 1.0f : ex2(static_cast<float>(vref - tv));
+        kref = tk;
+        vref = tv;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float x = fq[nb][c] * ldexpf(1.0f, kref - 136);
+            fk[nb][c] = x < FLT_MIN ? FLT_MIN : x;
+            pass[nb][c] = (m[nb][c] + 8.0f) / fk[nb][c];
+          }
+#pragma unroll
+          for (int i2 = 0; i2 < kK; ++i2) {
+            o[nb][i2][0] *= f;
+            o[nb][i2][1] *= f;
+            o[nb][i2][2] *= f;
+            o[nb][i2][3] *= f;
+          }
         }
       }
     };
@@ -794,7 +1035,8 @@ __global__ void __launch_bounds__(kThreads, Smem<D, FMT, NB>::kCtas) kv_attn_ker
         slot = 0;
         phase ^= 1u;
       }
-      float sc[2][NB][4];
+      if constexpr (FMT == kMXFP4) refer(sm.ring[stage], i, sm.valid[stage]);
+      float sc[kU][NB][4];
       scores(sm.ring[stage], sc);
       weigh(sm.ring[stage], i, sm.valid[stage], sc);
     }
@@ -803,7 +1045,7 @@ __global__ void __launch_bounds__(kThreads, Smem<D, FMT, NB>::kCtas) kv_attn_ker
     // ---- the warps' results meet: each puts its eight rows (unscaled O,
     // maximum, sum) into its last stage, a warp then adds a row of all warps
     const float gv = a.cache.scales ? a.cache.scales[a.cache.heads + w.h] : 1.0f;
-    const float vscale = FMT == kMXFP4 ? ldexpf(1.0f, max(vref, 0) - 127 - 9) : 1.0f;
+    const float vscale = FMT == kMXFP4 ? ldexpf(1.0f, vref - 136) : 1.0f;
     const bool whole = count == s.tiles;
     constexpr size_t kPart = partial_floats<NB>(D);
     constexpr int kE = D / 32;            // dimensions of a lane in a merged row
@@ -827,7 +1069,7 @@ __global__ void __launch_bounds__(kThreads, Smem<D, FMT, NB>::kCtas) kv_attn_ker
         }
         const int row = nb * 8 + r8;
         if (out) {
-          if (row < w.rows) store_row<D>(a, s, w.row0 + row, w.h, lane, M, L, acc, gv);
+          if (row < w.rows) store_row<D>(a, s.q0, w.row0 + row, w.h, lane, M, L, acc, gv);
         } else {
           store_part<kE>(mine + row * D + lane * kE, acc);
           if (lane == 0) {
@@ -841,11 +1083,6 @@ __global__ void __launch_bounds__(kThreads, Smem<D, FMT, NB>::kCtas) kv_attn_ker
     for (int nb = 0; nb < NB; ++nb) {
       if (nb > 0) consumers_sync();   // the stages and sums are free
       if (stage >= 0) {
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1) {
-          l[nb][0] += __shfl_xor_sync(0xFFFFFFFFu, l[nb][0], off);
-          l[nb][1] += __shfl_xor_sync(0xFFFFFFFFu, l[nb][1], off);
-        }
         if (g == 0) {
           sm.m[warp][2 * t] = m[nb][0];
           sm.m[warp][2 * t + 1] = m[nb][1];
@@ -865,71 +1102,7 @@ __global__ void __launch_bounds__(kThreads, Smem<D, FMT, NB>::kCtas) kv_attn_ker
       consumers_sync();
       merge(nb, whole);
     }
-    if (!whole) {
-      const int64_t item0 = range.begin + w.at;
-      const int c0 = cta_of(range.total, range.ctas, item0);
-      const int c1 = cta_of(range.total, range.ctas, item0 + (s.tiles > 1 ? s.tiles - 1 + kItemCost : 0));
-      consumers_sync();
-      if (tid == 0) sm.last = atomic_add_acq_rel_gpu(&counters[c0], 1u) == static_cast<uint32_t>(c1 - c0);
-      consumers_sync();
-      if (sm.last) {
-        if (tid == 0) counters[c0] = 0;   // every CTA of the item has arrived
-        // the warps that hold a stage add the partials of every so-manieth CTA,
-        // eight rows at a time; then their sums meet as above
-        int before = 0, holders = 0;
-        for (int v = 0; v < kWarps; ++v) {
-          before += v < warp && sm.held[v] >= 0;
-          holders += sm.held[v] >= 0;
-        }
-#pragma unroll 1
-        for (int nb = 0; nb < NB; ++nb) {
-          consumers_sync();   // the stages are free
-          if (stage >= 0) {
-#pragma unroll 1
-            for (int r0 = 0; r0 < 8; r0 += 4) {
-              float M[4], L[4], acc[4][kE];
-#pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                M[r] = -INFINITY;
-                L[r] = 0.0f;
-#pragma unroll
-                for (int e = 0; e < kE; ++e) acc[r][e] = 0.0f;
-              }
-#pragma unroll 1
-              for (int c = c0 + before; c <= c1; c += holders) {
-                const float* p = partials + (2 * static_cast<size_t>(c) + (c == c0)) * kPart;
-                const int row = nb * 8 + r0;
-                const float4 mc = __ldcg(reinterpret_cast<const float4*>(p + kRows * D + row));
-                const float4 lc = __ldcg(reinterpret_cast<const float4*>(p + kRows * D + kRows + row));
-                float x[4][kE];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) load_part<kE>(p + (row + r) * D + lane * kE, x[r]);
-                const float m4[4] = {mc.x, mc.y, mc.z, mc.w}, l4[4] = {lc.x, lc.y, lc.z, lc.w};
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                  const float top = fmaxf(M[r], m4[r]);
-                  const float f0 = weight_of(M[r], L[r], top), f1 = weight_of(m4[r], l4[r], top);
-                  M[r] = top;
-                  L[r] = L[r] * f0 + l4[r] * f1;
-#pragma unroll
-                  for (int e = 0; e < kE; ++e) acc[r][e] = acc[r][e] * f0 + x[r][e] * f1;
-                }
-              }
-#pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                store_part<kE>(&results(stage)[r0 + r][lane * kE], acc[r]);
-                if (lane == 0) {
-                  sm.m[warp][r0 + r] = M[r];
-                  sm.l[warp][r0 + r] = L[r];
-                }
-              }
-            }
-          }
-          consumers_sync();
-          merge(nb, true);
-        }
-      }
-    }
+    if (!whole) finish_split<D, FMT, NB>(a, sm, stage, s.q0, s.tiles, w.at, w.h, w.row0, w.rows);
     fence_async_shared();   // (results in the stages, before the next copies into them)
     consumers_sync();       // stages, sums, queries and sm.last may be written again
     if (stage >= 0 && lane == 0) mbar_arrive(smem_u32(&sm.empty[stage]));

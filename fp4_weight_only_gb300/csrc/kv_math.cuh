@@ -27,6 +27,13 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return r;
 }
 
+// FP16x2 of 2^(lo + 9) and 2^(hi + 9), for lo, hi <= 3: through FP32's exponent
+// field, whose conversion makes subnormals and zero of what is below FP16.
+__device__ __forceinline__ uint32_t f16x2_power(int lo, int hi) {
+  return pack_f16(__uint_as_float(static_cast<uint32_t>(max(lo + 136, 0)) << 23),
+                  __uint_as_float(static_cast<uint32_t>(max(hi + 136, 0)) << 23));
+}
+
 // FP16 bits of 2^n, n <= 15: subnormal below 2^-14, zero below 2^-24.
 __device__ __forceinline__ uint32_t f16_power(int n) {
   return n >= -14 ? static_cast<uint32_t>(n + 15) << 10 : 0x400u >> min(-14 - n, 31);
