@@ -55,7 +55,7 @@ constexpr int kConsumers = kWarps * 32;
 constexpr int kThreads = kConsumers + 32;
 constexpr int kMostCtas = 480;               // partial slots are sized for this
 constexpr int kGroupCounters = kMostCtas;    // counters[kGroupCounters + ..]: arrivals of groups of partials
-constexpr int kJoinFlat = 48;                // partials joined in one step; more in groups
+constexpr int kJoinFlat = 16;                // partials joined in one step; more in groups
 
 // Keys of a tile: 4.5 KB of codes and scales in either head dimension.
 template <int D>
@@ -394,7 +394,6 @@ struct Smem {
   // a warp's eight rows of results fit the stage it used last
   static constexpr int kORow = D + 4;
   static_assert(8 * kORow * 4 <= kStage, "results in a stage");
-  static_assert(kWarps >= 4, "a warp a row where partials are joined");
   alignas(128) uint8_t ring[kStages][kStage];
   static constexpr int kQueries = NB == 1 ? 4 : 2;   // items whose queries are on chip
   static constexpr int kList = 64;          // tiles listed ahead
@@ -420,16 +419,14 @@ __host__ __device__ constexpr size_t partial_floats(int D) { return static_cast<
 // The end of an item that CTAs share: its partial rows are written; the last
 // CTA to arrive joins them.
 template <int D, int FMT, int NB>
-__device__ __forceinline__ void finish_split(const KvAttnArgs& a, Smem<D, FMT, NB>& sm, int stage, int q0, int tiles, int at,
-                                          int h, int row0, int rows) {
-  using S = Smem<D, FMT, NB>;
+__device__ __forceinline__ void finish_split(const KvAttnArgs& a, Smem<D, FMT, NB>& sm, int q0, int tiles, int at, int h,
+                                             int row0, int rows) {
   constexpr int kRows = 8 * NB, kE = D / 32;
   constexpr size_t kPart = partial_floats<NB>(D);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint32_t* counters = reinterpret_cast<uint32_t*>(a.workspace + kWsHeaderBytes);
   float* partials = reinterpret_cast<float*>(a.workspace + kWsHeaderBytes + kWsCountersBytes);
   const float gv = a.cache.scales ? a.cache.scales[a.cache.heads + h] : 1.0f;
-  auto results = [&](int v) { return reinterpret_cast<float(*)[S::kORow]>(sm.ring[v]); };   // [8]
   const int64_t item0 = sm.range.begin + at;
   const int c0 = cta_of(sm.range.total, sm.range.ctas, item0);
   const int c1 = cta_of(sm.range.total, sm.range.ctas, item0 + (tiles > 1 ? tiles - 1 + sm.range.cost : 0));
@@ -444,97 +441,50 @@ __device__ __forceinline__ void finish_split(const KvAttnArgs& a, Smem<D, FMT, N
     consumers_sync();
     return sm.last != 0;
   };
-  // Joins contributors from, from + step, ... below `to`, into the output or
-  // the first one's place.  Every warp finds all weights, with a contributor a
-  // lane; the warps that hold a stage then add the rows of every so-manieth.
+  // Joins contributors from, from + step, ... below `to` (at most 32), into the
+  // output or the first one's place.  A warp joins whole rows, a contributor's
+  // maximum and sum to a lane.
   auto join = [&](int from, int to, int step, bool out) {
-    int before = 0, holders = 0;
-    for (int v = 0; v < kWarps; ++v) {
-      before += v < warp && sm.held[v] >= 0;
-      holders += sm.held[v] >= 0;
-    }
     const int n = (to - from + step - 1) / step;
     auto part = [&](int i) {
-      const int k = from + i * step;
+      const int k = from + min(i, n - 1) * step;
       return partials + (2 * static_cast<size_t>(c0 + k) + (k == 0)) * kPart;
     };
-    float* place = partials + (2 * static_cast<size_t>(c0 + from) + (from == 0)) * kPart;
 #pragma unroll 1
-    for (int half = 0; half < 2 * NB; ++half) {   // four rows at a time
-      consumers_sync();   // the stages are free
-      const int base = 4 * half;
-      float M[4], L[4] = {}, acc[4][kE] = {};
+    for (int row = warp; row < rows; row += kWarps) {
+      const float m = __ldcg(part(lane) + kRows * D + row), l = __ldcg(part(lane) + kRows * D + kRows + row);
+      constexpr int kBatch = 4;   // contributors on their way together
+      float x[kBatch][kE], y[kE] = {};
 #pragma unroll
-      for (int r = 0; r < 4; ++r) M[r] = -INFINITY;
+      for (int e = 0; e < kBatch; ++e) load_part<kE>(part(e) + row * D + lane * kE, x[e]);
+      float M = m, L = lane < n ? l : 0.0f;
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, off));
+      const float f = lane < n ? weight_of(m, l, M) : 0.0f;
+      L *= f;
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, off);
 #pragma unroll 1
-      for (int i0 = 0; i0 < n; i0 += 32) {
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(part(min(i0 + lane, n - 1)) + kRows * D + base));
-        M[0] = fmaxf(M[0], x.x), M[1] = fmaxf(M[1], x.y), M[2] = fmaxf(M[2], x.z), M[3] = fmaxf(M[3], x.w);
-      }
+      for (int j = 0; j < n; j += kBatch) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
+        for (int e = 0; e < kBatch; ++e) {
+          const float fe = __shfl_sync(0xFFFFFFFFu, f, j + e);   // (past n: the weight is 0, the row another's)
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) M[r] = fmaxf(M[r], __shfl_xor_sync(0xFFFFFFFFu, M[r], off));
-#pragma unroll 1
-      for (int i0 = 0; i0 < n; i0 += 32) {
-        const float* p = part(min(i0 + lane, n - 1)) + kRows * D + base;
-        const float4 m4 = __ldcg(reinterpret_cast<const float4*>(p));
-        const float4 l4 = __ldcg(reinterpret_cast<const float4*>(p + kRows));
-        const bool here = i0 + lane < n;
-        float f[4] = {weight_of(m4.x, l4.x, M[0]), weight_of(m4.y, l4.y, M[1]), weight_of(m4.z, l4.z, M[2]),
-                      weight_of(m4.w, l4.w, M[3])};
-        const float l1[4] = {l4.x, l4.y, l4.z, l4.w};
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          if (!here) f[r] = 0.0f;
-          L[r] += here ? f[r] * l1[r] : 0.0f;
+          for (int i = 0; i < kE; ++i) y[i] += fe * x[e][i];
         }
-        if (stage >= 0) {
-          const int most = min(32, n - i0);
-#pragma unroll 4
-          for (int j = before; j < most; j += holders) {
-            const float* q = part(i0 + j) + base * D + lane * kE;
-            float x[4][kE];
+        if (j + kBatch < n) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) load_part<kE>(q + r * D, x[r]);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const float fr = __shfl_sync(0xFFFFFFFFu, f[r], j);
-#pragma unroll
-              for (int e = 0; e < kE; ++e) acc[r][e] += fr * x[r][e];
-            }
-          }
+          for (int e = 0; e < kBatch; ++e) load_part<kE>(part(j + kBatch + e) + row * D + lane * kE, x[e]);
         }
       }
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) L[r] += __shfl_xor_sync(0xFFFFFFFFu, L[r], off);
-      if (stage >= 0) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) store_part<kE>(&results(stage)[r][lane * kE], acc[r]);
-      }
-      consumers_sync();   // (also: all have read the first one's maxima and sums)
-      if (warp < 4) {     // warp r adds row r
-        float y[kE] = {};
-        for (int v = 0; v < kWarps; ++v) {
-          if (sm.held[v] < 0) continue;
-          float x[kE];
-          load_row<kE>(&results(sm.held[v])[warp][lane * kE], x);
-#pragma unroll
-          for (int e = 0; e < kE; ++e) y[e] += x[e];
-        }
-        const int row = base + warp;
-        const float Mr = warp == 0 ? M[0] : warp == 1 ? M[1] : warp == 2 ? M[2] : M[3];
-        const float Lr = warp == 0 ? L[0] : warp == 1 ? L[1] : warp == 2 ? L[2] : L[3];
-        if (out) {
-          if (row < rows) store_row<D>(a, q0, row0 + row, h, lane, Mr, Lr, y, gv);
-        } else {
-          store_part<kE>(place + row * D + lane * kE, y);
-          if (lane == 0) {
-            place[kRows * D + row] = Mr;
-            place[kRows * D + kRows + row] = Lr;
-          }
+      if (out) {
+        store_row<D>(a, q0, row0 + row, h, lane, M, L, y, gv);
+      } else {
+        float* place = part(0);
+        store_part<kE>(place + row * D + lane * kE, y);
+        if (lane == 0) {
+          place[kRows * D + row] = M;
+          place[kRows * D + kRows + row] = L;
         }
       }
     }
@@ -543,7 +493,7 @@ __device__ __forceinline__ void finish_split(const KvAttnArgs& a, Smem<D, FMT, N
     if (last_of(&counters[c0], parts)) join(0, parts, 1, true);
   } else {
     // groups of about the square root, each joined by its last arriver
-    int per = 7;
+    int per = 5;
     while (per * per < parts) ++per;
     const int k = static_cast<int>(blockIdx.x) - c0;
     const int first = k / per * per, groups = (parts + per - 1) / per;
@@ -1102,7 +1052,7 @@ __global__ void __launch_bounds__(kThreads, Smem<D, FMT, NB>::kCtas) kv_attn_ker
       consumers_sync();
       merge(nb, whole);
     }
-    if (!whole) finish_split<D, FMT, NB>(a, sm, stage, s.q0, s.tiles, w.at, w.h, w.row0, w.rows);
+    if (!whole) finish_split<D, FMT, NB>(a, sm, s.q0, s.tiles, w.at, w.h, w.row0, w.rows);
     fence_async_shared();   // (results in the stages, before the next copies into them)
     consumers_sync();       // stages, sums, queries and sm.last may be written again
     if (stage >= 0 && lane == 0) mbar_arrive(smem_u32(&sm.empty[stage]));
