@@ -451,40 +451,59 @@ __device__ __forceinline__ void finish_split(const KvAttnArgs& a, Smem<D, FMT, N
       return partials + (2 * static_cast<size_t>(c0 + k) + (k == 0)) * kPart;
     };
 #pragma unroll 1
-    for (int row = warp; row < rows; row += kWarps) {
-      const float m = __ldcg(part(lane) + kRows * D + row), l = __ldcg(part(lane) + kRows * D + kRows + row);
+    for (int first_row = warp; first_row < rows; first_row += 2 * kWarps) {   // two rows at a time
       constexpr int kBatch = 4;   // contributors on their way together
-      float x[kBatch][kE], y[kE] = {};
+      float m[2], l[2], f[2], x[2][kBatch][kE], y[2][kE] = {};
+      auto row_of = [&](int i) { return min(first_row + i * kWarps, rows - 1); };
 #pragma unroll
-      for (int e = 0; e < kBatch; ++e) load_part<kE>(part(e) + row * D + lane * kE, x[e]);
-      float M = m, L = lane < n ? l : 0.0f;
+      for (int i = 0; i < 2; ++i) {
+        m[i] = __ldcg(part(lane) + kRows * D + row_of(i));
+        l[i] = __ldcg(part(lane) + kRows * D + kRows + row_of(i));
+      }
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, off));
-      const float f = lane < n ? weight_of(m, l, M) : 0.0f;
-      L *= f;
+      for (int e = 0; e < kBatch; ++e)
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, off);
+        for (int i = 0; i < 2; ++i) load_part<kE>(part(e) + row_of(i) * D + lane * kE, x[i][e]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float own = m[i];
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) m[i] = fmaxf(m[i], __shfl_xor_sync(0xFFFFFFFFu, m[i], off));
+        f[i] = lane < n ? weight_of(own, l[i], m[i]) : 0.0f;
+        l[i] = lane < n ? f[i] * l[i] : 0.0f;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], off);
+      }
 #pragma unroll 1
       for (int j = 0; j < n; j += kBatch) {
 #pragma unroll
-        for (int e = 0; e < kBatch; ++e) {
-          const float fe = __shfl_sync(0xFFFFFFFFu, f, j + e);   // (past n: the weight is 0, the row another's)
+        for (int e = 0; e < kBatch; ++e)
 #pragma unroll
-          for (int i = 0; i < kE; ++i) y[i] += fe * x[e][i];
-        }
+          for (int i = 0; i < 2; ++i) {
+            const float fe = __shfl_sync(0xFFFFFFFFu, f[i], j + e);   // (past n: the weight is 0, the row another's)
+#pragma unroll
+            for (int k = 0; k < kE; ++k) y[i][k] += fe * x[i][e][k];
+          }
         if (j + kBatch < n) {
 #pragma unroll
-          for (int e = 0; e < kBatch; ++e) load_part<kE>(part(j + kBatch + e) + row * D + lane * kE, x[e]);
+          for (int e = 0; e < kBatch; ++e)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) load_part<kE>(part(j + kBatch + e) + row_of(i) * D + lane * kE, x[i][e]);
         }
       }
-      if (out) {
-        store_row<D>(a, q0, row0 + row, h, lane, M, L, y, gv);
-      } else {
-        float* place = part(0);
-        store_part<kE>(place + row * D + lane * kE, y);
-        if (lane == 0) {
-          place[kRows * D + row] = M;
-          place[kRows * D + kRows + row] = L;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int row = first_row + i * kWarps;
+        if (row >= rows) continue;
+        if (out) {
+          store_row<D>(a, q0, row0 + row, h, lane, m[i], l[i], y[i], gv);
+        } else {
+          float* place = part(0);
+          store_part<kE>(place + row * D + lane * kE, y[i]);
+          if (lane == 0) {
+            place[kRows * D + row] = m[i];
+            place[kRows * D + kRows + row] = l[i];
+          }
         }
       }
     }
