@@ -234,12 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
   uint32_t* counters = reinterpret_cast<uint32_t*>(a.workspace + kWsHeaderBytes);
   float* partials = reinterpret_cast<float*>(a.workspace + kWsHeaderBytes + kWsCountersBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // waits never end the CTA: one that runs out raises the flag, later ones
-  // return at once, and every role walks on to its end
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (!mbar_wait_bounded(smem_u32(bar), parity, a.timeout_ns, &sm.abort)) *(volatile int*)&sm.abort = 1;
-    __syncwarp();
-  };
+  auto wait = [&](uint64_t* bar, uint32_t phase) { wait_phase(bar, phase, a.timeout_ns, &sm.abort); };
 
   if (tid == 0) {
     sm.abort = 0;
@@ -604,16 +599,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
           if constexpr (FMT == kMXFP4) wait(&sm.vfull[num & 1], (num >> 1) & 1);   // vfac, vscale
           tc_fence_after();
           uint32_t valid = 0;
-          float fc[4];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            valid |= sm.valid[num % kRing][c] << (2 * c);
-            fc[c] = FMT == kMXFP4 ? f * sm.kfac[num % kRing][c] : f;
-            // not zero, so that a masked score stays -inf (2^-126 of a score is nothing)
-            fc[c] = fc[c] < FLT_MIN ? FLT_MIN : fc[c];
-          }
+          for (int c = 0; c < 4; ++c) valid |= sm.valid[num % kRing][c] << (2 * c);
           if constexpr (FMT == kMXFP4) vs = sm.vscale[num % kRing];
           const bool masked = valid != 0xFFu || key0 + kKeys - 1 > all_hi || key0 < all_lo;
+          // factor of 32 keys' scores; not zero, so that a masked score stays
+          // -inf (2^-126 of a score is nothing)
+          auto factor_of = [&](int c) {
+            const float fc = FMT == kMXFP4 ? f * sm.kfac[num % kRing][c] : f;
+            return fc < FLT_MIN ? FLT_MIN : fc;
+          };
+          // 32 keys' scores (the loops over c stay rolled: this kernel's roles
+          // share an instruction cache that their code must fit)
           auto load_scores = [&](int c, float(&x)[32]) {
             uint32_t r[32];
             tmem_ld_x32(s_tmem + 32 * c, r);
@@ -622,21 +619,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
             for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(r[e]);
             if (masked) {
               const int from = lo - key0 - 32 * c, to = hi - key0 - 32 * c;
-              const bool g0 = (valid >> (2 * c)) & 1, g1 = (valid >> (2 * c + 1)) & 1;
+              // keys from..to of the 32, and of the groups that are there
+              uint32_t keep = to < 0 ? 0u : to >= 31 ? ~0u : (2u << to) - 1u;
+              keep &= from <= 0 ? ~0u : from > 31 ? 0u : ~0u << from;
+              if (!((valid >> (2 * c)) & 1)) keep &= 0xFFFF0000u;
+              if (!((valid >> (2 * c + 1)) & 1)) keep &= 0x0000FFFFu;
 #pragma unroll
               for (int e = 0; e < 32; ++e)
-                if (e < from || e > to || !(e < 16 ? g0 : g1)) x[e] = -INFINITY;
+                if (!((keep >> e) & 1)) x[e] = -INFINITY;
             }
           };
           // ---- the reference maximum moves only when passed by 2^8
           float top = -INFINITY;
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             float x[32], t = -INFINITY;
             load_scores(c, x);
 #pragma unroll
             for (int e = 0; e < 32; ++e) t = fmaxf(t, x[e]);
-            top = fmaxf(top, t * fc[c]);
+            top = fmaxf(top, t * factor_of(c));
           }
           const bool grow = top > m + 8.0f;
           const float vf = FMT == kMXFP4 && i > 0 ? sm.vfac[num % kRing] : 1.0f;
@@ -649,28 +650,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
             }
             if (i > 0) {
               r *= vf;
-#pragma unroll
-              for (int c = 0; c < D / 32; ++c) {
-                uint32_t o[32];
-                tmem_ld_x32(o_tmem + 32 * c, o);
+#pragma unroll 1
+              for (int c = 0; c < D / 16; ++c) {
+                uint32_t o[16];
+                tmem_ld_x16(o_tmem + 16 * c, o);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * r);
-                tmem_st_x16(o_tmem + 32 * c, *reinterpret_cast<uint32_t(*)[16]>(&o[0]));
-                tmem_st_x16(o_tmem + 32 * c + 16, *reinterpret_cast<uint32_t(*)[16]>(&o[16]));
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * r);
+                tmem_st_x16(o_tmem + 16 * c, o);
               }
             }
           }
           const float ref = m == -INFINITY ? 0.0f : m;
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             float x[32];
             load_scores(c, x);
+            const float fc = factor_of(c);
             uint32_t p[16];
             float l0 = 0.0f, l1 = 0.0f;
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const float p0 = ex2(fmaf(x[2 * e], fc[c], -ref)), p1 = ex2(fmaf(x[2 * e + 1], fc[c], -ref));
+              const float p0 = ex2(fmaf(x[2 * e], fc, -ref)), p1 = ex2(fmaf(x[2 * e + 1], fc, -ref));
               l0 += p0;
               l1 += p1;
               p[e] = pack_f16(p0, p1);
