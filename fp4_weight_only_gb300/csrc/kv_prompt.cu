@@ -14,10 +14,10 @@
 //   0-3, 4-7   softmax of row tile 0 and 1: a thread holds a row, so maximum
 //              and sum need no exchange; while one tile's scores are in the
 //              registers the tensor cores work on the other tile
-//   8-11       K: a thread converts a token's row (codes -> FP16, swizzled)
-//   12-15      V: a thread converts 8 tokens by D / 8 dimensions and writes
+//   8-11       V: a thread converts 8 tokens by D / 8 dimensions and writes
 //              them transposed (contraction along the tokens)
-//   16         issues the MMAs
+//   12-13      K: a thread converts two tokens' rows (codes -> FP16, swizzled)
+//   14         issues the MMAs
 // Codes go from global memory to registers a tile ahead; the converted tiles
 // are double-buffered.  Tensor memory: O_0, O_1, S_0, S_1 (all 512 columns at
 // D = 128).
@@ -40,8 +40,8 @@ namespace {
 constexpr int kKeys = 128;        // keys of a tile
 constexpr int kRowTile = 128;     // rows of an MMA tile
 constexpr int kRows = 2 * kRowTile;
-constexpr int kKWarp = 8, kVWarp = 12, kMmaWarp = 16;
-constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kVWarp = 8, kKWarp = 12, kMmaWarp = 14;
+constexpr int kThreads = 32 * 16;   // (warp 15 has no work)
 constexpr int kRing = 4;          // per-tile facts: written at most two tiles ahead of their last reader
 
 // ------------------------------------------------------------ work split
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
       mbar_init(smem_u32(&sm.sfull[i]), 1);
       mbar_init(smem_u32(&sm.pfull[i]), 4);
       mbar_init(smem_u32(&sm.ofull[i]), 1);
-      mbar_init(smem_u32(&sm.kfull[i]), 4);
+      mbar_init(smem_u32(&sm.kfull[i]), 2);
       mbar_init(smem_u32(&sm.kfree[i]), 1);
       mbar_init(smem_u32(&sm.vfull[i]), 4);
       mbar_init(smem_u32(&sm.vfree[i]), 1);
@@ -337,7 +337,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
     }
     commit(&sm.fin);
     mbar_wait_bounded(smem_u32(&sm.fin), 0, a.timeout_ns, nullptr);
-  } else if (warp >= kVWarp) {
+  } else if (warp > kMmaWarp) {
+    // (no work)
+  } else if (warp >= kVWarp && warp < kKWarp) {
     // ------------------------------------------------------------------ V
     constexpr int kD = D / 8;          // dimensions of a thread
     constexpr int kW = kD / 8;         // code words of a token
@@ -446,35 +448,37 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
   } else if (warp >= kKWarp) {
     // ------------------------------------------------------------------ K
     constexpr int kW = D / 8;          // code words of a token
+    constexpr int kS = (G::kScales + 3) / 4;
     const int kw = warp - kKWarp;
-    const int key_in = kw * 32 + lane;
-    uint32_t wd[kW];
-    uint32_t sc[(G::kScales + 3) / 4];
-    bool have = false;
+    uint32_t wd[2][kW], sc[2][kS];     // tokens kw 32 + lane and 64 + that
+    bool have[2] = {false, false};
     auto load = [&](int tile) {
-      const int key = w.k.lo + tile * kKeys + key_in;
-      const uint8_t* grp = group_of(key);
-      have = grp != nullptr;
 #pragma unroll
-      for (int j = 0; j < kW; ++j) wd[j] = 0;
+      for (int x = 0; x < 2; ++x) {
+        const int key = w.k.lo + tile * kKeys + x * 64 + kw * 32 + lane;
+        const uint8_t* grp = group_of(key);
+        have[x] = grp != nullptr;
 #pragma unroll
-      for (int j = 0; j < (G::kScales + 3) / 4; ++j) sc[j] = 0;
-      if (have) {
-        const int t = key % kKvGroup;
-        const uint4* p = reinterpret_cast<const uint4*>(grp + G::kKCodes + t * G::kRow);
+        for (int j = 0; j < kW; ++j) wd[x][j] = 0;
 #pragma unroll
-        for (int j = 0; j < kW / 4; ++j) {
-          const uint4 v = p[j];
-          wd[4 * j] = v.x, wd[4 * j + 1] = v.y, wd[4 * j + 2] = v.z, wd[4 * j + 3] = v.w;
-        }
-        const uint8_t* ps = grp + G::kKScales + t * G::kScales;
-        if constexpr (G::kScales == 8) {
-          const uint2 v = *reinterpret_cast<const uint2*>(ps);
-          sc[0] = v.x, sc[1] = v.y;
-        } else if constexpr (G::kScales == 4) {
-          sc[0] = *reinterpret_cast<const uint32_t*>(ps);
-        } else {
-          sc[0] = *reinterpret_cast<const uint16_t*>(ps);
+        for (int j = 0; j < kS; ++j) sc[x][j] = 0;
+        if (have[x]) {
+          const int t = key % kKvGroup;
+          const uint4* p = reinterpret_cast<const uint4*>(grp + G::kKCodes + t * G::kRow);
+#pragma unroll
+          for (int j = 0; j < kW / 4; ++j) {
+            const uint4 v = p[j];
+            wd[x][4 * j] = v.x, wd[x][4 * j + 1] = v.y, wd[x][4 * j + 2] = v.z, wd[x][4 * j + 3] = v.w;
+          }
+          const uint8_t* ps = grp + G::kKScales + t * G::kScales;
+          if constexpr (G::kScales == 8) {
+            const uint2 v = *reinterpret_cast<const uint2*>(ps);
+            sc[x][0] = v.x, sc[x][1] = v.y;
+          } else if constexpr (G::kScales == 4) {
+            sc[x][0] = *reinterpret_cast<const uint32_t*>(ps);
+          } else {
+            sc[x][0] = *reinterpret_cast<const uint16_t*>(ps);
+          }
         }
       }
     };
@@ -484,32 +488,36 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
       for (int i = 0; i < tiles; ++i) {
         const uint32_t num = n + i;
         if (num >= 2) wait(&sm.kfree[num & 1], ((num >> 1) - 1) & 1);
-        const unsigned held = __ballot_sync(0xFFFFFFFFu, have);
-        int top = 0;
-        if constexpr (FMT == kMXFP4) {
 #pragma unroll
-          for (int p = 0; p < G::kScales; ++p) top = max(top, static_cast<int>((sc[0] >> (8 * p)) & 0xFFu));
-          top = static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(top)));
-        }
-        if (lane == 0) {
-          sm.valid[num % kRing][kw] = (held & 0xFFFFu ? 1u : 0u) | (held >> 16 ? 2u : 0u);
-          if constexpr (FMT == kMXFP4) sm.kfac[num % kRing][kw] = e8m0_to_f32(top) * 0.000244140625f;
-        }
-        uint8_t* dst = &sm.k[num & 1][0][key_in * 128];
-        uint32_t s2 = 0;
+        for (int x = 0; x < 2; ++x) {
+          const int key_in = x * 64 + kw * 32 + lane, part = 2 * x + kw;
+          const unsigned held = __ballot_sync(0xFFFFFFFFu, have[x]);
+          int top = 0;
+          if constexpr (FMT == kMXFP4) {
 #pragma unroll
-        for (int j = 0; j < kW; ++j) {
-          if (j % (G::kBlock / 8) == 0) {   // this word begins a block
-            const int blk = j / (G::kBlock / 8);
-            const uint32_t b = (sc[blk / 4] >> (8 * (blk % 4))) & 0xFFu;
-            if constexpr (FMT == kNVFP4)
-              s2 = e4m3x2_to_f16x2(b * 0x0101u);
-            else
-              s2 = f16_power(static_cast<int>(b) - top + 12) * 0x10001u;
+            for (int p = 0; p < G::kScales; ++p) top = max(top, static_cast<int>((sc[x][0] >> (8 * p)) & 0xFFu));
+            top = static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(top)));
           }
-          *reinterpret_cast<uint4*>(dst + (j >> 3) * (kKeys * 128) + (((j & 7) ^ (key_in & 7)) << 4)) =
-              make_uint4(mul2(e2m1x2_to_f16x2<0>(wd[j]), s2), mul2(e2m1x2_to_f16x2<1>(wd[j]), s2),
-                         mul2(e2m1x2_to_f16x2<2>(wd[j]), s2), mul2(e2m1x2_to_f16x2<3>(wd[j]), s2));
+          if (lane == 0) {
+            sm.valid[num % kRing][part] = (held & 0xFFFFu ? 1u : 0u) | (held >> 16 ? 2u : 0u);
+            if constexpr (FMT == kMXFP4) sm.kfac[num % kRing][part] = e8m0_to_f32(top) * 0.000244140625f;
+          }
+          uint8_t* dst = &sm.k[num & 1][0][key_in * 128];
+          uint32_t s2 = 0;
+#pragma unroll
+          for (int j = 0; j < kW; ++j) {
+            if (j % (G::kBlock / 8) == 0) {   // this word begins a block
+              const int blk = j / (G::kBlock / 8);
+              const uint32_t b = (sc[x][blk / 4] >> (8 * (blk % 4))) & 0xFFu;
+              if constexpr (FMT == kNVFP4)
+                s2 = e4m3x2_to_f16x2(b * 0x0101u);
+              else
+                s2 = f16_power(static_cast<int>(b) - top + 12) * 0x10001u;
+            }
+            *reinterpret_cast<uint4*>(dst + (j >> 3) * (kKeys * 128) + (((j & 7) ^ (key_in & 7)) << 4)) =
+                make_uint4(mul2(e2m1x2_to_f16x2<0>(wd[x][j]), s2), mul2(e2m1x2_to_f16x2<1>(wd[x][j]), s2),
+                           mul2(e2m1x2_to_f16x2<2>(wd[x][j]), s2), mul2(e2m1x2_to_f16x2<3>(wd[x][j]), s2));
+          }
         }
         fence_async_shared();
         __syncwarp();
@@ -592,6 +600,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
         const int all_hi = a.causal ? w.s.len - w.s.nq + tok_a : w.s.len - 1;
         const int64_t all_lo = a.window > 0 ? static_cast<int64_t>(w.s.len) - w.s.nq + tok_b - a.window + 1 : 0;
 
+        // (the products of the tiles before are in O when a tile's scores have come)
+        auto scale_o = [&](float r) {
+#pragma unroll 1
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t o[16];
+            tmem_ld_x16(o_tmem + 16 * c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * r);
+            tmem_st_x16(o_tmem + 16 * c, o);
+          }
+        };
         for (int i = 0; i < tiles; ++i) {
           const uint32_t num = n + i;
           const int key0 = w.k.lo + (w.ta + i) * kKeys;
@@ -609,76 +629,79 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
             const float fc = FMT == kMXFP4 ? f * sm.kfac[num % kRing][c] : f;
             return fc < FLT_MIN ? FLT_MIN : fc;
           };
-          // 32 keys' scores (the loops over c stay rolled: this kernel's roles
-          // share an instruction cache that their code must fit)
-          auto load_scores = [&](int c, float(&x)[32]) {
-            uint32_t r[32];
-            tmem_ld_x32(s_tmem + 32 * c, r);
-            tmem_wait_ld();
+          auto mask = [&](int c, float(&x)[32]) {
+            const int from = lo - key0 - 32 * c, to = hi - key0 - 32 * c;
+            // keys from..to of the 32, and of the groups that are there
+            uint32_t keep = to < 0 ? 0u : to >= 31 ? ~0u : (2u << to) - 1u;
+            keep &= from <= 0 ? ~0u : from > 31 ? 0u : ~0u << from;
+            if (!((valid >> (2 * c)) & 1)) keep &= 0xFFFF0000u;
+            if (!((valid >> (2 * c + 1)) & 1)) keep &= 0x0000FFFFu;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(r[e]);
-            if (masked) {
-              const int from = lo - key0 - 32 * c, to = hi - key0 - 32 * c;
-              // keys from..to of the 32, and of the groups that are there
-              uint32_t keep = to < 0 ? 0u : to >= 31 ? ~0u : (2u << to) - 1u;
-              keep &= from <= 0 ? ~0u : from > 31 ? 0u : ~0u << from;
-              if (!((valid >> (2 * c)) & 1)) keep &= 0xFFFF0000u;
-              if (!((valid >> (2 * c + 1)) & 1)) keep &= 0x0000FFFFu;
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!((keep >> e) & 1)) x[e] = -INFINITY;
-            }
+            for (int e = 0; e < 32; ++e)
+              if (!((keep >> e) & 1)) x[e] = -INFINITY;
           };
-          // ---- the reference maximum moves only when passed by 2^8
-          float top = -INFINITY;
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            float x[32], t = -INFINITY;
-            load_scores(c, x);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) t = fmaxf(t, x[e]);
-            top = fmaxf(top, t * factor_of(c));
+          // MXFP4: V is held relative to a reference that this tile may raise
+          if constexpr (FMT == kMXFP4) {
+            const float vf = i > 0 ? sm.vfac[num % kRing] : 1.0f;
+            if (vf != 1.0f) scale_o(vf);
           }
-          const bool grow = top > m + 8.0f;
-          const float vf = FMT == kMXFP4 && i > 0 ? sm.vfac[num % kRing] : 1.0f;
-          if (__any_sync(0xFFFFFFFFu, grow || vf != 1.0f)) {
-            float r = 1.0f;
-            if (grow) {
-              r = ex2(m - top);
-              m = top;
-              l *= r;
-            }
-            if (i > 0) {
-              r *= vf;
+          // ---- one pass: a chunk's scores become weights of the reference
+          // maximum as it stands, which moves only when passed by 2^8 (p <= 2^8
+          // fits FP16); then O, and the tile's weights so far, are scaled
+          float2 sum = make_float2(0.0f, 0.0f);
+          auto weigh = [&](int c, uint32_t(&raw)[32]) {   // 32 keys
+            float x[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(raw[e]);
+            if (masked) mask(c, x);
+            const float fc = factor_of(c);
+            float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int e = 0; e < 32; ++e) t[e & 3] = fmaxf(t[e & 3], x[e]);
+            const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * fc;
+            const bool grow = top > m + 8.0f;
+            if (__any_sync(0xFFFFFFFFu, grow)) {
+              float r = 1.0f;
+              if (grow) {
+                r = ex2(m - top);
+                m = top;
+                l *= r;
+                sum.x *= r;
+                sum.y *= r;
+              }
+              if (i > 0) scale_o(r);
+              const __half2 rh = __float2half2_rn(r);   // (below FP16 it is 0, as the weights become)
 #pragma unroll 1
-              for (int c = 0; c < D / 16; ++c) {
-                uint32_t o[16];
-                tmem_ld_x16(o_tmem + 16 * c, o);
+              for (int c2 = 0; c2 < c; ++c2) {
+                uint32_t p[16];
+                tmem_ld_x16(s_tmem + 16 * c2, p);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * r);
-                tmem_st_x16(o_tmem + 16 * c, o);
+                for (int e = 0; e < 16; ++e) p[e] = mul2(p[e], reinterpret_cast<const uint32_t&>(rh));
+                tmem_st_x16(s_tmem + 16 * c2, p);
               }
             }
-          }
-          const float ref = m == -INFINITY ? 0.0f : m;
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            float x[32];
-            load_scores(c, x);
-            const float fc = factor_of(c);
+            const float ref = m == -INFINITY ? 0.0f : -m;
+            const float2 fc2 = make_float2(fc, fc), ref2 = make_float2(ref, ref);
             uint32_t p[16];
-            float l0 = 0.0f, l1 = 0.0f;
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const float p0 = ex2(fmaf(x[2 * e], fc, -ref)), p1 = ex2(fmaf(x[2 * e + 1], fc, -ref));
-              l0 += p0;
-              l1 += p1;
-              p[e] = pack_f16(p0, p1);
+              const float2 y = fma2(make_float2(x[2 * e], x[2 * e + 1]), fc2, ref2);
+              const float2 pe = make_float2(ex2(y.x), ex2(y.y));
+              sum = add2(sum, pe);
+              p[e] = pack_f16(pe.x, pe.y);
             }
-            l += l0 + l1;
             tmem_st_x16(s_tmem + 16 * c, p);
+          };
+          // (the loop stays rolled: this kernel's roles share an instruction cache)
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t x[32];
+            tmem_ld_x32(s_tmem + 32 * c, x);
+            tmem_wait_ld();
+            weigh(c, x);
           }
+          l += sum.x + sum.y;
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
