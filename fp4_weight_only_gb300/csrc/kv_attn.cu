@@ -323,12 +323,6 @@ __device__ __forceinline__ void pv_step(float (&o)[NB][K][4], const uint32_t (&p
   for (int nb = 0; nb < NB; ++nb) mma_f16(o[nb][i], a0, a1, a2, a3, p[nb][0], p[nb][1]);
 }
 
-// Weight of a partial result with maximum m and sum l when results meet at
-// maximum M (no key: none; a NaN sum stays one).
-__device__ __forceinline__ float weight_of(float m, float l, float M) {
-  return m == -INFINITY ? (l == 0.0f ? 0.0f : 1.0f) : ex2(m - M);
-}
-
 template <int E>
 __device__ __forceinline__ void load_row(const float* p, float (&v)[E]) {
   if constexpr (E == 4) {

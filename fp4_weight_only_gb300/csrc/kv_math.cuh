@@ -81,6 +81,12 @@ __device__ __forceinline__ int row_shift(float amax) {
   return amax == 0.0f ? 0 : min(139 - e, 127);
 }
 
+// Weight of a partial result with maximum m and sum l when results meet at
+// maximum M (no key: none; a NaN sum stays one).
+__device__ __forceinline__ float weight_of(float m, float l, float M) {
+  return m == -INFINITY ? (l == 0.0f ? 0.0f : 1.0f) : ex2(m - M);
+}
+
 // Waits for a phase of an mbarrier with the whole warp.  The loop is kept
 // short, because a kernel of many roles lives or dies by its instruction
 // cache: time and the abort flag are looked at every 1024 tries only.  A wait

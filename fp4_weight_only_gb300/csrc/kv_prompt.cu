@@ -42,6 +42,13 @@ constexpr int kRowTile = 128;     // rows of an MMA tile
 constexpr int kRows = 2 * kRowTile;
 constexpr int kVWarp = 8, kKWarp = 12, kMmaWarp = 14;
 constexpr int kThreads = 32 * 16;   // (warp 15 has no work)
+// What beginning and ending an item costs, in tiles (an item of a verified draft
+// takes 9 k cycles beside 1.9 k a tile), and the least a CTA gets: more than that,
+// so that every CTA with units of an item has a tile of it.
+#ifndef PIC
+#define PIC 4
+#endif
+constexpr int kItemCost = PIC, kMinUnits = 8;
 constexpr int kRing = 4;          // per-tile facts: written at most two tiles ahead of their last reader
 
 // ------------------------------------------------------------ work split
@@ -88,54 +95,62 @@ __device__ __forceinline__ Keys item_keys(const KvAttnArgs& a, const Seq& s, int
   return k;
 }
 
-// Tiles of a sequence over all its items; every lane of the warp calls it.
-__device__ __forceinline__ int64_t seq_tiles(const KvAttnArgs& a, int b, uint32_t* status) {
+// Units (tiles, and kItemCost an item) of a sequence over all its items; every
+// lane of the warp calls it.
+__device__ __forceinline__ int64_t seq_units(const KvAttnArgs& a, int b, uint32_t* status) {
   const Seq s = load_seq(a, b, status);
   int64_t sum = 0;
-  for (int rt = threadIdx.x & 31; rt < s.row_tiles; rt += 32) sum += item_keys(a, s, rt).tiles;
+  for (int rt = threadIdx.x & 31; rt < s.row_tiles; rt += 32) sum += item_keys(a, s, rt).tiles + kItemCost;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
   return sum * a.cache.heads;
 }
 
 __device__ __forceinline__ int64_t range_begin(int64_t total, int ctas, int64_t c) { return total * c / ctas; }
-__device__ __forceinline__ int cta_of_tile(int64_t total, int ctas, int64_t x) {
+// The CTA whose range holds unit x.
+__device__ __forceinline__ int cta_of(int64_t total, int ctas, int64_t x) {
   return static_cast<int>(((x + 1) * ctas + total - 1) / total) - 1;
 }
 
-// Items in order: sequence, row tile, head.
+// Walks the items of a CTA's range of units, in the order sequence, row tile,
+// head.  An item's tile 0 stands at its beginning, tile t > 0 kItemCost + t
+// after it.  Positions are relative to the range's beginning.
 struct Walk {
-  int64_t total, pos, end;
+  int64_t total, begin;   // units of the call; the range's first
   int ctas;
+  int span;               // the range's units
+  int at;                 // the item's first unit
   int b, rt, h;
   Seq s;
   Keys k;
-  int ta, tb;   // tiles of the item in this range
+  int ta, tb;             // tiles of the item in this range
 
-  __device__ __forceinline__ bool done() const { return pos >= end; }
+  __device__ __forceinline__ bool done() const { return at >= span; }
   __device__ __forceinline__ void cut() {
-    const int64_t left = end - pos;
-    tb = left < k.tiles - ta ? ta + static_cast<int>(left) : k.tiles;
+    const int below = span - at - kItemCost;   // tiles below the range's end
+    tb = below >= k.tiles ? k.tiles : below > ta ? below : ta + 1;
+  }
+  __device__ __forceinline__ void next_item(const KvAttnArgs& a, uint32_t* status) {
+    at += k.tiles + kItemCost;
+    if (done()) return;
+    if (++h == static_cast<int>(a.cache.heads)) {
+      h = 0;
+      if (++rt == s.row_tiles) {
+        rt = 0;
+        do {
+          s = load_seq(a, ++b, status);
+        } while (s.row_tiles == 0 && b + 1 < a.batch);
+      }
+      k = item_keys(a, s, rt);
+    }
+    ta = 0;
+    cut();
   }
   __device__ __forceinline__ void next(const KvAttnArgs& a, uint32_t* status) {
-    pos += tb - ta;
-    if (pos >= end) return;
-    if (tb == k.tiles) {
-      if (++h == static_cast<int>(a.cache.heads)) {
-        h = 0;
-        if (++rt == s.row_tiles) {
-          rt = 0;
-          do {
-            s = load_seq(a, ++b, status);
-          } while (s.row_tiles == 0 && b + 1 < a.batch);
-        }
-        k = item_keys(a, s, rt);
-      }
-      ta = 0;
-    } else {
-      ta = tb;
-    }
-    cut();
+    if (tb < k.tiles)
+      at = span;
+    else
+      next_item(a, status);
   }
 };
 
@@ -148,7 +163,7 @@ __device__ Walk find_range(const KvAttnArgs& a, int64_t* sh, uint32_t* status) {
   auto chunk = [&](int b0) {   // totals of the sequences b0.. into sh; returns their sum
     __syncthreads();
     for (int i = warp; i < kSeqChunk; i += kW) {
-      const int64_t t = b0 + i < a.batch ? seq_tiles(a, b0 + i, status) : 0;
+      const int64_t t = b0 + i < a.batch ? seq_units(a, b0 + i, status) : 0;
       if (lane == 0) sh[i] = t;
     }
     __syncthreads();
@@ -159,31 +174,34 @@ __device__ Walk find_range(const KvAttnArgs& a, int64_t* sh, uint32_t* status) {
   };
   Walk w{};
   for (int b0 = 0; b0 < a.batch; b0 += kSeqChunk) w.total += chunk(b0);
-  w.ctas = w.total < gridDim.x ? static_cast<int>(w.total) : static_cast<int>(gridDim.x);
-  if (static_cast<int>(blockIdx.x) >= w.ctas) return w;
-  w.pos = range_begin(w.total, w.ctas, blockIdx.x);
-  w.end = range_begin(w.total, w.ctas, blockIdx.x + 1);
+  w.ctas = w.total >= static_cast<int64_t>(gridDim.x) * kMinUnits ? static_cast<int>(gridDim.x)
+           : w.total >= kMinUnits                                 ? static_cast<int>(w.total) / kMinUnits
+                                                                  : w.total > 0;
+  if (static_cast<int>(blockIdx.x) >= w.ctas) return w;   // (an empty range: done)
+  w.begin = range_begin(w.total, w.ctas, blockIdx.x);
+  w.span = static_cast<int>(range_begin(w.total, w.ctas, blockIdx.x + 1) - w.begin);
   int64_t before = 0;
   int b0 = 0;
   for (;; b0 += kSeqChunk) {
     const int64_t sum = a.batch > kSeqChunk ? chunk(b0) : w.total;
-    if (before + sum > w.pos) break;
+    if (before + sum > w.begin) break;
     before += sum;
   }
   w.b = b0;
-  while (before + sh[w.b - b0] <= w.pos) before += sh[w.b++ - b0];
+  while (before + sh[w.b - b0] <= w.begin) before += sh[w.b++ - b0];
   w.s = load_seq(a, w.b, status);
   // the row tile: prefix sums of 32 at a time
   for (int rt0 = 0;; rt0 += 32) {
     const int64_t mine =
-        rt0 + lane < w.s.row_tiles ? static_cast<int64_t>(item_keys(a, w.s, rt0 + lane).tiles) * a.cache.heads : 0;
+        rt0 + lane < w.s.row_tiles ? static_cast<int64_t>(item_keys(a, w.s, rt0 + lane).tiles + kItemCost) * a.cache.heads
+                                   : 0;
     int64_t pre = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t v = __shfl_up_sync(0xFFFFFFFFu, pre, o);
       if (lane >= o) pre += v;
     }
-    const unsigned over = __ballot_sync(0xFFFFFFFFu, before + pre > w.pos);
+    const unsigned over = __ballot_sync(0xFFFFFFFFu, before + pre > w.begin);
     if (over) {
       const int l = __ffs(over) - 1;
       w.rt = rt0 + l;
@@ -193,10 +211,15 @@ __device__ Walk find_range(const KvAttnArgs& a, int64_t* sh, uint32_t* status) {
     before += __shfl_sync(0xFFFFFFFFu, pre, 31);
   }
   w.k = item_keys(a, w.s, w.rt);
-  const int64_t in = w.pos - before;
-  w.h = static_cast<int>(in / w.k.tiles);
-  w.ta = static_cast<int>(in - static_cast<int64_t>(w.h) * w.k.tiles);
-  w.cut();
+  const int units = w.k.tiles + kItemCost;
+  w.h = static_cast<int>((w.begin - before) / units);
+  const int in = static_cast<int>(w.begin - before - static_cast<int64_t>(w.h) * units);
+  w.at = -in;
+  w.ta = in == 0 ? 0 : in <= kItemCost ? 1 : in - kItemCost;   // the first tile at or past the beginning
+  if (w.ta < w.k.tiles)
+    w.cut();
+  else   // the range begins between an item's only tile and the next item
+    w.next_item(a, status);
   return w;
 }
 
@@ -209,7 +232,7 @@ struct Smem {
   uint64_t qfull[2], sfull[2], pfull[2], ofull[2], kfull[2], kfree[2], vfull[2], vfree[2], fin;
   int64_t scan[kSeqChunk];
   float kfac[kRing][4];       // MXFP4: factor of the scores of 32 keys
-  float vfac[kRing];          // MXFP4: factor of O before this tile
+  float m1[kRowTile], l1[kRowTile];   // what the second half of an item's keys leaves
   uint32_t valid[kRing][4];   // of 32 keys: bit 0, 1: the 16-key group's page is in the cache
   int vtop;                   // MXFP4: largest V scale of the tile
   float vscale[kRing];        // MXFP4: what O needs if the item ends with this tile
@@ -297,42 +320,70 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
     for (; !w.done(); w.next(a, status)) {
       const int tiles = w.tb - w.ta;
       const int rows = min(w.s.tokens, w.s.nq - w.rt * w.s.tokens) * a.group;
-      const int nt = rows > kRowTile ? 2 : 1;
-      for (int q = 0; q < nt; ++q) {
-        wait(&sm.qfull[q], items[q] & 1);
-        if (q == 0) wait(&sm.kfull[n & 1], (n >> 1) & 1);
-        tc_fence_after();
-        scores(q, n);
-      }
-      commit(&sm.kfree[n & 1]);
-      for (int i = 0; i < tiles; ++i) {
-        const uint32_t num = n + i;
-        for (int q = 0; q < nt; ++q) {
-          wait(&sm.pfull[q], ptiles[q]++ & 1);
-          if (q == 0) wait(&sm.vfull[num & 1], (num >> 1) & 1);
-          tc_fence_after();
-          if (elect_one()) {
-            const uint32_t va = smem_u32(sm.v[num & 1]);
+      // tile `num` for row tile (or half) q; `first`: it begins O_q, `last`: it ends it
+      auto weigh = [&](int q, uint32_t num, bool first, bool last) {
+        if (elect_one()) {
+          const uint32_t va = smem_u32(sm.v[num & 1]);
 #pragma unroll
-            for (int j = 0; j < kKeys / 16; ++j)
-              mma_ts_f16(tmem + kO + q * D, tmem + kS + q * kKeys + j * 8,
-                         smem_desc_kmajor_sw128(va + (j >> 2) * (D * 128)) + (j & 3) * 2, kIdescO, i > 0 || j > 0);
-          }
-          __syncwarp();
-          if (i + 1 < tiles) {
-            if (q == 0) {
-              wait(&sm.kfull[(num + 1) & 1], ((num + 1) >> 1) & 1);
-              tc_fence_after();
-            }
-            scores(q, num + 1);
-          } else {
-            commit(&sm.ofull[q]);
-          }
+          for (int j = 0; j < kKeys / 16; ++j)
+            mma_ts_f16(tmem + kO + q * D, tmem + kS + q * kKeys + j * 8,
+                       smem_desc_kmajor_sw128(va + (j >> 2) * (D * 128)) + (j & 3) * 2, kIdescO, !first || j > 0);
+          if (last) mma_commit(smem_u32(&sm.ofull[q]));
         }
-        commit(&sm.vfree[num & 1]);
-        if (i + 1 < tiles) commit(&sm.kfree[(num + 1) & 1]);
+        __syncwarp();
+      };
+      auto await_p = [&](int q) { wait(&sm.pfull[q], ptiles[q]++ & 1); };
+      auto await_k = [&](uint32_t num) { wait(&sm.kfull[num & 1], (num >> 1) & 1); };
+      auto await_v = [&](uint32_t num) { wait(&sm.vfull[num & 1], (num >> 1) & 1); };
+      if (rows > kRowTile) {
+        // two row tiles, each of which meets every key tile
+        await_k(n);
+        for (int q = 0; q < 2; ++q) {
+          wait(&sm.qfull[q], items[q]++ & 1);
+          tc_fence_after();
+          scores(q, n);
+        }
+        commit(&sm.kfree[n & 1]);
+        for (int i = 0; i < tiles; ++i) {
+          const uint32_t num = n + i;
+          for (int q = 0; q < 2; ++q) {
+            await_p(q);
+            if (q == 0) await_v(num);
+            tc_fence_after();
+            weigh(q, num, i == 0, i + 1 == tiles);
+            if (i + 1 < tiles) {
+              if (q == 0) {
+                await_k(num + 1);
+                tc_fence_after();
+              }
+              scores(q, num + 1);
+            }
+          }
+          commit(&sm.vfree[num & 1]);
+          if (i + 1 < tiles) commit(&sm.kfree[(num + 1) & 1]);
+        }
+      } else {
+        // one row tile: its even and its odd key tiles as two chains
+        auto begin = [&](int q, uint32_t num) {
+          await_k(num);
+          tc_fence_after();
+          scores(q, num);
+          commit(&sm.kfree[num & 1]);
+        };
+        for (int q = 0; q < min(2, tiles); ++q) {
+          wait(&sm.qfull[q], items[q]++ & 1);
+          begin(q, n + q);
+        }
+        for (int i = 0; i < tiles; ++i) {
+          const uint32_t num = n + i;
+          await_p(i & 1);
+          await_v(num);
+          tc_fence_after();
+          weigh(i & 1, num, i < 2, i + 2 >= tiles);
+          commit(&sm.vfree[num & 1]);
+          if (i + 2 < tiles) begin(i & 1, num + 2);
+        }
       }
-      for (int q = 0; q < nt; ++q) ++items[q];
       n += tiles;
     }
     commit(&sm.fin);
@@ -396,7 +447,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
           const int t = max(vref, sm.vtop);
           asm volatile("bar.sync 2, 128;" ::: "memory");
           if (warp == kVWarp && lane == 0) {
-            sm.vfac[num % kRing] = t == vref ? 1.0f : ex2(static_cast<float>(vref - t));
             sm.vscale[num % kRing] = ldexpf(1.0f, t - 127 - 12);
           }
           vref = t;
@@ -540,14 +590,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
       const int tok0 = w.rt * w.s.tokens;
       const int rows = min(w.s.tokens, w.s.nq - tok0) * a.group;
       const bool whole = tiles == w.k.tiles;
-      const int row = q * kRowTile + row_in;
+      // one row tile: both groups take it, the second its odd key tiles
+      const bool one = rows <= kRowTile;
+      const bool works = q == 0 || !one || tiles > 1, puts = q == 0 || !one;
+      const int tile_row = one ? 0 : q * kRowTile;
+      const int row = tile_row + row_in;
       const bool mine = row < rows;
       const int tok = tok0 + min(row, rows - 1) / a.group;   // (a row past the last masks like it)
       const int64_t head = static_cast<int64_t>(w.h) * a.group + (mine ? row % a.group : 0);
       const float gv = a.cache.scales ? a.cache.scales[a.cache.heads + w.h] : 1.0f;
       float m = -INFINITY, l = 0.0f;
       float vs = 1.0f;
-      if (q * kRowTile < rows) {
+      if (works) {
         // ---- the row to FP16, swizzled; the sign of the scale goes with it
         float f;
         {
@@ -596,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
         const int hi = a.causal ? w.s.len - w.s.nq + tok : w.s.len - 1;
         const int64_t first = a.window > 0 ? static_cast<int64_t>(hi) - a.window + 1 : 0;
         const int lo = first > 0 ? static_cast<int>(first) : 0;
-        const int tok_a = tok0 + q * kRowTile / a.group, tok_b = tok0 + (min(rows, (q + 1) * kRowTile) - 1) / a.group;
+        const int tok_a = tok0 + tile_row / a.group, tok_b = tok0 + (min(rows, tile_row + kRowTile) - 1) / a.group;
         const int all_hi = a.causal ? w.s.len - w.s.nq + tok_a : w.s.len - 1;
         const int64_t all_lo = a.window > 0 ? static_cast<int64_t>(w.s.len) - w.s.nq + tok_b - a.window + 1 : 0;
 
@@ -612,16 +666,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
             tmem_st_x16(o_tmem + 16 * c, o);
           }
         };
-        for (int i = 0; i < tiles; ++i) {
+        const int first_tile = one ? q : 0;
+#pragma unroll 1
+        for (int i = first_tile; i < tiles; i += one ? 2 : 1) {
           const uint32_t num = n + i;
           const int key0 = w.k.lo + (w.ta + i) * kKeys;
           wait(&sm.sfull[q], my_tiles++ & 1);
-          if constexpr (FMT == kMXFP4) wait(&sm.vfull[num & 1], (num >> 1) & 1);   // vfac, vscale
+          if constexpr (FMT == kMXFP4) wait(&sm.vfull[num & 1], (num >> 1) & 1);   // vscale
           tc_fence_after();
           uint32_t valid = 0;
 #pragma unroll
           for (int c = 0; c < 4; ++c) valid |= sm.valid[num % kRing][c] << (2 * c);
-          if constexpr (FMT == kMXFP4) vs = sm.vscale[num % kRing];
           const bool masked = valid != 0xFFu || key0 + kKeys - 1 > all_hi || key0 < all_lo;
           // factor of 32 keys' scores; not zero, so that a masked score stays
           // -inf (2^-126 of a score is nothing)
@@ -640,10 +695,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
             for (int e = 0; e < 32; ++e)
               if (!((keep >> e) & 1)) x[e] = -INFINITY;
           };
-          // MXFP4: V is held relative to a reference that this tile may raise
+          // MXFP4: V is held relative to a reference that has risen since this
+          // chain's last tile, perhaps
           if constexpr (FMT == kMXFP4) {
-            const float vf = i > 0 ? sm.vfac[num % kRing] : 1.0f;
-            if (vf != 1.0f) scale_o(vf);
+            const float now = sm.vscale[num % kRing];
+            if (i > first_tile && now != vs) scale_o(vs / now);   // (powers of two)
+            vs = now;
           }
           // ---- one pass: a chunk's scores become weights of the reference
           // maximum as it stands, which moves only when passed by 2^8 (p <= 2^8
@@ -669,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                 sum.x *= r;
                 sum.y *= r;
               }
-              if (i > 0) scale_o(r);
+              if (i > first_tile) scale_o(r);
               const __half2 rh = __float2half2_rn(r);   // (below FP16 it is 0, as the weights become)
 #pragma unroll 1
               for (int c2 = 0; c2 < c; ++c2) {
@@ -711,13 +768,46 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
         tc_fence_after();
       }
       n += tiles;
+      // ---- the halves of one row tile's keys meet, where the queries were
+      // (every product with them is done when both groups have seen ofull)
+      float4* other = reinterpret_cast<float4*>(&sm.q[0][0][0]);   // [D / 4][128 rows]
+      float w0 = vs, w1 = 0.0f;
+      const bool meet = one && tiles > 1;
+      if (meet) {
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (q == 1) {
+#pragma unroll 1
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t r[16];
+            tmem_ld_x16(o_tmem + 16 * c, r);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              other[(4 * c + e) * kRowTile + row_in] =
+                  make_float4(__uint_as_float(r[4 * e]) * vs, __uint_as_float(r[4 * e + 1]) * vs,
+                              __uint_as_float(r[4 * e + 2]) * vs, __uint_as_float(r[4 * e + 3]) * vs);
+          }
+          tc_fence_before();
+          sm.m1[row_in] = m;
+          sm.l1[row_in] = l;
+        }
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (q == 0) {
+          const float m1 = sm.m1[row_in], l1 = sm.l1[row_in], M = fmaxf(m, m1);
+          const float f0 = weight_of(m, l, M);
+          w1 = weight_of(m1, l1, M);
+          w0 *= f0;
+          l = l * f0 + l1 * w1;
+          m = M;
+        }
+      }
       // ---- O of the row: the output, or a partial
       const int64_t out_row = w.s.q0 + static_cast<int64_t>(tok);
-      auto store_out = [&](int c, const float(&x)[32], float inv) {   // 32 dimensions from 32 c on
+      auto store_out = [&](int c, const float(&x)[16], float inv) {   // 16 dimensions from 16 c on
         uint16_t* dst = static_cast<uint16_t*>(a.out.data) + out_row * a.out.token_stride + head * a.out.head_stride +
-                        32 * c;
+                        16 * c;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+        for (int e = 0; e < 2; ++e)
           reinterpret_cast<uint4*>(dst)[e] =
               make_uint4(pack2(x[8 * e] * inv, x[8 * e + 1] * inv, a.bf16), pack2(x[8 * e + 2] * inv, x[8 * e + 3] * inv, a.bf16),
                          pack2(x[8 * e + 4] * inv, x[8 * e + 5] * inv, a.bf16),
@@ -729,23 +819,30 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
               L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
       };
       float* slot = partials + (2 * static_cast<size_t>(blockIdx.x) + (w.ta == 0 ? 1 : 0)) * partial_floats<D>();
-      if (q * kRowTile < rows) {
-        const float inv = l == 0.0f ? 0.0f : vs * gv / l;   // no key: zeros
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t r[32];
-          float x[32];
-          tmem_ld_x32(o_tmem + 32 * c, r);
+      if (puts) {
+        const float inv = l == 0.0f ? 0.0f : gv / l;   // no key: zeros
+#pragma unroll 1
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t r[16];
+          float x[16];
+          tmem_ld_x16(o_tmem + 16 * c, r);
           tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(r[e]);
+          for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(r[e]) * w0;
+          if (meet) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float4 y = other[(4 * c + e) * kRowTile + row_in];
+              x[4 * e] += w1 * y.x, x[4 * e + 1] += w1 * y.y, x[4 * e + 2] += w1 * y.z, x[4 * e + 3] += w1 * y.w;
+            }
+          }
           if (whole) {
             if (mine) store_out(c, x, inv);
           } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              reinterpret_cast<float4*>(slot)[(8 * c + e) * kRows + row] =
-                  make_float4(x[4 * e] * vs, x[4 * e + 1] * vs, x[4 * e + 2] * vs, x[4 * e + 3] * vs);
+            for (int e = 0; e < 4; ++e)
+              reinterpret_cast<float4*>(slot)[(4 * c + e) * kRows + row] =
+                  make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
           }
         }
         if (whole) {
@@ -757,43 +854,51 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
         tc_fence_before();
       }
       if (!whole) {
-        const int64_t item0 = w.pos - w.ta;
-        const int c0 = cta_of_tile(w.total, w.ctas, item0), c1 = cta_of_tile(w.total, w.ctas, item0 + w.k.tiles - 1);
+        const int64_t item0 = w.begin + w.at;
+        const int c0 = cta_of(w.total, w.ctas, item0);
+        const int c1 = cta_of(w.total, w.ctas, item0 + (w.k.tiles > 1 ? w.k.tiles - 1 + kItemCost : 0));
         asm volatile("bar.sync 1, 256;" ::: "memory");
         if (tid == 0) sm.last = atomic_add_acq_rel_gpu(&counters[c0], 1u) == static_cast<uint32_t>(c1 - c0);
         asm volatile("bar.sync 1, 256;" ::: "memory");
         if (sm.last) {
           if (tid == 0) counters[c0] = 0;   // every CTA of the item has arrived
-          if (mine) {
+          if (mine && puts) {
             auto part = [&](int c) { return partials + (2 * static_cast<size_t>(c) + (c == c0)) * partial_floats<D>(); };
             float M = -INFINITY, L = 0.0f;
+#pragma unroll 4
             for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(part(c) + kRows * D + row));
-            auto weight = [&](int c, float lc) {
-              const float mc = __ldcg(part(c) + kRows * D + row);
-              return mc == -INFINITY ? (lc == 0.0f ? 0.0f : 1.0f) : ex2(mc - M);
-            };
-            for (int c = c0; c <= c1; ++c) {
+            auto weight = [&](int c, float* sum) {
               const float lc = __ldcg(part(c) + kRows * D + kRows + row);
-              L += weight(c, lc) * lc;
-            }
+              const float f = weight_of(__ldcg(part(c) + kRows * D + row), lc, M);
+              if (sum) *sum += f * lc;
+              return f;
+            };
+            // (mostly two CTAs share an item: their weights stay in registers)
+            const float f0 = weight(c0, &L), f1 = weight(c0 + 1, &L);
+            for (int c = c0 + 2; c <= c1; ++c) weight(c, &L);
             const float inv2 = L == 0.0f ? 0.0f : gv / L;
-            for (int d = 0; d < D / 32; ++d) {
-              float x[32] = {};
-              for (int c = c0; c <= c1; ++c) {
-                const float wt = weight(c, __ldcg(part(c) + kRows * D + kRows + row));
+#pragma unroll 2
+            for (int d = 0; d < D / 16; ++d) {
+              float x[16] = {};
+              auto add = [&](int c, float f) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const float4 v = __ldcg(reinterpret_cast<const float4*>(part(c)) + (8 * d + e) * kRows + row);
-                  x[4 * e] += wt * v.x, x[4 * e + 1] += wt * v.y, x[4 * e + 2] += wt * v.z, x[4 * e + 3] += wt * v.w;
+                for (int e = 0; e < 4; ++e) {
+                  const float4 v = __ldcg(reinterpret_cast<const float4*>(part(c)) + (4 * d + e) * kRows + row);
+                  x[4 * e] += f * v.x, x[4 * e + 1] += f * v.y, x[4 * e + 2] += f * v.z, x[4 * e + 3] += f * v.w;
                 }
-              }
+              };
+              add(c0, f0);
+              add(c0 + 1, f1);
+#pragma unroll 1
+              for (int c = c0 + 2; c <= c1; ++c) add(c, weight(c, nullptr));
               store_out(d, x, inv2);
             }
             store_lse(M, L);
           }
         }
-        asm volatile("bar.sync 1, 256;" ::: "memory");   // sm.last may be written again
       }
+      // sm.last, and queries where the halves met, may be written again
+      if (!whole || meet) asm volatile("bar.sync 1, 256;" ::: "memory");
     }
   }
   tc_fence_before();
