@@ -1,5 +1,9 @@
 // The 4-bit K/V cache: quantising rows as they are written, and reading them
-// back.  Both are one pass over the rows with nothing kept on chip.
+// back.  Both are one pass over the rows with nothing kept on chip, and what
+// bounds them is memory: 8 heads of 128, 131071 tokens read in 113 us
+// (6.1 TB/s), 8192 written and read back in 19.1 us (4.5 TB/s, two launches).
+// Below some thousand tokens they are a launch: 1501 tokens read in 2.9 us, one
+// written and read back in 3.8.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -205,6 +209,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(KvCacheArgs c, KvRo
 
 // A thread decodes 8 codes (4 bytes in, 16 out) of K and of V, for kReadRows
 // rows a pass apart: their loads are in flight together.
+// (131071 tokens: 113 us with 2 and with 4, 135 with 1; 1501 tokens: 2.9, 3.1, 2.7.)
 constexpr int kReadRows = 2;
 
 template <int D, int FMT, bool BF16>

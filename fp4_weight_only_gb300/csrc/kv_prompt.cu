@@ -24,6 +24,13 @@
 //
 // The key tiles of all items are cut into equal ranges as in kv_attn.cu; an
 // item cut between CTAs leaves FP32 partials that the last arriver adds.
+//
+// Measured: 4096 new tokens behind 12288, 64 query heads of 128 over 8 NVFP4
+// heads, 1.55 ms, 1.24 PFLOP/s (65 % of a cuBLAS product's rate): a softmax
+// warpgroup's pass over 128 x 128 scores (about 2300 cycles beside the other's)
+// is the longest stage, the two MMAs of both row tiles take about 1530.  Five
+// ragged pieces of 3 to 1100 tokens with a window of 1024, heads of 64, 63 us:
+// an item's beginning and end (8 to 10 k cycles) next to 13 tiles.
 #include <cfloat>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -45,10 +52,7 @@ constexpr int kThreads = 32 * 16;   // (warp 15 has no work)
 // What beginning and ending an item costs, in tiles (an item of a verified draft
 // takes 9 k cycles beside 1.9 k a tile), and the least a CTA gets: more than that,
 // so that every CTA with units of an item has a tile of it.
-#ifndef PIC
-#define PIC 4
-#endif
-constexpr int kItemCost = PIC, kMinUnits = 8;
+constexpr int kItemCost = 4, kMinUnits = 8;
 constexpr int kRing = 4;          // per-tile facts: written at most two tiles ahead of their last reader
 
 // ------------------------------------------------------------ work split
@@ -873,24 +877,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
               if (sum) *sum += f * lc;
               return f;
             };
-            // (mostly two CTAs share an item: their weights stay in registers)
-            const float f0 = weight(c0, &L), f1 = weight(c0 + 1, &L);
-            for (int c = c0 + 2; c <= c1; ++c) weight(c, &L);
-            const float inv2 = L == 0.0f ? 0.0f : gv / L;
+            // the row's weights stay where the queries were, as many as fit there
+            constexpr int kKept = sizeof(sm.q) / (kRows * sizeof(float));
+            float* kept = reinterpret_cast<float*>(&sm.q[0][0][0]) + row;
 #pragma unroll 2
+            for (int c = c0; c <= c1; ++c) {
+              const float f = weight(c, &L);
+              if (c - c0 < kKept) kept[(c - c0) * kRows] = f;
+            }
+            const float inv2 = L == 0.0f ? 0.0f : gv / L;
+#pragma unroll 1
             for (int d = 0; d < D / 16; ++d) {
               float x[16] = {};
-              auto add = [&](int c, float f) {
+#pragma unroll 4
+              for (int c = c0; c <= c1; ++c) {
+                const float f = c - c0 < kKept ? kept[(c - c0) * kRows] : weight(c, nullptr);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                   const float4 v = __ldcg(reinterpret_cast<const float4*>(part(c)) + (4 * d + e) * kRows + row);
                   x[4 * e] += f * v.x, x[4 * e + 1] += f * v.y, x[4 * e + 2] += f * v.z, x[4 * e + 3] += f * v.w;
                 }
-              };
-              add(c0, f0);
-              add(c0 + 1, f1);
-#pragma unroll 1
-              for (int c = c0 + 2; c <= c1; ++c) add(c, weight(c, nullptr));
+              }
               store_out(d, x, inv2);
             }
             store_lse(M, L);

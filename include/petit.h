@@ -372,9 +372,11 @@ petit_status_t petit_kv_read(const petit_kv_cache_t* cache, const int64_t* slots
  *     x_j = scale * q . k_j,  out = sum_j softmax(x)_j v_j,
  *     lse = log(sum_j exp(x_j))        (natural logarithm, FP32)
  * A query that sees no key (len = 0, or p < 0) gets out = 0 and lse = -inf.
- * Products are FP16 by FP16 with FP32 sums (q by a power of two per row, the
- * softmax's weights rounded to 11 bits); scores, the softmax's maximum and
- * sum, and the output's sums are FP32.
+ * Products are FP16 by FP16 with FP32 sums: q takes a power of two per row
+ * (exact but for elements 2^26 below the row's largest), the softmax's weights
+ * are rounded to 11 bits, and values of an MXFP4 cache lose bits only where
+ * their scale lies 2^32 or more below the largest of the keys around them.
+ * Scores, the softmax's maximum and sum, and the output's sums are FP32.
  *
  * A length past max_pages * page_size, a page outside the cache and query
  * offsets outside 0..total_q are recorded as PETIT_ERR_BOUNDS in the
@@ -409,7 +411,10 @@ size_t petit_kv_attention_workspace_bytes(int32_t num_kv_heads, int32_t head_dim
 
 /* Runs it.  Nothing about the sequences is read on the host, so a captured
  * graph follows changed lengths, tables and offsets.  Errors: INVALID_ARG,
- * UNSUPPORTED_SHAPE, MISALIGNED, WORKSPACE, ARCH, CUDA. */
+ * UNSUPPORTED_SHAPE (cache geometry, batch past 2^20, total_q or max_q past
+ * 2^24, more than 1024 query heads a K/V head, total_q * num_q_heads >=
+ * 2^31 - 64, max_pages * page_size past 2^30), MISALIGNED, WORKSPACE, ARCH,
+ * CUDA. */
 petit_status_t petit_kv_attention(const petit_kv_cache_t* cache, const petit_kv_attention_t* args,
                                   void* workspace, size_t workspace_bytes, petit_stream_t stream);
 
