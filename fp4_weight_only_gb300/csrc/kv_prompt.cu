@@ -26,7 +26,7 @@
 // item cut between CTAs leaves FP32 partials that the last arriver adds.
 //
 // Measured: 4096 new tokens behind 12288, 64 query heads of 128 over 8 NVFP4
-// heads, 1.55 ms, 1.24 PFLOP/s (65 % of a cuBLAS product's rate): a softmax
+// heads, 1.53 ms, 1.25 PFLOP/s (65 % of a cuBLAS product's rate): a softmax
 // warpgroup's pass over 128 x 128 scores (about 2300 cycles beside the other's)
 // is the longest stage, the two MMAs of both row tiles take about 1530.  Five
 // ragged pieces of 3 to 1100 tokens with a window of 1024, heads of 64, 63 us:
@@ -49,10 +49,17 @@ constexpr int kRowTile = 128;     // rows of an MMA tile
 constexpr int kRows = 2 * kRowTile;
 constexpr int kVWarp = 8, kKWarp = 12, kMmaWarp = 14;
 constexpr int kThreads = 32 * 16;   // (warp 15 has no work)
-// What beginning and ending an item costs, in tiles (an item of a verified draft
-// takes 9 k cycles beside 1.9 k a tile), and the least a CTA gets: more than that,
-// so that every CTA with units of an item has a tile of it.
-constexpr int kItemCost = 4, kMinUnits = 8;
+// The split counts units: an item's tiles, and its cost.
+//  - Many items (more than half the CTAs): beginning and ending one costs some
+//    9 k cycles beside 2 to 4 k a tile, so it counts kItemCost tiles, and a CTA
+//    gets kMinUnits at least: more than the cost, so that every CTA with units
+//    of an item has a tile of it.  (24 drafts: 51 us, 79 without a cost.)
+//  - Few items: each is cut into equal pieces of kFewTiles tiles or more, none
+//    of which begins a second item; short ones into pairs of tiles.  64 query
+//    heads over 8: 8 tokens at 2000 take 20.5 us (as above: 26.5), 100 at 6000
+//    37.9 (40.2), 200 of a new prompt 22 (31), 64 of two sequences at 4000 53
+//    (49).
+constexpr int kItemCost = 4, kMinUnits = 8, kFewTiles = 4;
 constexpr int kRing = 4;          // per-tile facts: written at most two tiles ahead of their last reader
 
 // ------------------------------------------------------------ work split
@@ -99,15 +106,17 @@ __device__ __forceinline__ Keys item_keys(const KvAttnArgs& a, const Seq& s, int
   return k;
 }
 
-// Units (tiles, and kItemCost an item) of a sequence over all its items; every
-// lane of the warp calls it.
-__device__ __forceinline__ int64_t seq_units(const KvAttnArgs& a, int b, uint32_t* status) {
+// Tiles and items: of a sequence (every lane of the warp calls this), or more.
+struct Work {
+  int64_t tiles, items;
+};
+__device__ __forceinline__ Work seq_work(const KvAttnArgs& a, int b, uint32_t* status) {
   const Seq s = load_seq(a, b, status);
   int64_t sum = 0;
-  for (int rt = threadIdx.x & 31; rt < s.row_tiles; rt += 32) sum += item_keys(a, s, rt).tiles + kItemCost;
+  for (int rt = threadIdx.x & 31; rt < s.row_tiles; rt += 32) sum += item_keys(a, s, rt).tiles;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-  return sum * a.cache.heads;
+  return {sum * a.cache.heads, static_cast<int64_t>(s.row_tiles) * a.cache.heads};
 }
 
 __device__ __forceinline__ int64_t range_begin(int64_t total, int ctas, int64_t c) { return total * c / ctas; }
@@ -117,11 +126,12 @@ __device__ __forceinline__ int cta_of(int64_t total, int ctas, int64_t x) {
 }
 
 // Walks the items of a CTA's range of units, in the order sequence, row tile,
-// head.  An item's tile 0 stands at its beginning, tile t > 0 kItemCost + t
-// after it.  Positions are relative to the range's beginning.
+// head.  An item's tile 0 stands at its beginning, tile t > 0 cost + t after
+// it.  Positions are relative to the range's beginning.
 struct Walk {
   int64_t total, begin;   // units of the call; the range's first
   int ctas;
+  int cost;               // of an item
   int span;               // the range's units
   int at;                 // the item's first unit
   int b, rt, h;
@@ -131,11 +141,11 @@ struct Walk {
 
   __device__ __forceinline__ bool done() const { return at >= span; }
   __device__ __forceinline__ void cut() {
-    const int below = span - at - kItemCost;   // tiles below the range's end
+    const int below = span - at - cost;   // tiles below the range's end
     tb = below >= k.tiles ? k.tiles : below > ta ? below : ta + 1;
   }
   __device__ __forceinline__ void next_item(const KvAttnArgs& a, uint32_t* status) {
-    at += k.tiles + kItemCost;
+    at += k.tiles + cost;
     if (done()) return;
     if (++h == static_cast<int>(a.cache.heads)) {
       h = 0;
@@ -161,43 +171,62 @@ struct Walk {
 constexpr int kSeqChunk = 64;
 
 // Every thread of the CTA calls this; sh holds kSeqChunk values.
-__device__ Walk find_range(const KvAttnArgs& a, int64_t* sh, uint32_t* status) {
+__device__ Walk find_range(const KvAttnArgs& a, Work* sh, uint32_t* status) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kW = kThreads / 32;
-  auto chunk = [&](int b0) {   // totals of the sequences b0.. into sh; returns their sum
+  auto chunk = [&](int b0) {   // the work of the sequences b0.. into sh; returns their sum
     __syncthreads();
     for (int i = warp; i < kSeqChunk; i += kW) {
-      const int64_t t = b0 + i < a.batch ? seq_units(a, b0 + i, status) : 0;
+      const Work t = b0 + i < a.batch ? seq_work(a, b0 + i, status) : Work{0, 0};
       if (lane == 0) sh[i] = t;
     }
     __syncthreads();
-    int64_t sum = sh[lane] + sh[lane + 32];
+    Work sum = {sh[lane].tiles + sh[lane + 32].tiles, sh[lane].items + sh[lane + 32].items};
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    for (int o = 16; o > 0; o >>= 1) {
+      sum.tiles += __shfl_xor_sync(0xFFFFFFFFu, sum.tiles, o);
+      sum.items += __shfl_xor_sync(0xFFFFFFFFu, sum.items, o);
+    }
     return sum;
   };
   Walk w{};
-  for (int b0 = 0; b0 < a.batch; b0 += kSeqChunk) w.total += chunk(b0);
-  w.ctas = w.total >= static_cast<int64_t>(gridDim.x) * kMinUnits ? static_cast<int>(gridDim.x)
-           : w.total >= kMinUnits                                 ? static_cast<int>(w.total) / kMinUnits
-                                                                  : w.total > 0;
+  Work all = {0, 0};
+  for (int b0 = 0; b0 < a.batch; b0 += kSeqChunk) {
+    const Work sum = chunk(b0);
+    all.tiles += sum.tiles;
+    all.items += sum.items;
+  }
+  const int grid = static_cast<int>(gridDim.x);
+  auto units = [&](const Work& x) { return x.tiles + w.cost * x.items; };
+  if (2 * all.items <= grid) {
+    const int items = static_cast<int>(all.items);
+    const int64_t pieces = items == 0 ? 0 : all.tiles / (items * kFewTiles);
+    w.cost = 0;
+    w.total = units(all);
+    w.ctas = pieces >= 2 ? items * static_cast<int>(pieces < grid / items ? pieces : grid / items)
+                         : static_cast<int>((all.tiles + 1) / 2 < grid ? (all.tiles + 1) / 2 : grid);
+  } else {
+    w.cost = kItemCost;
+    w.total = units(all);
+    w.ctas = w.total >= static_cast<int64_t>(grid) * kMinUnits ? grid : max(static_cast<int>(w.total) / kMinUnits, 1);
+  }
   if (static_cast<int>(blockIdx.x) >= w.ctas) return w;   // (an empty range: done)
   w.begin = range_begin(w.total, w.ctas, blockIdx.x);
   w.span = static_cast<int>(range_begin(w.total, w.ctas, blockIdx.x + 1) - w.begin);
   int64_t before = 0;
   int b0 = 0;
   for (;; b0 += kSeqChunk) {
-    const int64_t sum = a.batch > kSeqChunk ? chunk(b0) : w.total;
+    const int64_t sum = a.batch > kSeqChunk ? units(chunk(b0)) : w.total;
     if (before + sum > w.begin) break;
     before += sum;
   }
   w.b = b0;
-  while (before + sh[w.b - b0] <= w.begin) before += sh[w.b++ - b0];
+  while (before + units(sh[w.b - b0]) <= w.begin) before += units(sh[w.b++ - b0]);
   w.s = load_seq(a, w.b, status);
   // the row tile: prefix sums of 32 at a time
   for (int rt0 = 0;; rt0 += 32) {
     const int64_t mine =
-        rt0 + lane < w.s.row_tiles ? static_cast<int64_t>(item_keys(a, w.s, rt0 + lane).tiles + kItemCost) * a.cache.heads
+        rt0 + lane < w.s.row_tiles ? static_cast<int64_t>(item_keys(a, w.s, rt0 + lane).tiles + w.cost) * a.cache.heads
                                    : 0;
     int64_t pre = mine;
 #pragma unroll
@@ -215,11 +244,11 @@ __device__ Walk find_range(const KvAttnArgs& a, int64_t* sh, uint32_t* status) {
     before += __shfl_sync(0xFFFFFFFFu, pre, 31);
   }
   w.k = item_keys(a, w.s, w.rt);
-  const int units = w.k.tiles + kItemCost;
-  w.h = static_cast<int>((w.begin - before) / units);
-  const int in = static_cast<int>(w.begin - before - static_cast<int64_t>(w.h) * units);
+  const int item = w.k.tiles + w.cost;
+  w.h = static_cast<int>((w.begin - before) / item);
+  const int in = static_cast<int>(w.begin - before - static_cast<int64_t>(w.h) * item);
   w.at = -in;
-  w.ta = in == 0 ? 0 : in <= kItemCost ? 1 : in - kItemCost;   // the first tile at or past the beginning
+  w.ta = in == 0 ? 0 : in <= w.cost ? 1 : in - w.cost;   // the first tile at or past the beginning
   if (w.ta < w.k.tiles)
     w.cut();
   else   // the range begins between an item's only tile and the next item
@@ -234,7 +263,7 @@ struct Smem {
   uint8_t k[2][D / 64][kKeys * 128];
   uint8_t v[2][kKeys / 64][D * 128];                    // 64 tokens a slab
   uint64_t qfull[2], sfull[2], pfull[2], ofull[2], kfull[2], kfree[2], vfull[2], vfree[2], fin;
-  int64_t scan[kSeqChunk];
+  Work scan[kSeqChunk];
   float kfac[kRing][4];       // MXFP4: factor of the scores of 32 keys
   float m1[kRowTile], l1[kRowTile];   // what the second half of an item's keys leaves
   uint32_t valid[kRing][4];   // of 32 keys: bit 0, 1: the 16-key group's page is in the cache
@@ -610,16 +639,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
         float f;
         {
           const float gk = a.cache.scales ? a.cache.scales[w.h] : 1.0f;
+          // the warp copies its 32 rows with whole rows in an access (a thread's
+          // own row at a time would touch 32 lines in each), then a thread takes
+          // its own
+          constexpr int kPer = D / 8;   // 16-byte parts of a row
+          const uint64_t own = mine ? reinterpret_cast<uint64_t>(static_cast<const uint16_t*>(a.q.data) +
+                                                                 (w.s.q0 + static_cast<int64_t>(tok)) * a.q.token_stride +
+                                                                 head * a.q.head_stride)
+                                    : 0;
+          const int part = lane % kPer;
+#pragma unroll 4
+          for (int j = 0; j < kPer; ++j) {
+            const int from = j * (32 / kPer) + lane / kPer, r = (warp & 3) * 32 + from;
+            const uint64_t src = __shfl_sync(0xFFFFFFFFu, own, from);
+            cp_async16(smem_u32(&sm.q[q][part >> 3][r * 128 + (((part & 7) ^ (r & 7)) << 4)]),
+                       src ? reinterpret_cast<const uint8_t*>(src) + 16 * part : a.q.data, src ? 16 : 0);
+          }
+          cp_async_wait_all();
+          __syncwarp();
           uint4 x[D / 8];
 #pragma unroll
-          for (int j = 0; j < D / 8; ++j) x[j] = make_uint4(0, 0, 0, 0);
-          if (mine) {
-            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q.data) +
-                                                              (w.s.q0 + static_cast<int64_t>(tok)) * a.q.token_stride +
-                                                              head * a.q.head_stride);
-#pragma unroll
-            for (int j = 0; j < D / 8; ++j) x[j] = src[j];
-          }
+          for (int j = 0; j < D / 8; ++j)
+            x[j] = *reinterpret_cast<const uint4*>(&sm.q[q][j >> 3][row_in * 128 + (((j & 7) ^ (row_in & 7)) << 4)]);
           float amax = 0.0f;
 #pragma unroll
           for (int j = 0; j < D / 8; ++j) {
@@ -807,9 +848,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
       }
       // ---- O of the row: the output, or a partial
       const int64_t out_row = w.s.q0 + static_cast<int64_t>(tok);
-      auto store_out = [&](int c, const float(&x)[16], float inv) {   // 16 dimensions from 16 c on
-        uint16_t* dst = static_cast<uint16_t*>(a.out.data) + out_row * a.out.token_stride + head * a.out.head_stride +
-                        16 * c;
+      auto store_out = [&](int c, const float(&x)[16], float inv, int64_t place) {   // 16 dimensions from 16 c on
+        uint16_t* dst = static_cast<uint16_t*>(a.out.data) + place + 16 * c;
 #pragma unroll
         for (int e = 0; e < 2; ++e)
           reinterpret_cast<uint4*>(dst)[e] =
@@ -841,7 +881,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
             }
           }
           if (whole) {
-            if (mine) store_out(c, x, inv);
+            if (mine) store_out(c, x, inv, out_row * a.out.token_stride + head * a.out.head_stride);
           } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -860,47 +900,82 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
       if (!whole) {
         const int64_t item0 = w.begin + w.at;
         const int c0 = cta_of(w.total, w.ctas, item0);
-        const int c1 = cta_of(w.total, w.ctas, item0 + (w.k.tiles > 1 ? w.k.tiles - 1 + kItemCost : 0));
+        const int c1 = cta_of(w.total, w.ctas, item0 + (w.k.tiles > 1 ? w.k.tiles - 1 + w.cost : 0));
         asm volatile("bar.sync 1, 256;" ::: "memory");
         if (tid == 0) sm.last = atomic_add_acq_rel_gpu(&counters[c0], 1u) == static_cast<uint32_t>(c1 - c0);
         asm volatile("bar.sync 1, 256;" ::: "memory");
         if (sm.last) {
           if (tid == 0) counters[c0] = 0;   // every CTA of the item has arrived
-          if (mine && puts) {
-            auto part = [&](int c) { return partials + (2 * static_cast<size_t>(c) + (c == c0)) * partial_floats<D>(); };
+          // The item's parts, weighed by their maxima.  First a thread takes a
+          // row's maxima and sums; the weights' exponents stay where the queries
+          // were, as many as fit there.  Then all threads take 16 dimensions of a
+          // row at a time, two parts of them in flight.  (Short code: it comes
+          // cold into the instruction cache.)
+          constexpr int kKept = sizeof(sm.q) / (kRows * sizeof(float)) - 4, kAt = 4;
+          float* kept = reinterpret_cast<float*>(&sm.q[0][0][0]);      // [kKept][kRows], then maxima, factors, places
+          float* const top = kept + kKept * kRows;
+          int64_t* const place = reinterpret_cast<int64_t*>(top + 2 * kRows);
+          const int parts = c1 - c0 + 1;
+          auto part = [&](int c) {
+            return partials + (2 * static_cast<size_t>(c0 + c) + (c == 0)) * partial_floats<D>();
+          };
+          if (tid < rows) {
             float M = -INFINITY, L = 0.0f;
-#pragma unroll 4
-            for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(part(c) + kRows * D + row));
-            auto weight = [&](int c, float* sum) {
-              const float lc = __ldcg(part(c) + kRows * D + kRows + row);
-              const float f = weight_of(__ldcg(part(c) + kRows * D + row), lc, M);
-              if (sum) *sum += f * lc;
-              return f;
-            };
-            // the row's weights stay where the queries were, as many as fit there
-            constexpr int kKept = sizeof(sm.q) / (kRows * sizeof(float));
-            float* kept = reinterpret_cast<float*>(&sm.q[0][0][0]) + row;
-#pragma unroll 2
-            for (int c = c0; c <= c1; ++c) {
-              const float f = weight(c, &L);
-              if (c - c0 < kKept) kept[(c - c0) * kRows] = f;
-            }
-            const float inv2 = L == 0.0f ? 0.0f : gv / L;
 #pragma unroll 1
-            for (int d = 0; d < D / 16; ++d) {
-              float x[16] = {};
-#pragma unroll 4
-              for (int c = c0; c <= c1; ++c) {
-                const float f = c - c0 < kKept ? kept[(c - c0) * kRows] : weight(c, nullptr);
+            for (int c = 0; c < parts; c += kAt) {
+              float pm[kAt], pl[kAt];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const float4 v = __ldcg(reinterpret_cast<const float4*>(part(c)) + (4 * d + e) * kRows + row);
-                  x[4 * e] += f * v.x, x[4 * e + 1] += f * v.y, x[4 * e + 2] += f * v.z, x[4 * e + 3] += f * v.w;
+              for (int e = 0; e < kAt; ++e) {
+                const float* from = part(min(c + e, parts - 1)) + kRows * D + tid;
+                pm[e] = __ldcg(from);
+                pl[e] = __ldcg(from + kRows);
+              }
+#pragma unroll
+              for (int e = 0; e < kAt; ++e) {
+                if (c + e >= parts) break;
+                const float to = fmaxf(M, pm[e]);
+                L = L * weight_of(M, L, to) + pl[e] * weight_of(pm[e], pl[e], to);
+                M = to;
+                if (c + e < kKept) kept[(c + e) * kRows + tid] = pm[e];
+              }
+            }
+            top[tid] = M;
+            top[kRows + tid] = L == 0.0f ? 0.0f : gv / L;   // (NaN: the whole row)
+            const int64_t token = w.s.q0 + static_cast<int64_t>(tok0 + tid / a.group);
+            const int64_t to_head = static_cast<int64_t>(w.h) * a.group + tid % a.group;
+            place[tid] = token * a.out.token_stride + to_head * a.out.head_stride;
+            if (a.lse)
+              a.lse[token * (static_cast<int64_t>(a.cache.heads) * a.group) + to_head] =
+                  L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+          }
+          asm volatile("bar.sync 1, 256;" ::: "memory");
+          const int elements = rows * (D / 16);
+#pragma unroll 1
+          for (int e = tid; e < elements; e += 256) {
+            const int d16 = e / rows, r = e - d16 * rows;
+            const float M = top[r];
+            float x[16] = {};
+#pragma unroll 1
+            for (int c = 0; c < parts; c += 2) {
+              float4 v[2][4];
+#pragma unroll
+              for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  v[p][k] = __ldcg(reinterpret_cast<const float4*>(part(min(c + p, parts - 1))) + (4 * d16 + k) * kRows + r);
+#pragma unroll
+              for (int p = 0; p < 2; ++p) {
+                if (c + p >= parts) break;
+                const float fe =
+                    weight_of(c + p < kKept ? kept[(c + p) * kRows + r] : __ldcg(part(c + p) + kRows * D + r), 0.0f, M);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  x[4 * k] += fe * v[p][k].x, x[4 * k + 1] += fe * v[p][k].y;
+                  x[4 * k + 2] += fe * v[p][k].z, x[4 * k + 3] += fe * v[p][k].w;
                 }
               }
-              store_out(d, x, inv2);
             }
-            store_lse(M, L);
+            store_out(d16, x, top[kRows + r], place[r]);
           }
         }
       }
