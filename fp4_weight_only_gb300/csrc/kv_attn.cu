@@ -1108,11 +1108,11 @@ cudaError_t launch_kv_attention(const KvAttnArgs& a, int num_sms, cudaStream_t s
   // By the rows of a K/V head in the longest sequence.  This kernel's work grows
   // with them, the tensor-memory kernel's is a 128-row tile's whatever they are.
   // Us here / there for 24 ragged contexts of up to 4096 tokens (group 8):
-  //   rows               16       32       48       64 (there)
-  //   8 heads of 64    34/55    47/55    61/55      56
-  //   8 heads of 128   47/90    69/92    96/91      91
-  // and for 2 contexts of 60000, heads of 128, 42/104, 62/102, 79/105 and 106;
-  // at 96 rows of heads of 64, 106/87.
+  //   rows                            16    32    48    any (there)
+  //   8 heads of 64                   34    47    61    55
+  //   8 heads of 128                  47    69    96    88
+  //   2 contexts of 60000, of 128     42    62    79    82
+  // and at 96 rows of heads of 64 106 here, 87 there.
   // Up to 8 rows the one-column instance: three CTAs of it fit an SM, two of
   // the other.  64 ragged contexts up to 8192 take 71 us, 102 with two columns,
   // one of 131071 39 and 52.  Groups beyond 128 heads have no tile of whole

@@ -26,10 +26,10 @@
 // item cut between CTAs leaves FP32 partials that the last arriver adds.
 //
 // Measured: 4096 new tokens behind 12288, 64 query heads of 128 over 8 NVFP4
-// heads, 1.53 ms, 1.25 PFLOP/s (65 % of a cuBLAS product's rate): a softmax
-// warpgroup's pass over 128 x 128 scores (about 2300 cycles beside the other's)
-// is the longest stage, the two MMAs of both row tiles take about 1530.  Five
-// ragged pieces of 3 to 1100 tokens with a window of 1024, heads of 64, 63 us:
+// heads, 1.43 ms, 1.35 PFLOP/s (70 % of a cuBLAS product's rate; MXFP4 1.65):
+// a softmax warpgroup's pass over 128 x 128 scores is the longest stage, the
+// tensor pipe is busy 56 % of the time.  Five ragged pieces of 3 to 1100 tokens
+// with a window of 1024, heads of 64, MXFP4, 64 us:
 // an item's beginning and end (8 to 10 k cycles) next to 13 tiles.
 #include <cfloat>
 #include <cuda_bf16.h>
@@ -751,16 +751,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
           // maximum as it stands, which moves only when passed by 2^8 (p <= 2^8
           // fits FP16); then O, and the tile's weights so far, are scaled
           float2 sum = make_float2(0.0f, 0.0f);
-          auto weigh = [&](int c, uint32_t(&raw)[32]) {   // 32 keys
-            float x[32];
+          auto weigh = [&](int c, float(&xa)[32], float(&xb)[32]) {   // 64 keys
+            if (masked) {
+              mask(c, xa);
+              mask(c + 1, xb);
+            }
+            const float fa = factor_of(c), fb = factor_of(c + 1);
+            float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, u[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(raw[e]);
-            if (masked) mask(c, x);
-            const float fc = factor_of(c);
-            float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int e = 0; e < 32; ++e) t[e & 3] = fmaxf(t[e & 3], x[e]);
-            const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * fc;
+            for (int e = 0; e < 32; ++e) t[e & 3] = fmaxf(t[e & 3], xa[e]), u[e & 3] = fmaxf(u[e & 3], xb[e]);
+            const float top = fmaxf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * fa,
+                                    fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3])) * fb);
             const bool grow = top > m + 8.0f;
             if (__any_sync(0xFFFFFFFFu, grow)) {
               float r = 1.0f;
@@ -784,24 +785,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
               }
             }
             const float ref = m == -INFINITY ? 0.0f : -m;
-            const float2 fc2 = make_float2(fc, fc), ref2 = make_float2(ref, ref);
-            uint32_t p[16];
+            const float2 ref2 = make_float2(ref, ref);
+            auto put = [&](int at, float(&x)[32], float fc) {
+              const float2 fc2 = make_float2(fc, fc);
+              uint32_t p[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float2 y = fma2(make_float2(x[2 * e], x[2 * e + 1]), fc2, ref2);
-              const float2 pe = make_float2(ex2(y.x), ex2(y.y));
-              sum = add2(sum, pe);
-              p[e] = pack_f16(pe.x, pe.y);
-            }
-            tmem_st_x16(s_tmem + 16 * c, p);
+              for (int e = 0; e < 16; ++e) {
+                const float2 y = fma2(make_float2(x[2 * e], x[2 * e + 1]), fc2, ref2);
+                const float2 pe = make_float2(ex2(y.x), ex2(y.y));
+                sum = add2(sum, pe);
+                p[e] = pack_f16(pe.x, pe.y);
+              }
+              tmem_st_x16(s_tmem + 16 * at, p);
+            };
+            put(c, xa, fa);
+            put(c + 1, xb, fb);
           };
-          // (the loop stays rolled: this kernel's roles share an instruction cache)
+          // (the loop stays rolled: this kernel's roles share an instruction cache.
+          // 64 keys at a time, 4096-token piece: 1.43 ms, 32 keys 1.54, 16 keys
+          // 1.98; a vote, a wait and a store's latency a chunk)
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t x[32];
-            tmem_ld_x32(s_tmem + 32 * c, x);
+          for (int c = 0; c < 4; c += 2) {
+            uint32_t ra[32], rb[32];
+            tmem_ld_x32(s_tmem + 32 * c, ra);
+            tmem_ld_x32(s_tmem + 32 * c + 32, rb);
             tmem_wait_ld();
-            weigh(c, x);
+            weigh(c, reinterpret_cast<float(&)[32]>(ra), reinterpret_cast<float(&)[32]>(rb));
           }
           l += sum.x + sum.y;
           tmem_wait_st();
