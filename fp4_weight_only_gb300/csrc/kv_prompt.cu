@@ -717,7 +717,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
           const uint32_t num = n + i;
           const int key0 = w.k.lo + (w.ta + i) * kKeys;
           wait(&sm.sfull[q], my_tiles++ & 1);
-          if constexpr (FMT == kMXFP4) wait(&sm.vfull[num & 1], (num >> 1) & 1);   // vscale
           tc_fence_after();
           uint32_t valid = 0;
 #pragma unroll
@@ -740,13 +739,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
             for (int e = 0; e < 32; ++e)
               if (!((keep >> e) & 1)) x[e] = -INFINITY;
           };
-          // MXFP4: V is held relative to a reference that has risen since this
-          // chain's last tile, perhaps
-          if constexpr (FMT == kMXFP4) {
-            const float now = sm.vscale[num % kRing];
-            if (i > first_tile && now != vs) scale_o(vs / now);   // (powers of two)
-            vs = now;
-          }
           // ---- one pass: a chunk's scores become weights of the reference
           // maximum as it stands, which moves only when passed by 2^8 (p <= 2^8
           // fits FP16); then O, and the tile's weights so far, are scaled
@@ -813,6 +805,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
             weigh(c, reinterpret_cast<float(&)[32]>(ra), reinterpret_cast<float(&)[32]>(rb));
           }
           l += sum.x + sum.y;
+          // MXFP4: V is held relative to a reference that has risen since this
+          // chain's last tile, perhaps (looked at last, when V has long come)
+          if constexpr (FMT == kMXFP4) {
+            wait(&sm.vfull[num & 1], (num >> 1) & 1);
+            const float now = sm.vscale[num % kRing];
+            if (i > first_tile && now != vs) scale_o(vs / now);   // (powers of two)
+            vs = now;
+          }
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
