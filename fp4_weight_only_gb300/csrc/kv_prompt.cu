@@ -26,7 +26,7 @@
 // item cut between CTAs leaves FP32 partials that the last arriver adds.
 //
 // Measured: 4096 new tokens behind 12288, 64 query heads of 128 over 8 NVFP4
-// heads, 1.43 ms, 1.35 PFLOP/s (70 % of a cuBLAS product's rate; MXFP4 1.65):
+// heads, 1.43 ms, 1.35 PFLOP/s (70 % of a cuBLAS product's rate; MXFP4 1.62 ms):
 // a softmax warpgroup's pass over 128 x 128 scores is the longest stage, the
 // tensor pipe is busy 56 % of the time.  Five ragged pieces of 3 to 1100 tokens
 // with a window of 1024, heads of 64, MXFP4, 64 us:
