@@ -646,10 +646,15 @@ __global__ void __launch_bounds__(kThreads, Smem<D, FMT, NB>::kCtas) kv_attn_ker
         }
         sm.valid[lane] = valid;
         mbar_arrive_expect_tx(bar, __popc(valid) * G::kBytes);
-        // groups that follow one another in a page go with one copy
+        // groups that follow one another in memory go with one copy (each is
+        // compared with the one before it: the last may lie kU - 1 groups after
+        // the first and those between them anywhere)
+        bool run = true;
+#pragma unroll
+        for (int u = 0; u < kU; ++u) run = run && src[u] && src[u] == src[0] + u * G::kBytes;
 #pragma unroll
         for (int u = 0; u < kU; u += 2) {
-          if (kU == 4 && u == 0 && valid == 15 && src[kU - 1] == src[0] + (kU - 1) * G::kBytes) {
+          if (kU == 4 && u == 0 && run) {
             bulk_g2s(dst, src[0], kU * G::kBytes, bar, policy);
             break;
           }
