@@ -756,6 +756,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                                     fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3])) * fb);
             const bool grow = top > m + 8.0f;
             if (__any_sync(0xFFFFFFFFu, grow)) {
+              // (weights and O that this tile has stored are loaded again)
+              tmem_wait_st();
               float r = 1.0f;
               if (grow) {
                 r = ex2(m - top);
@@ -810,7 +812,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
           if constexpr (FMT == kMXFP4) {
             wait(&sm.vfull[num & 1], (num >> 1) & 1);
             const float now = sm.vscale[num % kRing];
-            if (i > first_tile && now != vs) scale_o(vs / now);   // (powers of two)
+            if (i > first_tile && now != vs) {
+              tmem_wait_st();   // (the tile may have scaled O already)
+              scale_o(vs / now);   // (powers of two)
+            }
             vs = now;
           }
           tmem_wait_st();
