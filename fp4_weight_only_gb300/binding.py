@@ -553,7 +553,8 @@ def kv_attention(cache, q, block_table, seq_lens, q_offsets=None, max_q=1, scale
     queries begin; None: max_q queries for every sequence.  max_q: the most
     queries of a sequence.  scale: by default head_dim ** -0.5.  causal: the
     last query sees every key, the one before it all but the last, and so on;
-    window > 0 keeps the nearest `window` of them.  lse: an FP32 tensor
+    window > 0 keeps the nearest `window` of them (pages whose keys no query
+    sees may have been given back: any entry will do).  lse: an FP32 tensor
     [total_q, num_q_heads] that receives the log of the softmax's sum.  A
     query that sees no key gives zeros (and an lse of -inf)."""
     if q.dtype not in _DTYPES or q.dim() != 3:

@@ -102,6 +102,8 @@ struct Seq {
   int len;      // keys
   int nq;       // query rows
   int q0;       // first query row
+  int first;    // first key that a query of the sequence sees: those before it,
+                // outside every window, may be gone (no page, any bytes)
   int lo;       // first key of tile 0
   int tiles;    // tiles of an item, at least 1 so that empty rows are written
   int blocks;   // row blocks
@@ -125,11 +127,12 @@ __device__ __forceinline__ Seq load_seq(const KvAttnArgs& a, int b, uint32_t* st
     s.nq = static_cast<int>(a.max_q);
   }
   if (bad) atomicOr(status, kStatusBounds);
-  s.lo = 0;
+  s.first = 0;
   if (a.window > 0) {
     const int64_t first = static_cast<int64_t>(s.len) - s.nq - a.window + 1;
-    s.lo = first > 0 ? static_cast<int>(first) & ~(TILE - 1) : 0;
+    s.first = first > 0 ? static_cast<int>(first) : 0;
   }
+  s.lo = s.first & ~(TILE - 1);
   s.tiles = s.len > s.lo ? (s.len - s.lo + TILE - 1) / TILE : 1;
   s.blocks = (s.nq * a.group + ROWS - 1) / ROWS;
   return s;
@@ -318,12 +321,6 @@ struct Walk {
 };
 
 // ------------------------------------------------------------ the kernel
-template <int N>
-__device__ __forceinline__ void zero(uint32_t (&w)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) w[i] = 0;
-}
-
 // One 16-dimension step of O^T += V^T P^T: byte I of the interleaved words
 // holds dimensions 2 i and 2 i + 1 of the lane's part for its four keys.
 template <int I, int NB, int K>
@@ -606,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, Smem<D, FMT, NB>::kCtas) kv_attn_ker
           for (int u = 0; u < kU; ++u) {
             const int key = key0 + u * kKvGroup;
             src[u] = nullptr;
-            if (t0 + lane < w.tb && key < w.s.len) {
+            if (t0 + lane < w.tb && key < w.s.len && key + kKvGroup > w.s.first) {
               const int64_t page = table[key >> a.cache.page_shift];
               if (page >= 0 && page < a.cache.num_pages)
                 src[u] = a.cache.data + page * a.cache.page_stride + w.h * head_stride +
@@ -917,12 +914,15 @@ __global__ void __launch_bounds__(kThreads, Smem<D, FMT, NB>::kCtas) kv_attn_ker
           cv[e] = base[u * G::kBytes + v_scales + key * G::kScales];
         }
         if (masked) {
-          // past the end the page may hold anything, NaN scales among it, and
-          // 0 * NaN would reach the sums: such keys count as zeros
+          // past the end and before the window the page may hold anything, NaN
+          // scales among it, and 0 * NaN would reach the sums: such keys' scales
+          // count as zeros
           const bool here = (valid >> u) & 1;
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (!here || key0 + u * kKvGroup + (e & 1 ? key_y : key_x) + (e & 2 ? 8 : 0) >= s.len) cv[e] = 0, zero(wv[e]);
+          for (int e = 0; e < 4; ++e) {
+            const int key = key0 + u * kKvGroup + (e & 1 ? key_y : key_x) + (e & 2 ? 8 : 0);
+            if (!here || key >= s.len || key < s.first) cv[e] = 0;
+          }
         }
         uint32_t s01, s23;
         if constexpr (FMT == kNVFP4) {
@@ -960,7 +960,8 @@ __global__ void __launch_bounds__(kThreads, Smem<D, FMT, NB>::kCtas) kv_attn_ker
         // the group's 16 tokens' scales, kScales bytes each for K and for V: a
         // lane looks at the bytes of token lane / 2
         const int tok = lane >> 1;
-        const bool here = ((valid >> u) & 1) && key0 + u * kKvGroup + tok < s.len;
+        const int key = key0 + u * kKvGroup + tok;
+        const bool here = ((valid >> u) & 1) && key < s.len && key >= s.first;
         constexpr int kB = G::kScales / 2;   // 1 or 2
         const uint8_t* pk = grp + G::kKScales + tok * G::kScales + (lane & 1) * kB;
         const uint8_t* pv = grp + G::kVScales + tok * G::kScales + (lane & 1) * kB;

@@ -96,12 +96,20 @@ struct Keys {
   int tiles;   // at least 1, so that rows without keys are written
 };
 
+// First key that a row of the item sees: those before it, outside every window,
+// may be gone (no page, any bytes).
+__device__ __forceinline__ int first_key(const KvAttnArgs& a, const Seq& s, int rt) {
+  // (len and nq are below 2^31, a window 1..2^31 - 1 in 32 bits)
+  const int last = s.len - s.nq + rt * s.tokens + 1;   // keys that the first row sees without a window
+  const int window = static_cast<int>(a.window);
+  return a.window > 0 && last > window ? last - window : 0;
+}
+
 __device__ __forceinline__ Keys item_keys(const KvAttnArgs& a, const Seq& s, int rt) {
   const int t0 = rt * s.tokens, t1 = min(s.nq, t0 + s.tokens) - 1;
   const int64_t hi = a.causal ? static_cast<int64_t>(s.len) - s.nq + t1 : s.len - 1;
-  const int64_t first = a.window > 0 ? static_cast<int64_t>(s.len) - s.nq + t0 - a.window + 1 : 0;
   Keys k;
-  k.lo = first > 0 ? static_cast<int>(first) & ~(kKeys - 1) : 0;
+  k.lo = first_key(a, s, rt) & ~(kKeys - 1);
   k.tiles = hi >= k.lo ? static_cast<int>(hi - k.lo) / kKeys + 1 : 1;
   return k;
 }
@@ -318,9 +326,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
   const int64_t head_stride = static_cast<int64_t>(G::kBytes) << (a.cache.page_shift - 4);
-  // 16-token group of `key` in sequence w.b, or null
-  auto group_of = [&](int key) -> const uint8_t* {
-    if (key >= w.s.len) return nullptr;
+  // 16-token group of `key` in sequence w.b, or null (also where all of it lies
+  // before the first key that is seen)
+  auto group_of = [&](int key, int first) -> const uint8_t* {
+    if (key >= w.s.len || (key | (kKvGroup - 1)) < first) return nullptr;
     const int64_t page = a.block_table[w.b * a.table_stride + (key >> a.cache.page_shift)];
     if (page < 0 || page >= a.cache.num_pages) {
       atomicOr(status, kStatusBounds);
@@ -435,15 +444,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
     uint32_t sc[8];
     auto load = [&](int tile) {
       const int key = w.k.lo + tile * kKeys + key_in;
-      const uint8_t* grp = group_of(key);
+      const int first = first_key(a, w.s, w.rt);
+      const uint8_t* grp = group_of(key, first);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int t = (kg & 1) * 8 + i;
 #pragma unroll
         for (int j = 0; j < kW; ++j) wd[i][j] = 0;
         sc[i] = 0;
-        // a token past the end may hold anything, NaN scales among it: zeros
-        if (grp && key + i < w.s.len) {
+        if (grp) {
           const uint8_t* p = grp + G::kVCodes + t * G::kRow + d0 / 2;
           if constexpr (kW == 2) {
             const uint2 v = *reinterpret_cast<const uint2*>(p);
@@ -454,6 +463,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
           }
           sc[i] = grp[G::kVScales + t * G::kScales + d0 / G::kBlock];
         }
+      }
+      // a token past the end or before the window may hold anything, and 0 times
+      // a NaN scale would reach the sums: its scale counts as zero
+      if (key < first || key + 8 > w.s.len) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (key + i < first || key + i >= w.s.len) sc[i] = 0;
       }
     };
     if (!w.done()) load(w.ta);
@@ -536,11 +552,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
     uint32_t wd[2][kW], sc[2][kS];     // tokens kw 32 + lane and 64 + that
     bool have[2] = {false, false};
     auto load = [&](int tile) {
+      const int first = first_key(a, w.s, w.rt);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int key = w.k.lo + tile * kKeys + x * 64 + kw * 32 + lane;
-        const uint8_t* grp = group_of(key);
-        have[x] = grp != nullptr;
+        const uint8_t* grp = group_of(key, first);
+        have[x] = grp != nullptr && key >= first;
 #pragma unroll
         for (int j = 0; j < kW; ++j) wd[x][j] = 0;
 #pragma unroll

@@ -375,8 +375,14 @@ petit_status_t petit_kv_read(const petit_kv_cache_t* cache, const int64_t* slots
  * Products are FP16 by FP16 with FP32 sums: q takes a power of two per row
  * (exact but for elements 2^26 below the row's largest), the softmax's weights
  * are rounded to 11 bits, and values of an MXFP4 cache lose bits only where
- * their scale lies 2^32 or more below the largest of the keys around them.
+ * their scale lies 2^32 or more below the largest among the sequence's keys
+ * that queries of the call see (one query's reference counts keys that only
+ * another of them sees).
  * Scores, the softmax's maximum and sum, and the output's sums are FP32.
+ *
+ * Keys that lie outside the window of every query of their sequence are not
+ * looked at: their pages may have been given back (any entry of block_table
+ * for pages of such keys alone) and their bytes may be anything.
  *
  * A length past max_pages * page_size, a page outside the cache and query
  * offsets outside 0..total_q are recorded as PETIT_ERR_BOUNDS in the
