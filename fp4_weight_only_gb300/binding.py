@@ -567,6 +567,10 @@ def kv_attention(cache, q, block_table, seq_lens, q_offsets=None, max_q=1, scale
     batch, max_pages = block_table.shape
     if block_table.dtype is not torch.int32 or block_table.get_device() != cache.device_index:
         raise ValueError("block_table: need int32 on the cache's device")
+    # (with one row, or rows without entries, torch's stride says nothing)
+    table_stride = block_table.stride(0) if batch > 1 and max_pages > 0 else max(max_pages, 1)
+    if table_stride < max_pages:
+        raise ValueError("block_table: need rows of their own (an expanded one: make it contiguous)")
     rq = _rows(q, cache, heads, q.dtype, "q")
     if out is None:
         out, ro = _new_rows(cache, total_q, heads, q.dtype)
@@ -576,9 +580,8 @@ def kv_attention(cache, q, block_table, seq_lens, q_offsets=None, max_q=1, scale
         rq, ro, None if lse is None else _ptr(lse), _ptr(block_table),
         _indices(seq_lens, cache, torch.int32, (batch,), "seq_lens"),
         None if q_offsets is None else _indices(q_offsets, cache, torch.int32, (batch + 1,), "q_offsets"),
-        batch, total_q, int(max_q), max_pages, max(block_table.stride(0), max_pages) if batch > 1 else max_pages,
-        heads, _DTYPES[q.dtype], cache.head_dim ** -0.5 if scale is None else float(scale), int(bool(causal)),
-        int(window))
+        batch, total_q, int(max_q), max_pages, table_stride, heads, _DTYPES[q.dtype],
+        cache.head_dim ** -0.5 if scale is None else float(scale), int(bool(causal)), int(window))
     if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (total_q, heads)
                             or not lse.is_contiguous() or lse.get_device() != cache.device_index):
         raise ValueError(f"lse: need a contiguous FP32 tensor [{total_q}, {heads}] on the cache's device")
