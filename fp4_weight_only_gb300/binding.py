@@ -268,20 +268,25 @@ def workspace_bytes(m, n, k, fmt="nvfp4"):
 
 
 class Workspace:
-    """A zero-filled device workspace that grows on demand."""
+    """A zero-filled device workspace that grows on demand.  What it has
+    outgrown is kept: calls that are queued or captured in a graph still use it
+    and record their errors there."""
 
     def __init__(self, device=None, nbytes=0):
         self.device = torch.device(device or "cuda")
         self.buf = torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=self.device)
+        self._outgrown = []
 
     def ensure(self, nbytes):
         if nbytes > self.buf.numel():
+            self._outgrown.append(self.buf)
             self.buf = torch.zeros(int(nbytes), dtype=torch.uint8, device=self.device)
         return self.buf
 
     def status(self):
         """PETIT_OK (0) or the error the kernels recorded (clears it)."""
-        return load().petit_get_device_status(_ptr(self.buf), self.buf.numel(), _stream())
+        found = [load().petit_get_device_status(_ptr(b), b.numel(), _stream()) for b in (*self._outgrown, self.buf)]
+        return next((s for s in found if s), 0)
 
 
 def gemm(A, rep, n, fmt="nvfp4", global_scale=1.0, workspace=None, out=None):
