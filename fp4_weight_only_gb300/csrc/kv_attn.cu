@@ -24,10 +24,13 @@
 //    transposes (movmatrix), with no shared memory.
 // Both products are FP16: codes times NVFP4 scales are exact in FP16, q is
 // brought into FP16's range by a power of two per row (exact but for elements
-// 2^26 below the row's largest), and p is rounded to 11 bits, which adds less
-// than the rounding of a 16-bit output.  MXFP4 scales exceed FP16's range: they
-// are taken relative to the largest that the warp has met in the item, for K
-// and for V, and that is applied in FP32 (exact for scales up to 2^32 below it).
+// 2^26 below the row's largest), and p is rounded to FP16 (kv_math.cuh): 2^-11
+// of a weight at most, an eighth of what a BF16 output's rounding may be and as
+// much as an FP16 output's.  (FP32 weights would need a second and a third
+// product each.)  Sums are of the rounded weights, so that what rounding does
+// to all alike cancels.  MXFP4 scales exceed FP16's range: they are taken
+// relative to the largest that the warp has met in the item, for K and for V,
+// and that is applied in FP32 (exact for scales up to 2^32 below it).
 //
 // Work split.  The keys of every (sequence, K/V head, block of 8 NB rows) are
 // cut into tiles; the tiles of the whole call, numbered in that order, are cut
@@ -380,8 +383,7 @@ __device__ __forceinline__ void store_row(const KvAttnArgs& a, int q0, int row, 
   else
     *reinterpret_cast<uint32_t*>(dst) = w[0];
   if (a.lse && lane == 0)
-    a.lse[tok * (static_cast<int64_t>(a.cache.heads) * a.group) + head] =
-        L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+    a.lse[tok * (static_cast<int64_t>(a.cache.heads) * a.group) + head] = lse_of(M, L);
 }
 
 template <int D, int FMT, int NB>
@@ -848,7 +850,7 @@ __global__ void __launch_bounds__(kThreads, Smem<D, FMT, NB>::kCtas) kv_attn_ker
 
       float(&fac)[NB][2] = FMT == kMXFP4 ? fk : fq;
       // ---- softmax: the reference maximum moves only when a score passes it
-      // by 2^8, so most tiles need no exchange between lanes (p <= 2^8 fits FP16)
+      // by 2^kWeightRoom, so most tiles need no exchange between lanes
       uint32_t pb[kU][NB][2];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
@@ -872,8 +874,8 @@ __global__ void __launch_bounds__(kThreads, Smem<D, FMT, NB>::kCtas) kv_attn_ker
             f[c] = top == m[nb][c] ? 1.0f : ex2(m[nb][c] - top);
             m[nb][c] = top;
             // (a row with no key yet: its scores are all -inf, and p = 0)
-            ref[nb][c] = top == -INFINITY ? 0.0f : top;
-            pass[nb][c] = (top + 8.0f) / fac[nb][c];
+            ref[nb][c] = top == -INFINITY ? 0.0f : top - kWeightLift;
+            pass[nb][c] = (top + kWeightRoom) / fac[nb][c];
             l[nb][c] *= f[c];
           }
 #pragma unroll
@@ -985,7 +987,7 @@ __global__ void __launch_bounds__(kThreads, Smem<D, FMT, NB>::kCtas) kv_attn_ker
           for (int c = 0; c < 2; ++c) {
             const float x = fq[nb][c] * ldexpf(1.0f, kref - 136);
             fk[nb][c] = x < FLT_MIN ? FLT_MIN : x;
-            pass[nb][c] = (m[nb][c] + 8.0f) / fk[nb][c];
+            pass[nb][c] = (m[nb][c] + kWeightRoom) / fk[nb][c];
           }
 #pragma unroll
           for (int i2 = 0; i2 < kK; ++i2) {

@@ -81,6 +81,19 @@ __device__ __forceinline__ int row_shift(float amax) {
   return amax == 0.0f ? 0 : min(139 - e, 127);
 }
 
+// The softmax's weights are FP16: 2^(x - m + kWeightLift) with m the running
+// maximum in log2 units, which moves when a score passes it by kWeightRoom, so
+// a weight is at most 2^15.  They have 11 bits down to 2^-21 of the row's
+// largest, and what lies below is a multiple of 2^-31 of it: a long context's
+// many small weights beside one large one still add up.  (Without the lift all
+// below 2^-25 were lost.)
+constexpr float kWeightLift = 7.0f, kWeightRoom = 8.0f;
+
+// Natural logarithm of a row's sum of e^x, of its maximum and sum of weights.
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return l == 0.0f ? -INFINITY : (m - kWeightLift + log2f(l)) * 0.69314718055994531f;
+}
+
 // Weight of a partial result with maximum m and sum l when results meet at
 // maximum M (no key: none; a NaN sum stays one).
 __device__ __forceinline__ float weight_of(float m, float l, float M) {

@@ -757,8 +757,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
               if (!((keep >> e) & 1)) x[e] = -INFINITY;
           };
           // ---- one pass: a chunk's scores become weights of the reference
-          // maximum as it stands, which moves only when passed by 2^8 (p <= 2^8
-          // fits FP16); then O, and the tile's weights so far, are scaled
+          // maximum as it stands, which moves only when passed by 2^kWeightRoom;
+          // then O, and the tile's weights so far, are scaled
           float2 sum = make_float2(0.0f, 0.0f);
           auto weigh = [&](int c, float(&xa)[32], float(&xb)[32]) {   // 64 keys
             if (masked) {
@@ -771,7 +771,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
             for (int e = 0; e < 32; ++e) t[e & 3] = fmaxf(t[e & 3], xa[e]), u[e & 3] = fmaxf(u[e & 3], xb[e]);
             const float top = fmaxf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * fa,
                                     fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3])) * fb);
-            const bool grow = top > m + 8.0f;
+            const bool grow = top > m + kWeightRoom;
             if (__any_sync(0xFFFFFFFFu, grow)) {
               // (weights and O that this tile has stored are loaded again)
               tmem_wait_st();
@@ -795,7 +795,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                 tmem_st_x16(s_tmem + 16 * c2, p);
               }
             }
-            const float ref = m == -INFINITY ? 0.0f : -m;
+            const float ref = m == -INFINITY ? 0.0f : kWeightLift - m;
             const float2 ref2 = make_float2(ref, ref);
             auto put = [&](int at, float(&x)[32], float fc) {
               const float2 fc2 = make_float2(fc, fc);
@@ -889,9 +889,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                          pack2(x[8 * e + 6] * inv, x[8 * e + 7] * inv, a.bf16));
       };
       auto store_lse = [&](float M, float L) {
-        if (a.lse)
-          a.lse[out_row * (static_cast<int64_t>(a.cache.heads) * a.group) + head] =
-              L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+        if (a.lse) a.lse[out_row * (static_cast<int64_t>(a.cache.heads) * a.group) + head] = lse_of(M, L);
       };
       float* slot = partials + (2 * static_cast<size_t>(blockIdx.x) + (w.ta == 0 ? 1 : 0)) * partial_floats<D>();
       if (puts) {
@@ -976,8 +974,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
             const int64_t to_head = static_cast<int64_t>(w.h) * a.group + tid % a.group;
             place[tid] = token * a.out.token_stride + to_head * a.out.head_stride;
             if (a.lse)
-              a.lse[token * (static_cast<int64_t>(a.cache.heads) * a.group) + to_head] =
-                  L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+              a.lse[token * (static_cast<int64_t>(a.cache.heads) * a.group) + to_head] = lse_of(M, L);
           }
           asm volatile("bar.sync 1, 256;" ::: "memory");
           const int elements = rows * (D / 16);
