@@ -758,7 +758,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
           };
           // ---- one pass: a chunk's scores become weights of the reference
           // maximum as it stands, which moves only when passed by 2^kWeightRoom;
-          // then O, and the tile's weights so far, are scaled
+          // then O, and the tile's weights so far, are scaled: by a power of two
+          // (the reference is a whole number), so that a weight that has been
+          // rounded to FP16 is rounded again below its range only
           float2 sum = make_float2(0.0f, 0.0f);
           auto weigh = [&](int c, float(&xa)[32], float(&xb)[32]) {   // 64 keys
             if (masked) {
@@ -771,20 +773,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
             for (int e = 0; e < 32; ++e) t[e & 3] = fmaxf(t[e & 3], xa[e]), u[e & 3] = fmaxf(u[e & 3], xb[e]);
             const float top = fmaxf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * fa,
                                     fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3])) * fb);
-            const bool grow = top > m + kWeightRoom;
-            if (__any_sync(0xFFFFFFFFu, grow)) {
+            while (__any_sync(0xFFFFFFFFu, top > m + kWeightRoom)) {
               // (weights and O that this tile has stored are loaded again)
               tmem_wait_st();
               float r = 1.0f;
-              if (grow) {
-                r = ex2(m - top);
-                m = top;
+              if (top > m + kWeightRoom) {
+                // 2^-24, FP16's least number, at a time (2^-64 leaves nothing, so
+                // that this takes three times at most)
+                const float up = top - m < 64.0f ? fminf(ceilf(top), m + 24.0f) : ceilf(top);
+                r = ex2(m - up);
+                m = up;
                 l *= r;
                 sum.x *= r;
                 sum.y *= r;
               }
               if (i > first_tile) scale_o(r);
-              const __half2 rh = __float2half2_rn(r);   // (below FP16 it is 0, as the weights become)
+              const __half2 rh = __float2half2_rn(r);
 #pragma unroll 1
               for (int c2 = 0; c2 < c; ++c2) {
                 uint32_t p[16];

@@ -12,7 +12,7 @@ pytestmark = pytest.mark.gpu
 
 @pytest.mark.parametrize("fmt,dim", [("nvfp4", 128), ("mxfp4", 128), ("nvfp4", 64), ("mxfp4", 64)])
 @pytest.mark.parametrize("nq,group", [(1, 8), (3, 5), (50, 1), (64, 2), (90, 2), (256, 1), (400, 1)])
-@pytest.mark.parametrize("step", [33, 64])
+@pytest.mark.parametrize("step", [33, 64, 100])
 def test_maxima_that_rise_on_and_on(cuda_lib, fmt, dim, nq, group, step):
     """A score of 9 log2 units more every `step` keys; rows with a fraction of
     that, and with its opposite, stand between them."""

@@ -26,3 +26,20 @@ def test_many_small_weights_beside_a_large_one(cuda_lib, fmt, nq, group, batch, 
     q[..., 0] = 1.0
     scale = bits * np.log(2.0) / pool.k[0, 0, 0]
     pool.run(q, [nq] * batch, [list(range(pages))] * batch, [n] * batch, scale=float(scale))
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("nq", [64, 130])
+@pytest.mark.parametrize("at", [64, 100])
+@pytest.mark.parametrize("bits", [9.3, 17.3, 21.7, 26.0, 28.5])
+def test_weights_made_before_the_maximum_rose(cuda_lib, fmt, nq, at, bits):
+    """A key in the middle of a tile has 2^bits of the weight of those before
+    it, and a value of zero: the output is what they had."""
+    n, page, dim = 128 + nq, 64, 64
+    pages = -(-n // page)
+    k, v = np.zeros((2, pages * page, 1, dim))
+    k[at, 0, 0], v[:at], k[at + 1:, 0, 0] = 6.0, -6.0, -6.0
+    pool = Pool(cuda_lib, pages, 1, dim, fmt, page, rows=[k, v])
+    q = torch.zeros((nq, 1, dim), dtype=torch.float16, device="cuda")
+    q[..., 0] = 1.0
+    pool.run(q, [nq], [list(range(pages))], [n], scale=float(bits * np.log(2.0) / pool.k[at, 0, 0]))
