@@ -9,7 +9,9 @@ serves a batch of random prompts of different lengths: one call for all
 prompts, then token after token through one CUDA graph, whose lengths and
 slots the device advances.  It prints the times, and how far the attention
 lies from one in FP32 over the tokens that `kv_read` gives back.  Weights and
-inputs are random; position encoding, norms and the MLP are the caller's.
+inputs are random and carry no positions; norms and the MLP are the caller's,
+and so is position encoding, which enters between the product and the cache
+(`position`).
 """
 
 import argparse
@@ -45,17 +47,23 @@ class AttentionBlock:
         """q, k and v of x [tokens, hidden], as views [tokens, heads, head_dim] of one product."""
         return self.qkv(x, self.workspace).view(x.shape[0], sum(self.heads), self.head_dim).split(self.heads, dim=1)
 
-    def attend(self, x, slots, block_table, seq_lens, q_offsets=None, max_q=1, window=0):
-        """The heads' outputs [tokens, num_q_heads, head_dim]; x's K and V enter the cache at `slots`."""
+    def attend(self, x, slots, block_table, seq_lens, q_offsets=None, max_q=1, window=0, position=None):
+        """The heads' outputs [tokens, num_q_heads, head_dim]; x's K and V enter
+        the cache at `slots`.  `position`, if given, is called with q and k
+        ([tokens, heads, head_dim], views that it may change in place) and
+        returns them with their positions encoded."""
         q, k, v = self.project(x)
+        if position is not None:
+            q, k = position(q, k)
         self.cache.append(k, v, slots, self.workspace)
         return self.cache.attention(q, block_table, seq_lens, q_offsets, max_q, window=window,
                                     workspace=self.workspace)
 
-    def __call__(self, x, slots, block_table, seq_lens, q_offsets=None, max_q=1, window=0):
+    def __call__(self, x, slots, block_table, seq_lens, q_offsets=None, max_q=1, window=0, position=None):
         """Attention over the cached tokens and x's own, [tokens, hidden].
-        Arguments as :func:`binding.kv_attention`; `seq_lens` counts x's tokens."""
-        heads = self.attend(x, slots, block_table, seq_lens, q_offsets, max_q, window)
+        Arguments as :func:`binding.kv_attention`; `seq_lens` counts x's
+        tokens; `position` as :meth:`attend`."""
+        heads = self.attend(x, slots, block_table, seq_lens, q_offsets, max_q, window, position)
         return self.o(heads.view(x.shape[0], -1), self.workspace)
 
 
