@@ -1113,20 +1113,34 @@ size_t kv_attention_workspace(int head_dim, int num_sms) {
 }
 
 cudaError_t launch_kv_attention(const KvAttnArgs& a, int num_sms, cudaStream_t stream) {
-  // By the rows of a K/V head in the longest sequence.  This kernel's work grows
-  // with them, the tensor-memory kernel's is a 128-row tile's whatever they are.
-  // Us here / there for 24 ragged contexts of up to 4096 tokens (group 8):
-  //   rows                            16    32    48    any (there)
-  //   8 heads of 64                   34    47    61    55
-  //   8 heads of 128                  47    69    96    88
-  //   2 contexts of 60000, of 128     42    62    79    82
-  // and at 96 rows of heads of 64 106 here, 87 there.
+  // By the rows of a K/V head in a sequence, on average: this kernel's work grows
+  // with the rows of all sequences, the tensor-memory kernel's is a 128-row
+  // tile's for each sequence whatever its rows are.  Us here / there, NVFP4,
+  // group 8, ragged contexts of up to 4096 tokens, 8 K/V heads:
+  //   rows of every sequence       32        40        48        64
+  //    8 sequences, heads of 64   30 / 34   30 / 34   31 / 34   35 / 34
+  //    8 sequences, of 128        36 / 45   35 / 46   36 / 46   44 / 46
+  //   24 sequences, heads of 64   41 / 46   51 / 46   52 / 46   62 / 46
+  //   24 sequences, of 128        55 / 65   74 / 66   75 / 66   95 / 67
+  //   64 to 8192 tokens, of 128  211 / 256 308 / 258 309 / 258 406 / 258
+  //   and ragged, on average       27        34        40
+  //   24 sequences, heads of 64   40 / 45   40 / 46
+  //   24 sequences, of 128        51 / 62   57 / 62
+  //   64 sequences, of 128                           154 / 142
+  // (MXFP4 alike: 24 of 48 rows 59 / 54 and 85 / 82.)  One prompt piece of 200
+  // tokens among 63 single ones (33 rows on average) 68 / 120 and 98 / 161.
+  // With fewer (sequence, head) pairs than SMs contexts are cut, and the limit
+  // is higher; two contexts of 60000 are the exception (74 / 68 at 40 rows).  The
+  // longest sequence counts too, lest a long prompt in a batch that is padded
+  // with empty sequences come here.
   // Up to 8 rows the one-column instance: three CTAs of it fit an SM, two of
-  // the other.  64 ragged contexts up to 8192 take 71 us, 102 with two columns,
+  // the other.  64 ragged contexts up to 8192 take 70 us, 102 with two columns,
   // one of 131071 39 and 52.  Groups beyond 128 heads have no tile of whole
   // tokens in the other kernel.
   const int64_t rows = a.max_q * a.group;
-  if (rows > 48 && a.group <= kKvPromptGroup) return launch_kv_prompt(a, num_sms, stream);
+  const int64_t limit = static_cast<int64_t>(a.batch) * a.cache.heads <= num_sms ? 48 : 36;
+  const bool few = a.total_q * a.group <= limit * a.batch && rows <= 2048;
+  if (!few && a.group <= kKvPromptGroup) return launch_kv_prompt(a, num_sms, stream);
   return kv_dispatch(a.cache.head_dim, a.cache.fmt, true, [&](auto d, auto f, auto) {
     if (rows <= 8) return launch_as<d, f, 1>(a, num_sms, stream);
     return launch_as<d, f, 2>(a, num_sms, stream);

@@ -397,8 +397,8 @@ typedef struct petit_kv_attention {
   const int32_t* q_offsets;   /* (device) [batch + 1], or NULL */
   int64_t batch;              /* 0..2^20; 0 enqueues nothing */
   int64_t total_q;            /* query rows; batch * max_q if q_offsets is NULL */
-  int64_t max_q;              /* most query rows of a sequence (chooses the kernel;
-                                 longer sequences are still right) */
+  int64_t max_q;              /* most query rows of a sequence (with total_q and batch it
+                                 chooses the kernel; longer sequences are still right) */
   int64_t max_pages;          /* max_pages * page_size <= 2^30 */
   int64_t table_stride;       /* entries between rows of block_table, >= max_pages */
   int32_t num_q_heads;        /* a multiple of num_kv_heads */
