@@ -44,6 +44,13 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return reinterpret_cast<const float2&>(r);
 }
 
+// Adds the two FP16 of w to two FP32 sums, without a conversion between.
+__device__ __forceinline__ void add_f16x2(float2& sum, uint32_t w) {
+  asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tadd.rn.f32.f16 %0, a, %0;\n\tadd.rn.f32.f16 %1, b, %1;\n\t}"
+      : "+f"(sum.x), "+f"(sum.y)
+      : "r"(w));
+}
+
 // FP16x2 of 2^(lo + 9) and 2^(hi + 9), for lo, hi <= 3: through FP32's exponent
 // field, whose conversion makes subnormals and zero of what is below FP16.
 __device__ __forceinline__ uint32_t f16x2_power(int lo, int hi) {

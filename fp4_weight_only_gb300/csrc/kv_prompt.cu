@@ -285,7 +285,7 @@ struct Smem {
 template <int D>
 __host__ __device__ constexpr size_t partial_floats() { return static_cast<size_t>(kRows) * (D + 2); }
 
-template <int D, int FMT>
+template <int D, int FMT, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_constant__ KvAttnArgs a) {
   using S = Smem<D>;
   using G = KvGroup<D, FMT>;
@@ -684,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
             const uint32_t wd[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float2 v = unpack2(wd[e], a.bf16);
+              const float2 v = unpack2(wd[e], BF16);
               amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
             }
           }
@@ -698,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
             uint32_t o[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float2 v = unpack2(wd[e], a.bf16);
+              const float2 v = unpack2(wd[e], BF16);
               o[e] = pack_f16(v.x * up, v.y * up);
             }
             *reinterpret_cast<uint4*>(&sm.q[q][j >> 3][row_in * 128 + (((j & 7) ^ (row_in & 7)) << 4)]) =
@@ -808,8 +808,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
               for (int e = 0; e < 16; ++e) {
                 const float2 y = fma2(make_float2(x[2 * e], x[2 * e + 1]), fc2, ref2);
                 const float2 pe = make_float2(ex2(y.x), ex2(y.y));
-                sum = add2(sum, pe);
                 p[e] = pack_f16(pe.x, pe.y);
+                // FP16 outputs: the sum is of the rounded weights, so that what
+                // rounding does to the keys with most of a row's weight cancels:
+                // errors are 1.3 times an exact product's, 1.4 to 1.5 with the
+                // sum of the unrounded, which BF16's own rounding hides (8 bits)
+                // and which takes 1.42 ms in place of 1.49 (4096-token piece)
+                if constexpr (BF16)
+                  sum = add2(sum, pe);
+                else
+                  add_f16x2(sum, p[e]);
               }
               tmem_st_x16(s_tmem + 16 * at, p);
             };
@@ -888,9 +896,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
 #pragma unroll
         for (int e = 0; e < 2; ++e)
           reinterpret_cast<uint4*>(dst)[e] =
-              make_uint4(pack2(x[8 * e] * inv, x[8 * e + 1] * inv, a.bf16), pack2(x[8 * e + 2] * inv, x[8 * e + 3] * inv, a.bf16),
-                         pack2(x[8 * e + 4] * inv, x[8 * e + 5] * inv, a.bf16),
-                         pack2(x[8 * e + 6] * inv, x[8 * e + 7] * inv, a.bf16));
+              make_uint4(pack2(x[8 * e] * inv, x[8 * e + 1] * inv, BF16), pack2(x[8 * e + 2] * inv, x[8 * e + 3] * inv, BF16),
+                         pack2(x[8 * e + 4] * inv, x[8 * e + 5] * inv, BF16),
+                         pack2(x[8 * e + 6] * inv, x[8 * e + 7] * inv, BF16));
       };
       auto store_lse = [&](float M, float L) {
         if (a.lse) a.lse[out_row * (static_cast<int64_t>(a.cache.heads) * a.group) + head] = lse_of(M, L);
@@ -1024,13 +1032,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
   }
 }
 
-template <int D, int FMT>
+template <int D, int FMT, bool BF16>
 cudaError_t launch_as(const KvAttnArgs& a, int num_sms, cudaStream_t stream) {
   // more than half of an SM's shared memory, whatever D is: one CTA an SM, and
   // none of a GEMM's CTAs beside it (both allocate all of tensor memory)
   constexpr size_t kSmem = sizeof(Smem<D>) > 120 * 1024 ? sizeof(Smem<D>) : 120 * 1024;
-  if (cudaError_t e = kv_allow_smem<kv_prompt_kernel<D, FMT>>(a.device, kSmem)) return e;
-  kv_prompt_kernel<D, FMT><<<num_sms < kKvPromptCtas ? num_sms : kKvPromptCtas, kThreads, kSmem, stream>>>(a);
+  if (cudaError_t e = kv_allow_smem<kv_prompt_kernel<D, FMT, BF16>>(a.device, kSmem)) return e;
+  kv_prompt_kernel<D, FMT, BF16><<<num_sms < kKvPromptCtas ? num_sms : kKvPromptCtas, kThreads, kSmem, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -1042,8 +1050,8 @@ size_t kv_prompt_partials(int head_dim, int num_sms) {
 }
 
 cudaError_t launch_kv_prompt(const KvAttnArgs& a, int num_sms, cudaStream_t stream) {
-  return kv_dispatch(a.cache.head_dim, a.cache.fmt, true,
-                     [&](auto d, auto f, auto) { return launch_as<d, f>(a, num_sms, stream); });
+  return kv_dispatch(a.cache.head_dim, a.cache.fmt, a.bf16,
+                     [&](auto d, auto f, auto b) { return launch_as<d, f, b>(a, num_sms, stream); });
 }
 
 }  // namespace petit

@@ -374,7 +374,8 @@ petit_status_t petit_kv_read(const petit_kv_cache_t* cache, const int64_t* slots
  * A query that sees no key (len = 0, or p < 0) gets out = 0 and lse = -inf.
  * Products are FP16 by FP16 with FP32 sums: q takes a power of two per row
  * (exact but for elements 2^26 below the row's largest), the softmax's weights
- * are rounded to 11 bits, and values of an MXFP4 cache lose bits only where
+ * are rounded to 11 bits (those 2^-21 and less of the row's largest to a
+ * multiple of 2^-31 of it), and values of an MXFP4 cache lose bits only where
  * their scale lies 2^32 or more below the largest among the sequence's keys
  * that queries of the call see (one query's reference counts keys that only
  * another of them sees).

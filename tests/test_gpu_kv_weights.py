@@ -43,3 +43,15 @@ def test_weights_made_before_the_maximum_rose(cuda_lib, fmt, nq, at, bits):
     q = torch.zeros((nq, 1, dim), dtype=torch.float16, device="cuda")
     q[..., 0] = 1.0
     pool.run(q, [nq], [list(range(pages))], [n], scale=float(bits * np.log(2.0) / pool.k[at, 0, 0]))
+
+
+@pytest.mark.parametrize("fmt,dim", [("nvfp4", 128), ("mxfp4", 128), ("nvfp4", 64), ("mxfp4", 64)])
+@pytest.mark.parametrize("nq,group", [(1, 8), (3, 4), (64, 1), (90, 4)])
+def test_a_query_that_sees_one_key_gets_its_value(cuda_lib, fmt, dim, nq, group):
+    """Whatever its weight is rounded to, it is the sum too.  FP16: rounded once
+    (2^-11), after a division and a product in FP32 (2^-24 each, and g's)."""
+    pool = Pool(cuda_lib, 3, 2, dim, fmt, 64, seed=nq)
+    q = pool.queries(nq, group, torch.float16)
+    out, _ = pool.run(q, [nq], [[0, 1, 2]], [100 + nq - 10], window=1)
+    want = np.repeat(pool.v[90:90 + nq], group, axis=1)
+    assert (np.abs(out.double().cpu().numpy() - want) <= np.abs(want) * (2.0 ** -11 + 2.0 ** -22)).all()
