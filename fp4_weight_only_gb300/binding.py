@@ -514,8 +514,8 @@ def kv_append(cache, k, v, slots, workspace=None):
     """Quantise rows k and v ([tokens, num_kv_heads, head_dim], BF16 or FP16,
     any token and head stride that is a multiple of 8) and write token i to
     slot slots[i] (int64; slot = page * page_size + offset).  Negative slots
-    are skipped; a slot past the cache is skipped and recorded in `workspace`
-    (see :meth:`Workspace.status`) if one is given."""
+    are skipped; a slot past the cache is skipped and, if a `workspace` is
+    given, recorded in it (see :meth:`Workspace.status`)."""
     if k.dtype not in _DTYPES:
         raise ValueError("k: need BF16 or FP16")
     n = k.shape[0]
@@ -561,7 +561,9 @@ def kv_attention(cache, q, block_table, seq_lens, q_offsets=None, max_q=1, scale
     window > 0 keeps the nearest `window` of them (pages whose keys no query
     sees may have been given back: any entry will do).  lse: an FP32 tensor
     [total_q, num_q_heads] that receives the log of the softmax's sum.  A
-    query that sees no key gives zeros (and an lse of -inf)."""
+    query that sees no key gives zeros (and an lse of -inf).  workspace: keep
+    one; without it a call makes and zero-fills one of its own (some 40 MB),
+    and what it records of lengths and pages out of range is lost with it."""
     if q.dtype not in _DTYPES or q.dim() != 3:
         raise ValueError("q: need a BF16 or FP16 tensor [total_q, num_q_heads, head_dim]")
     total_q, heads = q.shape[0], q.shape[1]

@@ -40,14 +40,16 @@
 // maximum, and meet when the CTA leaves an item.  Items cut between CTAs leave
 // FP32 partials, and the last CTA to arrive adds them in CTA order.
 //
-// Measured, 8 K/V heads of 128: one sequence of 1000 tokens 8.9 us (launch,
+// Measured, 8 K/V heads of 128: one sequence of 1000 tokens 9 us (launch,
 // range, one tile a warp and the join), of 131071 39 us (3.8 TB/s: 24 us of
 // streaming at the 6.2 TB/s that reads alone reach, the rest is the first
 // copies' latency and the join); 64 ragged sequences up to 8192 in NVFP4 71 us
-// (4.3 TB/s); 160 up to 16000 in MXFP4 with 4 query heads a K/V head 316 us
-// (4.5 TB/s).  What holds the last two is issuing: some 350 warp instructions
-// for 16 keys of a head, 71 of them conversions and 170 FP16 scale products
-// and byte selection.
+// (4.3 TB/s), in MXFP4 80; 160 up to 16000 in MXFP4 with 4 query heads a K/V
+// head 321 us (4.4 TB/s).  What holds the last two is latency at 15 warps an
+// SM: some 350 warp instructions for 16 keys of a head (71 of them conversions
+// and 170 FP16 scale products and byte selection), issued in 55 % of the cycles,
+// with waits for their own results as the first stall and no unit near its rate
+// (ALU 47 %, tensor cores 23 %, DRAM 53 %).
 #include <cfloat>
 #include <climits>
 #include <cuda_bf16.h>

@@ -26,10 +26,10 @@
 // item cut between CTAs leaves FP32 partials that the last arriver adds.
 //
 // Measured: 4096 new tokens behind 12288, 64 query heads of 128 over 8 NVFP4
-// heads, 1.43 ms, 1.35 PFLOP/s (70 % of a cuBLAS product's rate; MXFP4 1.62 ms):
-// a softmax warpgroup's pass over 128 x 128 scores is the longest stage, the
-// tensor pipe is busy 56 % of the time.  Five ragged pieces of 3 to 1100 tokens
-// with a window of 1024, heads of 64, MXFP4, 64 us:
+// heads, 1.43 ms, 1.34 PFLOP/s (70 % of a cuBLAS product's rate; MXFP4 1.63 ms,
+// FP16 outputs 1.49): a softmax warpgroup's pass over 128 x 128 scores is the
+// longest stage, the tensor pipe is busy 52 % of the time.  Five ragged pieces of
+// 3 to 1100 tokens with a window of 1024, heads of 64, MXFP4, FP16, 65 us:
 // an item's beginning and end (8 to 10 k cycles) next to 13 tiles.
 #include <cfloat>
 #include <cuda_bf16.h>
@@ -674,6 +674,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
           }
           cp_async_wait_all();
           __syncwarp();
+          // (the row stays in registers for the second pass, at some 400 bytes of
+          // spills an item at D = 128: read again from shared memory it takes 92,
+          // and the 4096-token piece 1.455 ms in place of 1.436)
           uint4 x[D / 8];
 #pragma unroll
           for (int j = 0; j < D / 8; ++j)
