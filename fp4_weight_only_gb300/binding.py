@@ -9,6 +9,7 @@ there is no CPU fallback.
 import contextlib
 import ctypes
 import functools
+import math
 import os
 import threading
 
@@ -70,6 +71,23 @@ class KvAttentionArgs(ctypes.Structure):
                 ("window", _c_i64)]
 
 
+class RmsNormArgs(ctypes.Structure):
+    """petit_rms_norm_t"""
+    _fields_ = [("x", _c_p), ("residual", _c_p), ("weight", _c_p), ("sum", _c_p), ("out", _c_p), ("scales", _c_p),
+                ("rows", _c_i64), ("dim", _c_i64), ("x_stride", _c_i64), ("residual_stride", _c_i64),
+                ("sum_stride", _c_i64), ("out_stride", _c_i64), ("scale_stride", _c_i64),
+                ("dtype", ctypes.c_int32), ("weight_f32", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("group", ctypes.c_int32)]
+
+
+class RotaryArgs(ctypes.Structure):
+    """petit_rotary_t"""
+    _fields_ = [("q", Rows), ("k", Rows), ("q_out", Rows), ("k_out", Rows), ("turns", _c_p), ("positions", _c_p),
+                ("num_tokens", _c_i64), ("num_q_heads", ctypes.c_int32), ("num_k_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("positions_32", ctypes.c_int32), ("magnitude", ctypes.c_float)]
+
+
 # name -> (restype, argtypes)
 SIGNATURES = {
     "petit_layout_version": (ctypes.c_int, []),
@@ -115,6 +133,9 @@ SIGNATURES = {
     "petit_kv_read": (ctypes.c_int, [_c_p, _c_p, _c_i64, _c_p, _c_p, ctypes.c_int, _c_p, _c_sz, _c_p]),
     "petit_kv_attention_workspace_bytes": (_c_sz, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int]),
     "petit_kv_attention": (ctypes.c_int, [_c_p, _c_p, _c_p, _c_sz, _c_p]),
+    "petit_rms_norm": (ctypes.c_int, [_c_p, _c_p]),
+    "petit_rotary_turns": (_c_i64, [ctypes.c_double]),
+    "petit_rotary": (ctypes.c_int, [_c_p, _c_p]),
     "petit_device_limits": (ctypes.c_int, [ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int)]),
 }
 
@@ -191,6 +212,13 @@ def _stream():
     if _raw_stream is not None:
         return _raw_stream(torch.cuda.current_device())
     return torch.cuda.current_stream().cuda_stream
+
+
+def _stream_on(index):
+    """The current stream's handle, for calls on tensors of device `index`, which has to be the current one."""
+    if torch.cuda.current_device() != index:
+        raise ValueError(f"need tensors on the current device ({torch.cuda.current_device()}), got device {index}")
+    return _stream()
 
 
 def _ptr(t):
@@ -596,6 +624,159 @@ def kv_attention(cache, q, block_table, seq_lens, q_offsets=None, max_q=1, scale
     buf = ws.ensure(cache.workspace_bytes())
     _check(load().petit_kv_attention(cache._ref, ctypes.byref(args), _ptr(buf), buf.numel(), _stream()),
            "kv_attention")
+    return out
+
+
+# ----------------------------------------- around a decoder layer's products
+def _matrix(t, like, dtype, shape, name):
+    """(address, row stride) of a matrix on like's device whose rows are contiguous."""
+    # (of a dimension of one, torch's stride says nothing)
+    if (t.dtype is dtype and t.shape == shape and t.get_device() == like.get_device()
+            and (t.stride(1) == 1 or shape[1] == 1)):
+        return t.data_ptr(), t.stride(0) if shape[0] > 1 else 0
+    raise ValueError(f"{name}: need a {dtype} tensor {list(shape)} on x's device, contiguous in its last dimension")
+
+
+def _rms_norm(x, weight, eps, residual, sum_out, out, scales, group, where):
+    dtype = _DTYPES.get(x.dtype)
+    if dtype is None or x.dim() != 2 or not x.is_cuda or x.stride(1) != 1:
+        raise ValueError("x: need a BF16 or FP16 CUDA tensor [rows, dim], contiguous in its last dimension")
+    shape = x.shape
+    rows, dim = shape
+    xp, xs = _matrix(x, x, x.dtype, shape, "x")
+    rp, rs = (None, 0) if residual is None else _matrix(residual, x, x.dtype, shape, "residual")
+    sp, ss = (None, 0) if sum_out is None else _matrix(sum_out, x, x.dtype, shape, "sum_out")
+    f32, wp = 0, None
+    if weight is not None:
+        f32 = int(weight.dtype is torch.float32)
+        if ((not f32 and weight.dtype is not x.dtype) or weight.shape != (dim,) or not weight.is_contiguous()
+                or weight.get_device() != x.get_device()):
+            raise ValueError(f"weight: need a contiguous {x.dtype} or FP32 tensor [{dim}] on x's device")
+        wp = weight.data_ptr()
+    op, os_ = _matrix(out, x, x.dtype if scales is None else torch.float8_e4m3fn, shape, "out")
+    cp, cs = (None, 0) if scales is None else _matrix(scales, x, torch.float32, (rows, dim // (group or dim)), "scales")
+    args = RmsNormArgs(xp, rp, wp, sp, op, cp, rows, dim, xs, rs, ss, os_, cs, dtype, f32, eps, group)
+    _check(load().petit_rms_norm(ctypes.byref(args), _stream_on(x.get_device())), where)
+
+
+def rms_norm(x, weight=None, eps=1e-6, residual=None, out=None, sum_out=None):
+    """y = s * (mean(s^2) + eps)^(-1/2) * weight over the rows of s = x +
+    residual, [rows, dim] in BF16 or FP16 (any row stride that is a multiple of
+    8; dim a multiple of 8, at most 32768), computed in FP32 and rounded once.
+    `weight`: x's type or FP32, [dim]; None: ones.  Returns y, or (y, s rounded)
+    if there is a residual.  `out` may be x, `sum_out` x or residual."""
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if sum_out is None and residual is not None:
+        sum_out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _rms_norm(x, weight, eps, residual, sum_out, out, None, 0, "rms_norm")
+    return out if residual is None else (out, sum_out)
+
+
+def rms_norm_e4m3(x, weight=None, eps=1e-6, residual=None, group=128, out=None, scales=None, sum_out=None):
+    """:func:`rms_norm` with y in 8 bits: (codes, scales), or (codes, scales,
+    s rounded) if there is a residual.  codes: float8_e4m3fn [rows, dim];
+    scales: FP32 [rows, dim / group] (group 16, 32, 64, 128 or 256 elements; 0: a
+    whole row), the largest |y| of the group / 448; y is about code * scale."""
+    if x.dim() != 2 or group < 0 or (group and x.shape[1] % group):
+        raise ValueError(f"x, group: need [rows, dim] with dim a multiple of the group, got {tuple(x.shape)}, {group}")
+    if out is None:
+        out = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+    if scales is None:
+        scales = torch.empty((x.shape[0], x.shape[1] // (group or x.shape[1])), dtype=torch.float32, device=x.device)
+    if sum_out is None and residual is not None:
+        sum_out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _rms_norm(x, weight, eps, residual, sum_out, out, scales, group, "rms_norm_e4m3")
+    return (out, scales) if residual is None else (out, scales, sum_out)
+
+
+def rotary_frequencies(rot_dim, base=10000.0, factor=1.0, kind="linear", context=8192, low=1.0, high=4.0):
+    """Radians a position of the rot_dim / 2 pairs, base ** (-2 i / rot_dim),
+    for a context `factor` times the one that a model learned (`context`):
+
+    "linear": every frequency divided by `factor`;
+    "bands": those that turn less than `low` times within `context` are divided,
+        those that turn more than `high` times kept, between them by the turns;
+    "ramp": the same ends, between them by the pair's index."""
+    if rot_dim < 2 or rot_dim % 2 or not base > 1.0 or not factor > 0.0:
+        raise ValueError("rotary_frequencies: need an even rot_dim, base > 1 and factor > 0")
+    half = rot_dim // 2
+    f = [base ** (-i / half) for i in range(half)]
+    if kind == "linear":
+        return [v / factor for v in f]
+    if kind not in ("bands", "ramp") or not 0.0 < low < high or not context > 0:
+        raise ValueError("rotary_frequencies: need kind 'linear', 'bands' or 'ramp' and 0 < low < high")
+    if kind == "bands":
+        keep = [(context * v / (2 * math.pi) - low) / (high - low) for v in f]
+    else:   # the (fractional) pair that turns so many times within the context
+        last, first = (half * math.log(context / (2 * math.pi * n)) / math.log(base) for n in (low, high))
+        keep = [(last - i) / (last - first) for i in range(half)]
+    keep = [min(1.0, max(0.0, v)) for v in keep]
+    return [k * v + (1.0 - k) * v / factor for k, v in zip(keep, f)]
+
+
+class Rotary:
+    """Rotary positions of the first `rot_dim` elements of a head, in pairs of
+    neighbours (`interleaved`) or of elements rot_dim / 2 apart.  `frequencies`:
+    radians a position of each pair (numbers or a tensor; by default
+    :func:`rotary_frequencies` of `base`); angles are exact modulo a turn at any
+    position.  `magnitude` multiplies the turned elements."""
+
+    def __init__(self, rot_dim, base=10000.0, frequencies=None, interleaved=False, magnitude=1.0, device=None):
+        if frequencies is None:
+            frequencies = rotary_frequencies(rot_dim, base)
+        elif isinstance(frequencies, torch.Tensor):
+            device = device or (frequencies.device if frequencies.is_cuda else None)
+            frequencies = frequencies.double().tolist()
+        if rot_dim < 2 or rot_dim % 2 or len(frequencies) != rot_dim // 2:
+            raise ValueError(f"frequencies: need {rot_dim // 2}, one for each pair of an even rot_dim")
+        if not all(math.isfinite(f) for f in frequencies) or not math.isfinite(magnitude):
+            raise ValueError("frequencies, magnitude: need finite numbers")
+        turns = load().petit_rotary_turns
+        self.turns = torch.tensor([turns(f) for f in frequencies], dtype=torch.int64,
+                                  device=torch.device(device or "cuda"))
+        self.rot_dim, self.interleaved, self.magnitude = rot_dim, bool(interleaved), float(magnitude)
+        self.device_index = self.turns.get_device()
+
+    def __call__(self, q, k, positions, out=None):
+        return rotary(self, q, k, positions, out)
+
+
+def _heads(t, rope, like, name):
+    """petit_rows_t of [tokens, heads, head_dim] on the frequencies' device, contiguous in its last dimension."""
+    if (t.dim() == 3 and t.dtype is like.dtype and t.shape[0] == like.shape[0] and t.shape[2] == like.shape[2]
+            and t.stride(2) == 1 and t.get_device() == rope.device_index):
+        # (of a dimension of one, torch's stride says nothing)
+        return Rows(t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0)
+    raise ValueError(f"{name}: need a {like.dtype} tensor [{like.shape[0]}, heads, {like.shape[2]}] on the "
+                     f"frequencies' device, contiguous in its last dimension")
+
+
+def rotary(rope, q, k, positions, out=None):
+    """q and k ([tokens, heads, head_dim], BF16 or FP16, any token and head
+    stride that is a multiple of 8; k may be None) turned by their tokens'
+    `positions` (int64 or int32 [tokens]).  `rope`: a :class:`Rotary`.  Returns
+    (q, k) as new tensors, or in `out`, a pair of such tensors: (q, k) itself
+    turns them in place."""
+    if q.dtype not in _DTYPES or q.dim() != 3:
+        raise ValueError("q: need a BF16 or FP16 tensor [tokens, heads, head_dim]")
+    n = q.shape[0]
+    if out is None:
+        out = tuple(None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k))
+    rq, ro = _heads(q, rope, q, "q"), _heads(out[0], rope, q, "out[0]")
+    rk = rko = Rows()
+    if k is not None:
+        rk, rko = _heads(k, rope, q, "k"), _heads(out[1], rope, q, "out[1]")
+    if out[0].shape != q.shape or (k is not None and out[1].shape != k.shape):
+        raise ValueError("out: need tensors of q's and k's shapes")
+    wide = positions.dtype is torch.int64
+    if ((not wide and positions.dtype is not torch.int32) or positions.shape != (n,) or not positions.is_contiguous()
+            or positions.get_device() != rope.device_index):
+        raise ValueError(f"positions: need a contiguous int64 or int32 tensor [{n}] on the frequencies' device")
+    args = RotaryArgs(rq, rk, ro, rko, rope.turns.data_ptr(), positions.data_ptr(), n, q.shape[1],
+                      0 if k is None else k.shape[1], q.shape[2], rope.rot_dim, _DTYPES[q.dtype], rope.interleaved,
+                      not wide, rope.magnitude)
+    _check(load().petit_rotary(ctypes.byref(args), _stream_on(rope.device_index)), "rotary")
     return out
 
 

@@ -1,0 +1,143 @@
+// C ABI of the operators around a decoder layer's products: argument
+// validation and kernel dispatch.  Validation always comes first and never
+// touches the GPU, so a rejected call enqueues nothing.
+#include <cmath>
+
+#include "../../include/petit.h"
+#include "internal.h"
+#include "layer.h"
+
+namespace {
+
+constexpr int64_t kMaxTokens = int64_t(1) << 24;
+constexpr int64_t kMaxNormDim = 32768;
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+petit_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? PETIT_OK : PETIT_ERR_CUDA; }
+
+petit_status_t check_rows(const petit_rows_t& r, petit::KvRows* out) {
+  if (!r.data) return PETIT_ERR_INVALID_ARG;
+  if (!aligned(r.data, 16) || r.token_stride % 8 || r.head_stride % 8) return PETIT_ERR_MISALIGNED;
+  *out = {r.data, r.token_stride, r.head_stride};
+  return PETIT_OK;
+}
+
+// Rows to read and rows to write: `out` has rows of its own, or is `in` itself.
+petit_status_t check_turned(const petit_rows_t& in, const petit_rows_t& out, const petit_rotary_t& r, int32_t heads,
+                            petit::KvRows* in_rows, petit::KvRows* out_rows) {
+  if (petit_status_t st = check_rows(in, in_rows)) return st;
+  if (petit_status_t st = check_rows(out, out_rows)) return st;
+  auto apart = [&](int64_t stride, int64_t count) { return count <= 1 || stride >= r.head_dim || stride <= -r.head_dim; };
+  if (!apart(out.token_stride, r.num_tokens) || !apart(out.head_stride, heads)) return PETIT_ERR_INVALID_ARG;
+  if (in.data == out.data && ((r.num_tokens > 1 && in.token_stride != out.token_stride) ||
+                              (heads > 1 && in.head_stride != out.head_stride)))
+    return PETIT_ERR_INVALID_ARG;
+  return PETIT_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+petit_status_t petit_rms_norm(const petit_rms_norm_t* args, petit_stream_t stream) {
+  if (!args || args->rows < 0 || args->dim < 1 || (args->dtype != PETIT_BF16 && args->dtype != PETIT_F16) ||
+      (args->weight_f32 != 0 && args->weight_f32 != 1) || !(args->eps >= 0.0f) || !std::isfinite(args->eps))
+    return PETIT_ERR_INVALID_ARG;
+  if (args->dim % 8 || args->dim > kMaxNormDim || args->rows > kMaxTokens) return PETIT_ERR_UNSUPPORTED_SHAPE;
+  int64_t group = args->dim;
+  if (args->scales && args->group != 0) {
+    group = args->group;
+    if (group < 16 || group > 256 || (group & (group - 1)) || args->dim % group) return PETIT_ERR_UNSUPPORTED_SHAPE;
+  } else if (args->group != 0 && args->rows > 0) {
+    return PETIT_ERR_INVALID_ARG;   // a group of nothing
+  }
+  if (args->rows == 0) return PETIT_OK;
+  if (!args->x || !args->out) return PETIT_ERR_INVALID_ARG;
+  if (args->rows > 1) {   // rows of their own to write to
+    if (args->out_stride < args->dim || (args->sum && args->sum_stride < args->dim) ||
+        (args->scales && args->scale_stride < args->dim / group))
+      return PETIT_ERR_INVALID_ARG;
+  }
+  // an output in an input's place has its rows where the input has them
+  auto in_place = [&](const void* p, int64_t stride) {
+    return (p != args->x || args->rows == 1 || stride == args->x_stride) &&
+           (p != args->residual || args->rows == 1 || stride == args->residual_stride);
+  };
+  if (args->out == args->sum || !in_place(args->out, args->out_stride) ||
+      (args->sum && !in_place(args->sum, args->sum_stride)) ||
+      (args->scales && (args->out == args->x || args->out == args->residual)))
+    return PETIT_ERR_INVALID_ARG;
+  if (!aligned(args->x, 16) || !aligned(args->residual, 16) || !aligned(args->weight, 16) || !aligned(args->sum, 16) ||
+      !aligned(args->out, 16) || !aligned(args->scales, 4) || args->x_stride % 8 ||
+      (args->residual && args->residual_stride % 8) || (args->sum && args->sum_stride % 8) || args->out_stride % 8)
+    return PETIT_ERR_MISALIGNED;
+  if (int st = petit::usable_device(nullptr)) return static_cast<petit_status_t>(st);
+  petit::NormArgs a{};
+  a.x = static_cast<const uint16_t*>(args->x);
+  a.residual = static_cast<const uint16_t*>(args->residual);
+  a.weight = args->weight;
+  a.sum = static_cast<uint16_t*>(args->sum);
+  a.out = args->out;
+  a.scales = args->scales;
+  a.rows = args->rows;
+  a.x_stride = args->x_stride;
+  a.residual_stride = args->residual_stride;
+  a.sum_stride = args->sum_stride;
+  a.out_stride = args->out_stride;
+  a.scale_stride = args->scale_stride;
+  a.dim = static_cast<int32_t>(args->dim);
+  a.group = static_cast<int32_t>(group);
+  a.eps = args->eps;
+  a.weight_f32 = args->weight_f32 != 0;
+  return from_cuda(petit::launch_rms_norm(a, args->dtype == PETIT_BF16, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int64_t petit_rotary_turns(double frequency) {
+  if (!std::isfinite(frequency)) return 0;
+  // a whole number of turns a position is none
+  const double t = frequency * 0.15915494309189533577;   // 1 / (2 pi)
+  const double part = t - std::nearbyint(t);              // -0.5 .. 0.5, exact
+  return part >= 0.5 ? INT64_MIN : static_cast<int64_t>(part * 18446744073709551616.0);
+}
+
+petit_status_t petit_rotary(const petit_rotary_t* args, petit_stream_t stream) {
+  if (!args || args->num_tokens < 0 || args->num_q_heads < 0 || args->num_k_heads < 0 ||
+      (args->dtype != PETIT_BF16 && args->dtype != PETIT_F16) || (args->interleaved != 0 && args->interleaved != 1) ||
+      (args->positions_32 != 0 && args->positions_32 != 1) || !std::isfinite(args->magnitude))
+    return PETIT_ERR_INVALID_ARG;
+  const int64_t heads = static_cast<int64_t>(args->num_q_heads) + args->num_k_heads;
+  if (args->head_dim < 8 || args->head_dim > 1024 || args->head_dim % 8 || args->rot_dim < 2 || args->rot_dim % 2 ||
+      args->rot_dim > args->head_dim || heads < 1 || heads > 4096 || args->num_tokens > kMaxTokens ||
+      args->num_tokens * heads >= int64_t(1) << 31 ||
+      args->num_tokens * heads * args->head_dim > int64_t(1) << 36)
+    return PETIT_ERR_UNSUPPORTED_SHAPE;
+  if (args->num_tokens == 0) return PETIT_OK;
+  petit::RotaryArgs a{};
+  bool other = false;   // some rows go elsewhere
+  if (args->num_q_heads > 0) {
+    if (petit_status_t st = check_turned(args->q, args->q_out, *args, args->num_q_heads, &a.q, &a.q_out)) return st;
+    other |= a.q.data != a.q_out.data;
+  }
+  if (args->num_k_heads > 0) {
+    if (petit_status_t st = check_turned(args->k, args->k_out, *args, args->num_k_heads, &a.k, &a.k_out)) return st;
+    other |= a.k.data != a.k_out.data;
+  }
+  if (!args->turns || !args->positions) return PETIT_ERR_INVALID_ARG;
+  if (!aligned(args->turns, 8) || !aligned(args->positions, args->positions_32 ? 4 : 8)) return PETIT_ERR_MISALIGNED;
+  if (int st = petit::usable_device(nullptr)) return static_cast<petit_status_t>(st);
+  a.turns = reinterpret_cast<const uint64_t*>(args->turns);
+  a.positions = args->positions;
+  a.tokens = args->num_tokens;
+  a.q_heads = args->num_q_heads;
+  a.heads = static_cast<int32_t>(heads);
+  a.head_dim = args->head_dim;
+  a.rot_dim = args->rot_dim;
+  a.magnitude = args->magnitude;
+  a.positions_32 = args->positions_32 != 0;
+  a.copy_rest = other && args->rot_dim < args->head_dim;
+  return from_cuda(petit::launch_rotary(a, args->interleaved != 0, args->dtype == PETIT_BF16,
+                                        reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -425,6 +425,82 @@ size_t petit_kv_attention_workspace_bytes(int32_t num_kv_heads, int32_t head_dim
 petit_status_t petit_kv_attention(const petit_kv_cache_t* cache, const petit_kv_attention_t* args,
                                   void* workspace, size_t workspace_bytes, petit_stream_t stream);
 
+/* ------------------------------------- around a decoder layer's products */
+
+/* Root-mean-square norm of rows with the residual's addition:
+ *     s = x + residual,   sum = round(s)
+ *     y = s * (mean(s^2) + eps)^(-1/2) * weight
+ * in FP32 (s enters the norm unrounded).  `out` receives y in the rows' type,
+ * or, where `scales` is set, E4M3 codes with an FP32 scale for every `group`
+ * elements of a row (16, 32, 64, 128 or 256; 0: one a row):
+ *     scale = max(max |y|, 1e-8) / 448,   code = E4M3(y / scale)
+ * (nearest even; NaN stays NaN and is left out of the maximum).  Infinities and
+ * sums of squares past FP32 behave as in that arithmetic: such a row's finite
+ * elements become zeros.  `sum` and a 16-bit `out` may be x or residual (the
+ * same address and stride); otherwise outputs do not overlap inputs.
+ * Kernels launched just before may still be running when this one is set up;
+ * it reads and writes only after they have completed. */
+typedef struct petit_rms_norm {
+  const void* x;         /* (device) [rows][dim] 16-bit elements */
+  const void* residual;  /* the same, or NULL */
+  const void* weight;    /* (device) [dim], or NULL: ones */
+  void* sum;             /* [rows][dim] 16-bit elements, or NULL */
+  void* out;             /* [rows][dim] 16-bit elements, or E4M3 codes */
+  float* scales;         /* (device) [rows][dim / group], or NULL: 16-bit output */
+  int64_t rows;          /* 0..2^24; 0 enqueues nothing */
+  int64_t dim;           /* a multiple of 8, at most 32768 */
+  int64_t x_stride;      /* elements between rows, multiples of 8 (scale_stride: any) */
+  int64_t residual_stride;
+  int64_t sum_stride;
+  int64_t out_stride;
+  int64_t scale_stride;
+  int32_t dtype;         /* petit_dtype_t of x, residual, sum and a 16-bit out */
+  int32_t weight_f32;    /* weight: 0: of dtype, 1: FP32 */
+  float eps;             /* >= 0 */
+  int32_t group;
+} petit_rms_norm_t;
+
+/* Errors: INVALID_ARG (also outputs whose rows overlap or are in an input's
+ * place in another way than above), UNSUPPORTED_SHAPE (dim, rows, group),
+ * MISALIGNED, ARCH, CUDA. */
+petit_status_t petit_rms_norm(const petit_rms_norm_t* args, petit_stream_t stream);
+
+/* Rotary positions of query and key heads: pair i of the first rot_dim
+ * elements of a head, (a, b), of the token at position p becomes
+ *     (m (a cos t - b sin t), m (b cos t + a sin t)),   t = p * frequency_i
+ * with m = magnitude.  The pair's elements are 2 i and 2 i + 1 (interleaved), or
+ * i and i + rot_dim / 2.  Elements from rot_dim on stay as they are.
+ * Frequencies are given in 2^-64 turns a position (petit_rotary_turns), so that
+ * angles are exact modulo a turn at any position, negative ones too.
+ * q_out and k_out are q and k themselves (in place) or rows that do not overlap
+ * them.  Either may have no heads; its rows are then not looked at. */
+typedef struct petit_rotary {
+  petit_rows_t q;         /* [num_tokens][num_q_heads][head_dim] */
+  petit_rows_t k;         /* [num_tokens][num_k_heads][head_dim] */
+  petit_rows_t q_out;
+  petit_rows_t k_out;
+  const int64_t* turns;   /* (device) [rot_dim / 2] */
+  const void* positions;  /* (device) [num_tokens] */
+  int64_t num_tokens;     /* 0..2^24; 0 enqueues nothing */
+  int32_t num_q_heads;    /* together 1..4096 */
+  int32_t num_k_heads;
+  int32_t head_dim;       /* a multiple of 8, at most 1024 */
+  int32_t rot_dim;        /* even, at most head_dim */
+  int32_t dtype;          /* petit_dtype_t */
+  int32_t interleaved;    /* 0 or 1 */
+  int32_t positions_32;   /* positions: 0: int64, 1: int32 */
+  float magnitude;
+} petit_rotary_t;
+
+/* A frequency in radians a position as petit_rotary takes it; 0 for one that
+ * is not finite. */
+int64_t petit_rotary_turns(double frequency);
+
+/* Errors: INVALID_ARG (also strides of q_out or k_out below head_dim, or other
+ * ones than the input's where they are in place), UNSUPPORTED_SHAPE (heads,
+ * dimensions, more than 2^24 tokens, 2^31 heads or 2^36 elements over all tokens), MISALIGNED, ARCH, CUDA. */
+petit_status_t petit_rotary(const petit_rotary_t* args, petit_stream_t stream);
+
 /* ------------------------------------------------------------------ tuning */
 
 /* Forces the tile shape of every later GEMM plan in this process, for tile

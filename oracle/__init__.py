@@ -15,10 +15,11 @@ What it computes (sources are the four web pages on the method):
   reference product ``C = g * A . Wq^T`` in float64.
 * ``kv``       -- the 4-bit K/V cache (quantised rows, storage order) and
   attention over it in float64.
+* ``layer``    -- norm, rotary positions and gated projections in float64.
 
 Every function is pinned by ``tests/test_oracle_*.py`` (``-m "not gpu"``)
 against closed forms, library casts, invariants and brute force.  No part of
 the oracle is "parity unpinned".
 """
 
-from . import formats, quantize, gemm, kv  # noqa: F401
+from . import formats, quantize, gemm, kv, layer  # noqa: F401
