@@ -133,6 +133,10 @@ SIGNATURES = {
     "petit_kv_read": (ctypes.c_int, [_c_p, _c_p, _c_i64, _c_p, _c_p, ctypes.c_int, _c_p, _c_sz, _c_p]),
     "petit_kv_attention_workspace_bytes": (_c_sz, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int]),
     "petit_kv_attention": (ctypes.c_int, [_c_p, _c_p, _c_p, _c_sz, _c_p]),
+    "petit_gated_gemm": (ctypes.c_int, [ctypes.c_int, _c_p, _c_p, ctypes.c_float, ctypes.c_float, ctypes.c_int, _c_p,
+                                        _c_i64, _c_i64, _c_i64, _c_p, _c_sz, _c_p]),
+    "petit_moe_gated_gemm": (ctypes.c_int, [ctypes.c_int, _c_p, _c_p, _c_p, _c_p, _c_p, _c_i64, ctypes.c_int, _c_p,
+                                            _c_i64, _c_i64, _c_p, _c_sz, _c_p]),
     "petit_rms_norm": (ctypes.c_int, [_c_p, _c_p]),
     "petit_rotary_turns": (_c_i64, [ctypes.c_double]),
     "petit_rotary": (ctypes.c_int, [_c_p, _c_p]),
@@ -627,6 +631,80 @@ def kv_attention(cache, q, block_table, seq_lens, q_offsets=None, max_q=1, scale
     return out
 
 
+# ------------------------------------------------ gated feed-forward products
+ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
+
+
+def gated_repack(gate_packed, gate_scales, up_packed, up_scales, fmt="nvfp4"):
+    """Packed codes [n, k/2] and scale bytes of the gate and the up matrix -> one
+    repacked buffer for :func:`gated_gemm` (their rows alternate; n % 64 == 0)."""
+    if gate_packed.dim() != 2 or gate_packed.shape != up_packed.shape or gate_scales.shape != up_scales.shape:
+        raise ValueError("gated_repack: need two matrices of one shape")
+    return repack(torch.stack((gate_packed, up_packed), 1).flatten(0, 1),
+                  torch.stack((gate_scales, up_scales), 1).flatten(0, 1), fmt)
+
+
+def _gated_args(A, rep, n, fmt, act, out, rows_k):
+    """(activation number, output) after the checks that the dense and the grouped call share."""
+    dtype = torch.float16 if fmt == "nvfp4_f16" else torch.bfloat16
+    _need(A, dtype, "A")
+    _need(rep, torch.uint8, "rep")
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act: need one of {', '.join(ACTIVATIONS)}")
+    groups, k = rows_k
+    if A.dim() != 2 or rep.numel() < groups * load().petit_repacked_bytes(2 * n, k, FORMATS[fmt]):
+        raise ValueError(f"rep: need {groups} repacked matrices of {2 * n} x {k}")
+    if out is None:
+        out = torch.empty((A.shape[0], n), dtype=dtype, device=A.device)
+    else:
+        _need(out, dtype, "out")
+        if tuple(out.shape) != (A.shape[0], n):
+            raise ValueError(f"out: need shape ({A.shape[0]}, {n})")
+    if rep.get_device() != A.get_device() or out.get_device() != A.get_device():
+        raise ValueError("rep, out: need A's device")
+    return ACTIVATIONS[act], out
+
+
+def gated_gemm(A, rep, n, fmt="nvfp4", global_scales=(1.0, 1.0), act="silu", workspace=None, out=None):
+    """act(g A Wg^T) * (u A Wu^T) in one kernel: [m, n] in BF16 ("nvfp4_f16": FP16,
+    as A), with FP32 sums and one rounding.  rep: :func:`gated_repack`'s;
+    global_scales: (g, u), floats (MXFP4: ones); act: "silu", "gelu" or "gelu_tanh"."""
+    m, k = A.shape
+    number, C = _gated_args(A, rep, n, fmt, act, out, (1, k))
+    need = workspace_bytes(m, 2 * n, k, fmt)
+    if need == 0:
+        raise PetitError(2, "gated workspace size")
+    buf = (workspace or Workspace(A.device)).ensure(need)
+    g, u = global_scales
+    _check(load().petit_gated_gemm(FORMATS[fmt], _ptr(A), _ptr(rep), g, u, number, _ptr(C), m, n, k, _ptr(buf),
+                                   buf.numel(), _stream_on(A.get_device())), "gated_" + fmt)
+    return C
+
+
+def moe_gated_gemm(A, rep, expert_offsets, n, fmt="mxfp4", global_scales=None, act="silu", workspace=None, out=None):
+    """:func:`gated_gemm` for the experts of an MoE layer: rows, offsets and rep
+    (the experts' :func:`gated_repack` buffers back to back) as for
+    :func:`moe_gemm`; global_scales: a host sequence of E pairs (g, u)."""
+    T, k = A.shape
+    E = len(expert_offsets) - 1
+    off = (ctypes.c_int64 * (E + 1))(*[int(x) for x in expert_offsets])
+    if int(off[E]) != T:
+        raise ValueError("expert_offsets[-1] must equal A.shape[0]")
+    number, C = _gated_args(A, rep, n, fmt, act, out, (E, k))
+    L = load()
+    need = int(L.petit_moe_workspace_bytes(off, E, 2 * n, k, FORMATS[fmt]))
+    if need == 0 and T > 0:
+        raise PetitError(2, "moe gated workspace size")
+    buf = (workspace or Workspace(A.device)).ensure(max(need, 256))
+    scales = [(1.0, 1.0)] * E if global_scales is None else global_scales
+    if len(scales) != E:
+        raise ValueError(f"global_scales: need {E} pairs")
+    g, u = ((ctypes.c_float * E)(*column) for column in zip(*scales))
+    _check(L.petit_moe_gated_gemm(FORMATS[fmt], _ptr(A), _ptr(rep), g, u, off, E, number, _ptr(C), n, k, _ptr(buf),
+                                  buf.numel(), _stream_on(A.get_device())), "moe_gated_" + fmt)
+    return C
+
+
 # ----------------------------------------- around a decoder layer's products
 def _matrix(t, like, dtype, shape, name):
     """(address, row stride) of a matrix on like's device whose rows are contiguous."""
@@ -799,3 +877,29 @@ class FP4Weight:
 
     def __call__(self, A, workspace=None, out=None):
         return gemm(A, self.rep, self.n, self.fmt, self.global_scale, workspace, out)
+
+
+class GatedWeight:
+    """The gate and up matrices of a gated feed-forward block ([n, k], BF16 CUDA
+    tensors), quantised and laid out once for :func:`gated_gemm`.
+    `global_scale`: None (1.0), "amax" (each matrix by its own largest value) or
+    a pair of floats."""
+
+    def __init__(self, W_gate, W_up, fmt="nvfp4", global_scale=None):
+        if W_gate.dim() != 2 or W_gate.shape != W_up.shape:
+            raise ValueError("W_gate, W_up: need two matrices of one shape")
+        self.n, self.k = W_gate.shape
+        self.fmt = fmt
+        if fmt == "mxfp4" or global_scale is None:
+            self.global_scales = (1.0, 1.0)
+        elif global_scale == "amax":
+            self.global_scales = tuple(nvfp4_global_scale(absmax(w).item()) for w in (W_gate, W_up))
+        else:
+            self.global_scales = tuple(float(g) for g in global_scale)
+        packed = []
+        for w, g in zip((W_gate, W_up), self.global_scales):
+            packed.extend(quantize(w, "mxfp4" if fmt == "mxfp4" else "nvfp4", g))
+        self.rep = gated_repack(*packed, fmt)
+
+    def __call__(self, A, act="silu", workspace=None, out=None):
+        return gated_gemm(A, self.rep, self.n, self.fmt, self.global_scales, act, workspace, out)

@@ -14,6 +14,8 @@ namespace {
 using petit::kMXFP4;
 using petit::kNVFP4;
 using petit::kNVFP4F16;
+static_assert(int(PETIT_ACT_SILU) == int(petit::kActSilu) && int(PETIT_ACT_GELU) == int(petit::kActGelu) &&
+              int(PETIT_ACT_GELU_TANH) == int(petit::kActGeluTanh), "activations");
 
 constexpr int64_t kMaxDim = int64_t(1) << 24;
 constexpr uint64_t kGemmTimeoutNs = 2000000000ull;  // no legitimate wait lasts 2 s
@@ -233,6 +235,52 @@ petit_status_t moe_common(int fmt, const void* A, const uint8_t* rep, const floa
   return from_cuda(petit::launch_gemm(plan, args, map, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// The factor that turns the register decode's sums into g * A . Wq^T (it yields
+// Wq * 2^-8 for NVFP4, Wq * 2^-7 for its FP16 layout).
+float epilogue_factor(int fmt, float g) { return fmt == kNVFP4 ? g * 256.0f : fmt == kNVFP4F16 ? g * 128.0f : g; }
+
+bool good_scale(float g) { return g > 0.0f && g <= 1.0e36f; }
+
+// The gated products, dense (one group) and grouped.  n: output columns, each
+// of two weight rows.
+petit_status_t gated_common(int fmt, const void* A, const uint8_t* rep, const float* gate_scales,
+                            const float* up_scales, const int64_t* off, int64_t groups, int act, void* C,
+                            int64_t n, int64_t k, void* ws, size_t ws_bytes, petit_stream_t stream) {
+  if (act != PETIT_ACT_SILU && act != PETIT_ACT_GELU && act != PETIT_ACT_GELU_TANH)
+    return PETIT_ERR_INVALID_ARG;
+  if (!A || !rep || !C) return PETIT_ERR_INVALID_ARG;
+  if (n > kMaxDim) return PETIT_ERR_UNSUPPORTED_SHAPE;
+  if (petit_status_t st = check_tiled_shape(2 * n, k)) return st;
+  if (!aligned16(A) || !aligned16(rep) || !aligned16(C)) return PETIT_ERR_MISALIGNED;
+  float gate[petit::kMaxGroups], up[petit::kMaxGroups];
+  for (int64_t e = 0; e < groups; ++e) {
+    const float g = gate_scales ? gate_scales[e] : 1.0f, u = up_scales ? up_scales[e] : 1.0f;
+    if (!good_scale(g) || !good_scale(u)) return PETIT_ERR_INVALID_ARG;
+    gate[e] = epilogue_factor(fmt, g);
+    up[e] = epilogue_factor(fmt, u);
+  }
+  if (!ws) return PETIT_ERR_WORKSPACE;
+  if (!aligned16(ws)) return PETIT_ERR_MISALIGNED;
+  int sms = 0, dev = 0;
+  int pair_cap = 0;
+  if (petit_status_t st = current_device(&sms, &dev, &pair_cap)) return st;
+  const int64_t rows = off[groups];
+  const petit::GemmPlan plan =
+      petit::plan_grouped(off, static_cast<int>(groups), 2 * n, k, fmt, sms, pair_cap);
+  if (plan.units >= kMaxUnits) return PETIT_ERR_UNSUPPORTED_SHAPE;
+  if (ws_bytes < plan.ws.total) return PETIT_ERR_WORKSPACE;
+  CUtensorMap map;
+  if (petit_status_t st = cached_a_map(&map, A, rows, k, plan.pair ? plan.bn / 2 : plan.bn, plan.ku,
+                                       fmt == kNVFP4F16, dev))
+    return st;
+  petit::GemmArgs args{A, rep, C, rows, 2 * n, k, gate[0], static_cast<uint8_t*>(ws), kGemmTimeoutNs};
+  args.device = dev;
+  args.rep_stride = static_cast<int64_t>(petit_repacked_bytes(2 * n, k, fmt));
+  args.group_alpha = gate;
+  const petit::GatedArgs gated{act, up};
+  return from_cuda(petit::launch_gated(plan, args, gated, map, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 // Arguments of the plan queries that do not depend on the problem.
 petit_status_t check_plan_args(int num_sms, int pair_cap, const petit_plan_info_t* info) {
   if (!info || num_sms < 1 || num_sms > petit::kMaxCtas || pair_cap < 0 ||
@@ -336,6 +384,30 @@ petit_status_t petit_moe_gemm_bf16_nvfp4(const void* A, const uint8_t* rep,
   if (!global_scales) return PETIT_ERR_INVALID_ARG;
   return moe_common(kNVFP4, A, rep, global_scales, expert_offsets, num_experts, C, n, k, workspace,
                     workspace_bytes, stream);
+}
+
+petit_status_t petit_gated_gemm(int fmt, const void* A, const uint8_t* rep, float gate_scale,
+                                float up_scale, int act, void* C, int64_t m, int64_t n, int64_t k,
+                                void* workspace, size_t workspace_bytes, petit_stream_t stream) {
+  if (fmt != PETIT_FMT_NVFP4 && fmt != PETIT_FMT_MXFP4 && fmt != PETIT_FMT_NVFP4_F16)
+    return PETIT_ERR_INVALID_ARG;
+  if (m < 1) return PETIT_ERR_INVALID_ARG;
+  if (m > kMaxDim) return PETIT_ERR_UNSUPPORTED_SHAPE;
+  const int64_t off[2] = {0, m};
+  return gated_common(fmt, A, rep, &gate_scale, &up_scale, off, 1, act, C, n, k, workspace,
+                      workspace_bytes, stream);
+}
+
+petit_status_t petit_moe_gated_gemm(int fmt, const void* A, const uint8_t* rep, const float* gate_scales,
+                                    const float* up_scales, const int64_t* expert_offsets,
+                                    int64_t num_experts, int act, void* C, int64_t n, int64_t k,
+                                    void* workspace, size_t workspace_bytes, petit_stream_t stream) {
+  if (fmt != PETIT_FMT_NVFP4 && fmt != PETIT_FMT_MXFP4) return PETIT_ERR_INVALID_ARG;
+  if (petit_status_t st = check_offsets(expert_offsets, num_experts)) return st;
+  if (fmt == PETIT_FMT_NVFP4 && (!gate_scales || !up_scales)) return PETIT_ERR_INVALID_ARG;
+  if (expert_offsets[num_experts] == 0) return PETIT_OK;   // no routed tokens: nothing to compute
+  return gated_common(fmt, A, rep, gate_scales, up_scales, expert_offsets, num_experts, act, C, n, k,
+                      workspace, workspace_bytes, stream);
 }
 
 petit_status_t petit_absmax_bf16(const void* x, int64_t count, float* amax_out,

@@ -1,4 +1,5 @@
 // BF16 x FP4 weight-only GEMM for sm_103a (tcgen05 + tensor memory).
+// (gemm_gated.cu includes this file for the kernels with the gated epilogue.)
 //
 //   C[m, n] = alpha * sum_k A[m, k] * W'[n, k]
 //
@@ -41,6 +42,11 @@
 //   Keeping the dequantised weights in tensor memory avoids writing 2 bytes
 //   per weight back to shared memory, so shared-memory bandwidth only carries
 //   the FP4 chunk and the activation tile.
+// * Gated epilogue (GATED): weight rows 2j and 2j + 1 are row j of the gate and
+//   of the up matrix, so a tile's 128 rows are both rows of 64 output columns
+//   and the pair meets in neighbouring lanes: C[m, j] = act(gate) * up is formed
+//   from the FP32 sums, where the plain epilogue rounds and stores them.  The
+//   [m, 2n] product is never written, and the main loop does not change.
 // * Every wait is bounded; a wait that runs out records a timeout in the
 //   workspace status word and the CTA shuts down cleanly.
 // * Bounds-checking build (-DPETIT_CHECK_BOUNDS, a separate library): every
@@ -119,6 +125,13 @@ struct Params {
 #endif
 };
 
+// What the gated epilogue needs beside it: group_alpha is the gate's factor,
+// group_up the other matrix's.
+struct GatedParams : Params {
+  float group_up[kMaxGroups];
+  int32_t act;   // kActSilu, ...
+};
+
 // Split tiles.  A contributor stores its FP32 partial and then arrives on
 // the tile's counter (acq_rel); the last to arrive adds all partials in CTA
 // order and writes C, so the result is the same whichever CTA sums, and no
@@ -136,7 +149,7 @@ struct FixJob {
   uint16_t* c_g;                        // output rows of the tile's group
   int64_t c_first, c_last, first_slot;  // contributing CTAs, slot of the first
   int64_t row0, col0, g_rows;           // tile origin in C; rows of the group
-  float alpha;
+  float alpha, alpha_up;                // (gated: the gate's and the up matrix's)
   int32_t d;                            // accumulator buffer of the segment
   uint32_t has;                         // bit t: issuer t's accumulator contributes
   int32_t valid;
@@ -360,6 +373,36 @@ __device__ __forceinline__ uint16_t out_bits(float x) {
   else return __bfloat16_as_ushort(__float2bfloat16_rn(x));
 }
 
+// h = act(gate) * up of N rows, for a lane that holds the gate's (even lanes) or
+// the up matrix's (odd) sums x of an output column.  The lanes of a pair
+// exchange halves: even lanes take rows 0 .. N / 2 - 1, odd lanes the rest.
+// act in FP32, through the hardware's exponential (a few units at 2^-23 of a
+// result of which 8 or 11 bits are kept) and the CUDA library's erfc.
+template <int N>
+__device__ __forceinline__ void gate_rows(const float (&x)[N], int act, float (&h)[N / 2]) {
+  const bool odd = threadIdx.x & 1;
+  float gate[N / 2];
+#pragma unroll
+  for (int j = 0; j < N / 2; ++j) {
+    const float other = __shfl_xor_sync(0xffffffffu, odd ? x[j] : x[j + N / 2], 1);
+    gate[j] = odd ? other : x[j];
+    h[j] = odd ? x[j + N / 2] : other;   // up
+  }
+  if (act == kActSilu) {
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j) h[j] *= gate[j] / (1.0f + __expf(-gate[j]));
+  } else if (act == kActGelu) {
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j) h[j] *= 0.5f * gate[j] * erfcf(-0.70710678118654752f * gate[j]);
+  } else {   // 0.5 (1 + tanh z) = 1 / (1 + e^(-2 z))
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j) {
+      const float z2 = 1.5957691216057308f * (gate[j] + 0.044715f * gate[j] * gate[j] * gate[j]);
+      h[j] *= gate[j] / (1.0f + __expf(-z2));
+    }
+  }
+}
+
 // First unit of CTA c's stream-K range (c = P: the end of the last).  An
 // even split is floor(c U / P) = c q + c r / P with q = U / P, r = U % P;
 // c r < P^2 fits 32 bits, so no 64-bit division is needed (this sits before
@@ -382,9 +425,10 @@ __device__ __forceinline__ int32_t cta_of_unit(const Params& p, int64_t u) {
   return lo;
 }
 
-template <int FMT, int BN, int KU, bool PAIR>
+template <int FMT, int BN, int KU, bool PAIR, bool GATED>
 __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR>::kThreads), 1)
-    gemm_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tmap_a) {
+    gemm_kernel(const __grid_constant__ std::conditional_t<GATED, GatedParams, Params> p,
+                const __grid_constant__ CUtensorMap tmap_a) {
   using C = Cfg<FMT, BN, KU, PAIR>;
   using T = FmtTraits<FMT>;
   extern __shared__ uint8_t smem_raw[];
@@ -432,6 +476,8 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR>::kThreads), 1)
   const int64_t cta = PAIR ? (blockIdx.x >> 1) : blockIdx.x;
   auto sid = [&](int64_t c) -> int64_t { return PAIR ? 2 * c + rank : c; };
   const int32_t wmul = PAIR ? 2 : 1;   // weight tile of work tile nt: nt * wmul + rank
+  // columns of C: one a weight row, or one for each pair of them
+  const int32_t c_cols = GATED ? p.n / 2 : p.n;
   const int64_t u0 = cta_lo(p, static_cast<int32_t>(cta));
   const int64_t u1 = cta_lo(p, static_cast<int32_t>(cta) + 1);
   const int64_t KS = p.k_units;
@@ -805,7 +851,21 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR>::kThreads), 1)
     // against 2 us to drain a 256-row tile of the gate_up projection).
     auto put_rows = [&](const float (&val)[16], uint16_t* c_g, int64_t row0, int64_t col0,
                         int64_t g_rows, float alpha) {
-      if constexpr (C::kStageC > 0) {
+      if constexpr (GATED && C::kStageC > 0) {
+        // (16 rows x 64 columns: a vector for each of the 128 threads)
+        constexpr int kCols = kTileN / 2;
+        float h[8];
+        gate_rows(val, p.act, h);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) stage_c[(j + 8 * (r & 1)) * kCols + (r >> 1)] = out_bits<FMT>(h[j]);
+        if (!epi_sync()) return false;
+        const int64_t mrow = row0 + 4 * q + (lane >> 3), col = (col0 >> 1) + (lane & 7) * 8;
+        if (mrow < g_rows &&
+            PETIT_CHECK(col + 8 <= c_cols && (c_g - p.c) + mrow * c_cols + col + 8 <= p.chk_c_elems))
+          *reinterpret_cast<uint4*>(c_g + mrow * c_cols + col) =
+              *reinterpret_cast<const uint4*>(stage_c + (4 * q + (lane >> 3)) * kCols + (lane & 7) * 8);
+        return epi_sync();   // before the buffer is written again
+      } else if constexpr (C::kStageC > 0) {
 #pragma unroll
         for (int j = 0; j < 16; ++j) stage_c[j * kTileN + r] = out_bits<FMT>(alpha * val[j]);
         if (!epi_sync()) return false;
@@ -825,14 +885,31 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR>::kThreads), 1)
         return false;
       }
     };
+    // gated, smaller tiles: 16 rows of this lane's output column, stored directly
+    [[maybe_unused]] auto put_gated = [&](const float (&val)[16], uint16_t* c_g, int64_t row0, int64_t col, int64_t g_rows) {
+      if constexpr (GATED) {
+        float h[8];
+        gate_rows(val, p.act, h);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int64_t mrow = row0 + j + 8 * (r & 1);
+          if (mrow < g_rows && PETIT_CHECK(col < c_cols && (c_g - p.c) + mrow * c_cols + col < p.chk_c_elems))
+            c_g[mrow * c_cols + col] = out_bits<FMT>(h[j]);
+        }
+      }
+    };
     for (int64_t u = u0; u < u1; ++seg) {
       const int64_t tile = u / KS;
       const int64_t seg_end = (tile + 1) * KS < u1 ? (tile + 1) * KS : u1;
       const bool full_tile = (u == tile * KS) && (seg_end == (tile + 1) * KS);
       const int64_t nt = ec.nt, mt = ec.mt;
       const int64_t g_rows = p.row_off[ec.g + 1] - p.row_off[ec.g];  // this group's activation rows
-      uint16_t* const c_g = p.c + static_cast<int64_t>(p.row_off[ec.g]) * p.n;
+      uint16_t* const c_g = p.c + static_cast<int64_t>(p.row_off[ec.g]) * c_cols;
       const float alpha = p.alpha_dev ? alpha_dev : p.group_alpha[ec.g];
+      float alpha_up = alpha;
+      if constexpr (GATED) alpha_up = p.group_up[ec.g];
+      // the factor of this lane's weight row
+      [[maybe_unused]] const float row_alpha = GATED && (r & 1) ? alpha_up : alpha;
       cursor_next<BN>(p, ec);
       const int d = static_cast<int>(seg % C::kNumD);
       // split tile: its contributors and their partial slots (every
@@ -885,6 +962,7 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR>::kThreads), 1)
             fix->col0 = (static_cast<int64_t>(nt) * wmul + rank) * kTileN;
             fix->g_rows = g_rows;
             fix->alpha = alpha;
+            fix->alpha_up = alpha_up;
             fix->d = d;
             fix->has = has;
             fix->valid = 1;
@@ -921,11 +999,16 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR>::kThreads), 1)
         if (full_tile && C::kStageC > 0) {
           float fv[16];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) fv[j] = __uint_as_float(v[j]);
+          for (int j = 0; j < 16; ++j) fv[j] = GATED ? row_alpha * __uint_as_float(v[j]) : __uint_as_float(v[j]);
           if (!put_rows(fv, c_g, static_cast<int64_t>(mt) * BN + c0, ncol - r, g_rows, alpha)) {
             c_ok = false;
             break;
           }
+        } else if (GATED && full_tile) {
+          float fv[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) fv[j] = row_alpha * __uint_as_float(v[j]);
+          put_gated(fv, c_g, static_cast<int64_t>(mt) * BN + c0, ncol >> 1, g_rows);
         } else if (full_tile) {
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
@@ -973,6 +1056,7 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR>::kThreads), 1)
             fix->col0 = (static_cast<int64_t>(nt) * wmul + rank) * kTileN;
             fix->g_rows = g_rows;
             fix->alpha = alpha;
+            fix->alpha_up = alpha_up;
             fix->d = d;
             fix->has = has;
             fix->valid = 1;
@@ -1011,12 +1095,18 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR>::kThreads), 1)
             }
             // (stored directly: here the partial loads set the pace, and
             // staging, with its barriers between the warps, was slower)
+            if constexpr (GATED) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const int64_t mrow = static_cast<int64_t>(mt) * BN + c0 + j;
-              if (mrow < g_rows && PETIT_CHECK(ncol < p.n && (c_g - p.c) + mrow * p.n + ncol <
-                                                               p.chk_c_elems))
-                c_g[mrow * p.n + ncol] = out_bits<FMT>(alpha * acc[j]);
+              for (int j = 0; j < 16; ++j) acc[j] *= row_alpha;
+              put_gated(acc, c_g, static_cast<int64_t>(mt) * BN + c0, ncol >> 1, g_rows);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const int64_t mrow = static_cast<int64_t>(mt) * BN + c0 + j;
+                if (mrow < g_rows && PETIT_CHECK(ncol < p.n && (c_g - p.c) + mrow * p.n + ncol <
+                                                                 p.chk_c_elems))
+                  c_g[mrow * p.n + ncol] = out_bits<FMT>(alpha * acc[j]);
+              }
             }
           }
         }
@@ -1243,11 +1333,28 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR>::kThreads), 1)
               }
             }
           }
+          if constexpr (GATED) {
+            float h[8];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) gst[j * kTileN + r] = out_bits<FMT>(f.alpha * acc[j]);
+            for (int j = 0; j < 16; ++j) acc[j] *= r & 1 ? f.alpha_up : f.alpha;
+            gate_rows(acc, p.act, h);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              gst[(j + 8 * (r & 1)) * (kTileN / 2) + (r >> 1)] = out_bits<FMT>(h[j]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) gst[j * kTileN + r] = out_bits<FMT>(f.alpha * acc[j]);
+          }
         }
         __syncthreads();
-        if (mine) {
+        if (GATED && mine) {
+          const int row = 4 * q + (lane >> 3);   // warp q writes rows 4q .. 4q + 3
+          const int64_t mrow = f.row0 + m0 + row, col = (f.col0 >> 1) + (lane & 7) * 8;
+          if (mrow < f.g_rows &&
+              PETIT_CHECK(col + 8 <= c_cols && (f.c_g - p.c) + mrow * c_cols + col + 8 <= p.chk_c_elems))
+            *reinterpret_cast<uint4*>(f.c_g + mrow * c_cols + col) =
+                *reinterpret_cast<const uint4*>(gst + row * (kTileN / 2) + (lane & 7) * 8);
+        } else if (mine) {
 #pragma unroll
           for (int s2 = 0; s2 < 2; ++s2) {
             const int row = 4 * q + 2 * s2 + (lane >> 4);   // warp q writes rows 4q .. 4q + 3
@@ -1330,13 +1437,28 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR>::kThreads), 1)
               }
             }
           }
+          if constexpr (GATED) {
+            float h[kLd / 2];
   #pragma unroll
-          for (int j = 0; j < kLd; ++j) {
-            const int64_t mrow = f.row0 + m0 + j;
-            if (mrow < f.g_rows &&
-                PETIT_CHECK(f.col0 + r < p.n &&
-                            (f.c_g - p.c) + mrow * p.n + f.col0 + r < p.chk_c_elems))
-              f.c_g[mrow * p.n + f.col0 + r] = out_bits<FMT>(f.alpha * acc[j]);
+            for (int j = 0; j < kLd; ++j) acc[j] *= r & 1 ? f.alpha_up : f.alpha;
+            gate_rows(acc, p.act, h);
+            const int64_t col = (f.col0 + r) >> 1;
+  #pragma unroll
+            for (int j = 0; j < kLd / 2; ++j) {
+              const int64_t mrow = f.row0 + m0 + j + (r & 1 ? kLd / 2 : 0);
+              if (mrow < f.g_rows &&
+                  PETIT_CHECK(col < c_cols && (f.c_g - p.c) + mrow * c_cols + col < p.chk_c_elems))
+                f.c_g[mrow * c_cols + col] = out_bits<FMT>(h[j]);
+            }
+          } else {
+  #pragma unroll
+            for (int j = 0; j < kLd; ++j) {
+              const int64_t mrow = f.row0 + m0 + j;
+              if (mrow < f.g_rows &&
+                  PETIT_CHECK(f.col0 + r < p.n &&
+                              (f.c_g - p.c) + mrow * p.n + f.col0 + r < p.chk_c_elems))
+                f.c_g[mrow * p.n + f.col0 + r] = out_bits<FMT>(f.alpha * acc[j]);
+            }
           }
         }
       }
@@ -1365,14 +1487,22 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR>::kThreads), 1)
     atomicOr(p.status, (*abort_flag & kAbortBounds) ? kStatusBounds : kStatusTimeout);
 }
 
+#ifdef PETIT_GATED
+constexpr bool kGated = true;
+using LaunchParams = GatedParams;
+#else
+constexpr bool kGated = false;
+using LaunchParams = Params;
+#endif
+
 template <int FMT, int BN, int KU, bool PAIR = false>
-cudaError_t launch_t(const Params& prm, const CUtensorMap& tmap, cudaStream_t stream, int dev) {
+cudaError_t launch_t(const LaunchParams& prm, const CUtensorMap& tmap, cudaStream_t stream, int dev) {
   using C = Cfg<FMT, BN, KU, PAIR>;
   // the dynamic shared-memory limit is raised once per device
   static std::atomic<bool> attr_done[64];
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_done[dev].load(std::memory_order_acquire)) {
-    const cudaError_t e = cudaFuncSetAttribute(gemm_kernel<FMT, BN, KU, PAIR>,
+    const cudaError_t e = cudaFuncSetAttribute(gemm_kernel<FMT, BN, KU, PAIR, kGated>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                C::kSmemBytes);
     if (e != cudaSuccess) return e;
@@ -1393,41 +1523,11 @@ cudaError_t launch_t(const Params& prm, const CUtensorMap& tmap, cudaStream_t st
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = PAIR ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, gemm_kernel<FMT, BN, KU, PAIR>, prm, tmap);
-}
-
-// How many CTA pairs of the pair kernel (this format and tile height) can be
-// resident at once on the current device; 0 if the query fails.
-template <int FMT, int BN>
-int pair_capacity_t() {
-  using C = Cfg<FMT, BN, 1, true>;
-  auto kern = gemm_kernel<FMT, BN, 1, true>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) !=
-      cudaSuccess) {
-    cudaGetLastError();
-    return 0;
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * kMaxBoundCtas);
-  cfg.blockDim = dim3(C::kThreads);
-  cfg.dynamicSmemBytes = C::kSmemBytes;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
-    cudaGetLastError();
-    return 0;
-  }
-  return n;
+  return cudaLaunchKernelEx(&cfg, gemm_kernel<FMT, BN, KU, PAIR, kGated>, prm, tmap);
 }
 
 template <int FMT>
-cudaError_t launch_fmt(int bn, int ku, bool pair, const Params& prm, const CUtensorMap& tmap,
+cudaError_t launch_fmt(int bn, int ku, bool pair, const LaunchParams& prm, const CUtensorMap& tmap,
                        cudaStream_t s, int dev) {
   if (pair) {
     if (ku != 1) return cudaErrorInvalidValue;
@@ -1453,6 +1553,97 @@ cudaError_t launch_fmt(int bn, int ku, bool pair, const Params& prm, const CUten
     case 256: return launch_t<FMT, 256, 1>(prm, tmap, s, dev);
     default: return cudaErrorInvalidValue;
   }
+}
+
+// The kernel's parameters for a planned call.
+void fill_params(const GemmPlan& pl, const GemmArgs& a, Params& prm) {
+  prm.rep = a.rep;
+  prm.c = static_cast<uint16_t*>(a.C);
+  prm.partials = reinterpret_cast<float*>(a.workspace + pl.ws.partials_off);
+  prm.counters = reinterpret_cast<uint32_t*>(a.workspace + pl.ws.counters_off);
+  prm.status = reinterpret_cast<uint32_t*>(a.workspace);
+  prm.n = static_cast<int32_t>(a.n);
+  prm.n_tiles = pl.n_tiles;
+  prm.k_units = pl.k_stages / pl.ku;
+  prm.units = pl.units;
+  prm.num_ctas = pl.num_ctas;
+  prm.units_q = static_cast<int32_t>(pl.units / pl.num_ctas);
+  prm.units_r = static_cast<int32_t>(pl.units % pl.num_ctas);
+  prm.use_bounds = pl.use_bounds ? 1 : 0;
+  if (pl.use_bounds)
+    for (int c = 0; c <= pl.num_ctas; ++c) prm.bound[c] = pl.bound[c];
+  prm.weights_reused = pl.weights_reused ? 1 : 0;
+  prm.alpha_dev = a.alpha_dev;
+  prm.alpha_scale = a.alpha_scale;
+  prm.timeout_ns = a.timeout_ns;
+  prm.rep_stride = a.rep_stride;
+  prm.num_groups = pl.num_groups;
+  for (int g = 0; g <= pl.num_groups; ++g) {
+    prm.row_off[g] = pl.row_off[g];
+    prm.tile_base[g] = pl.tile_base[g];
+  }
+  for (int g = 0; g < pl.num_groups; ++g)
+    prm.group_alpha[g] = a.group_alpha ? a.group_alpha[g] : a.alpha;
+#ifdef PETIT_CHECK_BOUNDS
+  {
+    const int64_t chunk = pl.fmt == kMXFP4 ? FmtTraits<kMXFP4>::kChunkBytes
+                                           : FmtTraits<kNVFP4>::kChunkBytes;
+    // (with CTA pairs a work tile holds two 128-row weight tiles)
+    const int64_t wb = static_cast<int64_t>(pl.n_tiles) * (pl.pair ? 2 : 1) * pl.k_stages * chunk;
+    const int64_t ce = static_cast<int64_t>(pl.row_off[pl.num_groups]) * (kGated ? a.n / 2 : a.n);
+    int64_t lw = -1, lc = -1;
+    check_limits(&lw, &lc);
+    prm.chk_rep_bytes = lw >= 0 && lw < wb ? lw : wb;
+    prm.chk_c_elems = lc >= 0 && lc < ce ? lc : ce;
+    prm.chk_a_rows = pl.row_off[pl.num_groups];
+  }
+#endif
+}
+
+// Launches the planned kernel.
+cudaError_t launch_planned(const GemmPlan& pl, const GemmArgs& a, const LaunchParams& prm,
+                           const CUtensorMap& tmap, cudaStream_t stream) {
+  if (pl.fmt == kNVFP4)
+    return launch_fmt<kNVFP4>(pl.bn, pl.ku, pl.pair, prm, tmap, stream, a.device);
+  if (pl.fmt == kNVFP4F16)
+    return launch_fmt<kNVFP4F16>(pl.bn, pl.ku, pl.pair, prm, tmap, stream, a.device);
+  return launch_fmt<kMXFP4>(pl.bn, pl.ku, pl.pair, prm, tmap, stream, a.device);
+}
+
+}  // namespace
+
+#ifndef PETIT_GATED
+
+namespace {
+
+// How many CTA pairs of the pair kernel (this format and tile height) can be
+// resident at once on the current device; 0 if the query fails.
+template <int FMT, int BN>
+int pair_capacity_t() {
+  using C = Cfg<FMT, BN, 1, true>;
+  auto kern = gemm_kernel<FMT, BN, 1, true, false>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) !=
+      cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * kMaxBoundCtas);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  return n;
 }
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -1512,6 +1703,11 @@ std::atomic<int64_t> g_check_c_elems{-1};
 double late_start_ns() { return kLateStartNs; }
 
 }  // namespace
+
+void check_limits(int64_t* weight_bytes, int64_t* c_elems) {
+  *weight_bytes = g_check_weight_bytes.load();
+  *c_elems = g_check_c_elems.load();
+}
 
 int tile_override() { return g_tile_override.load(std::memory_order_relaxed); }
 
@@ -1673,51 +1869,10 @@ GemmPlan plan_gemm(int64_t m, int64_t n, int64_t k, int fmt, int num_sms, int pa
 cudaError_t launch_gemm(const GemmPlan& pl, const GemmArgs& a, const CUtensorMap& tmap,
                         cudaStream_t stream) {
   Params prm{};
-  prm.rep = a.rep;
-  prm.c = static_cast<uint16_t*>(a.C);
-  prm.partials = reinterpret_cast<float*>(a.workspace + pl.ws.partials_off);
-  prm.counters = reinterpret_cast<uint32_t*>(a.workspace + pl.ws.counters_off);
-  prm.status = reinterpret_cast<uint32_t*>(a.workspace);
-  prm.n = static_cast<int32_t>(a.n);
-  prm.n_tiles = pl.n_tiles;
-  prm.k_units = pl.k_stages / pl.ku;
-  prm.units = pl.units;
-  prm.num_ctas = pl.num_ctas;
-  prm.units_q = static_cast<int32_t>(pl.units / pl.num_ctas);
-  prm.units_r = static_cast<int32_t>(pl.units % pl.num_ctas);
-  prm.use_bounds = pl.use_bounds ? 1 : 0;
-  if (pl.use_bounds)
-    for (int c = 0; c <= pl.num_ctas; ++c) prm.bound[c] = pl.bound[c];
-  prm.weights_reused = pl.weights_reused ? 1 : 0;
-  prm.alpha_dev = a.alpha_dev;
-  prm.alpha_scale = a.alpha_scale;
-  prm.timeout_ns = a.timeout_ns;
-  prm.rep_stride = a.rep_stride;
-  prm.num_groups = pl.num_groups;
-  for (int g = 0; g <= pl.num_groups; ++g) {
-    prm.row_off[g] = pl.row_off[g];
-    prm.tile_base[g] = pl.tile_base[g];
-  }
-  for (int g = 0; g < pl.num_groups; ++g)
-    prm.group_alpha[g] = a.group_alpha ? a.group_alpha[g] : a.alpha;
-#ifdef PETIT_CHECK_BOUNDS
-  {
-    const int64_t chunk = pl.fmt == kMXFP4 ? FmtTraits<kMXFP4>::kChunkBytes
-                                           : FmtTraits<kNVFP4>::kChunkBytes;
-    // (with CTA pairs a work tile holds two 128-row weight tiles)
-    const int64_t wb = static_cast<int64_t>(pl.n_tiles) * (pl.pair ? 2 : 1) * pl.k_stages * chunk;
-    const int64_t ce = static_cast<int64_t>(pl.row_off[pl.num_groups]) * a.n;
-    const int64_t lw = g_check_weight_bytes.load(), lc = g_check_c_elems.load();
-    prm.chk_rep_bytes = lw >= 0 && lw < wb ? lw : wb;
-    prm.chk_c_elems = lc >= 0 && lc < ce ? lc : ce;
-    prm.chk_a_rows = pl.row_off[pl.num_groups];
-  }
-#endif
-  if (pl.fmt == kNVFP4)
-    return launch_fmt<kNVFP4>(pl.bn, pl.ku, pl.pair, prm, tmap, stream, a.device);
-  if (pl.fmt == kNVFP4F16)
-    return launch_fmt<kNVFP4F16>(pl.bn, pl.ku, pl.pair, prm, tmap, stream, a.device);
-  return launch_fmt<kMXFP4>(pl.bn, pl.ku, pl.pair, prm, tmap, stream, a.device);
+  fill_params(pl, a, prm);
+  return launch_planned(pl, a, prm, tmap, stream);
 }
+
+#endif  // PETIT_GATED
 
 }  // namespace petit

@@ -1,0 +1,18 @@
+// The FP4 GEMM's kernels with the gated epilogue: C = act(gate) * up, both
+// projections and their product in one kernel.  The main loop is gemm.cu's; its
+// own translation unit, so that the two sets of kernels compile side by side.
+#define PETIT_GATED
+#include "gemm.cu"
+
+namespace petit {
+
+cudaError_t launch_gated(const GemmPlan& pl, const GemmArgs& a, const GatedArgs& g, const CUtensorMap& tmap,
+                         cudaStream_t stream) {
+  GatedParams prm{};
+  fill_params(pl, a, prm);
+  prm.act = g.act;
+  for (int i = 0; i < pl.num_groups; ++i) prm.group_up[i] = g.group_up[i];
+  return launch_planned(pl, a, prm, tmap, stream);
+}
+
+}  // namespace petit

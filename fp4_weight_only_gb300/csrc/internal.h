@@ -74,6 +74,7 @@ int tile_override();   // bn | ku << 16, or 0
 // normal build.
 bool bounds_checking();
 bool set_check_limits(int64_t weight_bytes, int64_t c_elems);
+void check_limits(int64_t* weight_bytes, int64_t* c_elems);
 // Checks that the current device can run this library's kernels and gives its
 // SM count and index; returns a petit_status_t.
 int usable_device(int* sms, int* dev = nullptr);
@@ -107,6 +108,16 @@ struct GemmArgs {
 
 cudaError_t launch_gemm(const GemmPlan& plan, const GemmArgs& args, const CUtensorMap& tmap_a,
                         cudaStream_t stream);
+
+// The gated product (gemm_gated.cu): weight rows 2j and 2j + 1 are the gate's
+// and the up matrix's row j, a.n counts both, C has n / 2 columns.
+enum : int { kActSilu = 0, kActGelu = 1, kActGeluTanh = 2 };
+struct GatedArgs {
+  int act;
+  const float* group_up;   // the up matrices' epilogue factors (a.group_alpha: the gates')
+};
+cudaError_t launch_gated(const GemmPlan& plan, const GemmArgs& args, const GatedArgs& gated,
+                         const CUtensorMap& tmap_a, cudaStream_t stream);
 
 cudaError_t launch_absmax(const void* x, int64_t count, float* out, cudaStream_t stream);
 cudaError_t launch_quantize(int fmt, const void* W, float g, uint8_t* wp, uint8_t* sp,

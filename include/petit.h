@@ -425,6 +425,38 @@ size_t petit_kv_attention_workspace_bytes(int32_t num_kv_heads, int32_t head_dim
 petit_status_t petit_kv_attention(const petit_kv_cache_t* cache, const petit_kv_attention_t* args,
                                   void* workspace, size_t workspace_bytes, petit_stream_t stream);
 
+/* ------------------------------------------ gated feed-forward products */
+
+/* Both projections of a gated feed-forward block, the activation and their
+ * product in one kernel:
+ *     C[m][n] = act(gate_scale * A . Wg^T) * (up_scale * A . Wu^T)
+ * with FP32 sums, from which act and the product are formed (FP32) and rounded
+ * once.  Wg and Wu are n x k; `rep` holds them as one matrix of 2 n rows, row 2 j
+ * the gate's row j and row 2 j + 1 the other's: interleave the rows of the packed
+ * codes and of the scale bytes and give that to petit_repack_*(2 n, k).
+ * n counts C's columns: n % 64 == 0, k % 128 == 0.  fmt: the repacked format;
+ * PETIT_FMT_NVFP4_F16 takes and gives FP16, the others BF16.  The two scales are
+ * NVFP4's global scales (MXFP4: 1).  workspace: at least
+ * petit_gemm_workspace_bytes(m, 2 n, k, fmt) bytes, used and kept as a GEMM's.
+ *     silu x / (1 + e^-x),  gelu x Phi(x),  gelu_tanh x / (1 + e^(-2 z)),
+ *     z = sqrt(2 / pi) (x + 0.044715 x^3)
+ * Errors and everything else as petit_gemm_bf16_nvfp4. */
+typedef enum petit_act { PETIT_ACT_SILU = 0, PETIT_ACT_GELU = 1, PETIT_ACT_GELU_TANH = 2 } petit_act_t;
+
+petit_status_t petit_gated_gemm(int fmt, const void* A, const uint8_t* rep, float gate_scale,
+                                float up_scale, int act, void* C, int64_t m, int64_t n, int64_t k,
+                                void* workspace, size_t workspace_bytes, petit_stream_t stream);
+
+/* The same for the experts of an MoE layer: rows, offsets and rep as for
+ * petit_moe_gemm_bf16_*, each expert's matrix laid out as above, C [T][n].
+ * gate_scales, up_scales: host arrays of num_experts positive floats (MXFP4: may
+ * be NULL).  fmt: PETIT_FMT_NVFP4 or PETIT_FMT_MXFP4.  workspace: at least
+ * petit_moe_workspace_bytes(expert_offsets, num_experts, 2 n, k, fmt) bytes. */
+petit_status_t petit_moe_gated_gemm(int fmt, const void* A, const uint8_t* rep, const float* gate_scales,
+                                    const float* up_scales, const int64_t* expert_offsets,
+                                    int64_t num_experts, int act, void* C, int64_t n, int64_t k,
+                                    void* workspace, size_t workspace_bytes, petit_stream_t stream);
+
 /* ------------------------------------- around a decoder layer's products */
 
 /* Root-mean-square norm of rows with the residual's addition:
