@@ -135,6 +135,7 @@ SIGNATURES = {
     "petit_kv_attention": (ctypes.c_int, [_c_p, _c_p, _c_p, _c_sz, _c_p]),
     "petit_gated_gemm": (ctypes.c_int, [ctypes.c_int, _c_p, _c_p, ctypes.c_float, ctypes.c_float, ctypes.c_int, _c_p,
                                         _c_i64, _c_i64, _c_i64, _c_p, _c_sz, _c_p]),
+    "petit_moe_gated_workspace_bytes": (_c_sz, [_c_p, _c_i64, _c_i64, _c_i64, ctypes.c_int]),
     "petit_moe_gated_gemm": (ctypes.c_int, [ctypes.c_int, _c_p, _c_p, _c_p, _c_p, _c_p, _c_i64, ctypes.c_int, _c_p,
                                             _c_i64, _c_i64, _c_p, _c_sz, _c_p]),
     "petit_rms_norm": (ctypes.c_int, [_c_p, _c_p]),
@@ -637,11 +638,14 @@ ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
 
 def gated_repack(gate_packed, gate_scales, up_packed, up_scales, fmt="nvfp4"):
     """Packed codes [n, k/2] and scale bytes of the gate and the up matrix -> one
-    repacked buffer for :func:`gated_gemm` (their rows alternate; n % 64 == 0)."""
+    repacked buffer for :func:`gated_gemm` (eight rows of each in turn; n % 64 == 0)."""
     if gate_packed.dim() != 2 or gate_packed.shape != up_packed.shape or gate_scales.shape != up_scales.shape:
         raise ValueError("gated_repack: need two matrices of one shape")
-    return repack(torch.stack((gate_packed, up_packed), 1).flatten(0, 1),
-                  torch.stack((gate_scales, up_scales), 1).flatten(0, 1), fmt)
+    if gate_packed.shape[0] % 64 or gate_scales.shape[0] != gate_packed.shape[0]:
+        raise ValueError("gated_repack: need a multiple of 64 rows, with scales for each")
+    both = (torch.stack([t.unflatten(0, (-1, 8)) for t in pair], 1).flatten(0, 2)
+            for pair in ((gate_packed, up_packed), (gate_scales, up_scales)))
+    return repack(*both, fmt)
 
 
 def _gated_args(A, rep, n, fmt, act, out, rows_k):
@@ -692,7 +696,7 @@ def moe_gated_gemm(A, rep, expert_offsets, n, fmt="mxfp4", global_scales=None, a
         raise ValueError("expert_offsets[-1] must equal A.shape[0]")
     number, C = _gated_args(A, rep, n, fmt, act, out, (E, k))
     L = load()
-    need = int(L.petit_moe_workspace_bytes(off, E, 2 * n, k, FORMATS[fmt]))
+    need = int(L.petit_moe_gated_workspace_bytes(off, E, n, k, FORMATS[fmt]))
     if need == 0 and T > 0:
         raise PetitError(2, "moe gated workspace size")
     buf = (workspace or Workspace(A.device)).ensure(max(need, 256))

@@ -266,7 +266,7 @@ petit_status_t gated_common(int fmt, const void* A, const uint8_t* rep, const fl
   if (petit_status_t st = current_device(&sms, &dev, &pair_cap)) return st;
   const int64_t rows = off[groups];
   const petit::GemmPlan plan =
-      petit::plan_grouped(off, static_cast<int>(groups), 2 * n, k, fmt, sms, pair_cap);
+      petit::plan_grouped(off, static_cast<int>(groups), 2 * n, k, fmt, sms, pair_cap, true);
   if (plan.units >= kMaxUnits) return PETIT_ERR_UNSUPPORTED_SHAPE;
   if (ws_bytes < plan.ws.total) return PETIT_ERR_WORKSPACE;
   CUtensorMap map;
@@ -384,6 +384,20 @@ petit_status_t petit_moe_gemm_bf16_nvfp4(const void* A, const uint8_t* rep,
   if (!global_scales) return PETIT_ERR_INVALID_ARG;
   return moe_common(kNVFP4, A, rep, global_scales, expert_offsets, num_experts, C, n, k, workspace,
                     workspace_bytes, stream);
+}
+
+size_t petit_moe_gated_workspace_bytes(const int64_t* expert_offsets, int64_t num_experts, int64_t n,
+                                       int64_t k, int fmt) {
+  if (check_offsets(expert_offsets, num_experts) != PETIT_OK || n > kMaxDim ||
+      check_tiled_shape(2 * n, k) != PETIT_OK)
+    return 0;
+  if (fmt != PETIT_FMT_NVFP4 && fmt != PETIT_FMT_MXFP4) return 0;
+  int sms = 0;
+  int pair_cap = 0;
+  if (current_device(&sms, nullptr, &pair_cap) != PETIT_OK) return 0;
+  return petit::plan_grouped(expert_offsets, static_cast<int>(num_experts), 2 * n, k, fmt, sms,
+                             pair_cap, true)
+      .ws.total;
 }
 
 petit_status_t petit_gated_gemm(int fmt, const void* A, const uint8_t* rep, float gate_scale,

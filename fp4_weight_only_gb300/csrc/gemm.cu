@@ -42,11 +42,12 @@
 //   Keeping the dequantised weights in tensor memory avoids writing 2 bytes
 //   per weight back to shared memory, so shared-memory bandwidth only carries
 //   the FP4 chunk and the activation tile.
-// * Gated epilogue (GATED): weight rows 2j and 2j + 1 are row j of the gate and
-//   of the up matrix, so a tile's 128 rows are both rows of 64 output columns
-//   and the pair meets in neighbouring lanes: C[m, j] = act(gate) * up is formed
-//   from the FP32 sums, where the plain epilogue rounds and stores them.  The
-//   [m, 2n] product is never written, and the main loop does not change.
+// * Gated epilogue (GATED): weight rows 16b + i and 16b + 8 + i are row 8b + i of
+//   the gate and of the up matrix (i < 8), so a tile's 128 rows are both rows of
+//   64 output columns.  A 16-lane load from tensor memory gives a thread lanes i
+//   and i + 8 of a column: both sums of an output.  C[m, j] = act(gate) * up is
+//   formed from them, where the plain epilogue rounds and stores; the [m, 2n]
+//   product is never written, and the main loop does not change.
 // * Every wait is bounded; a wait that runs out records a timeout in the
 //   workspace status word and the CTA shuts down cleanly.
 // * Bounds-checking build (-DPETIT_CHECK_BOUNDS, a separate library): every
@@ -272,7 +273,7 @@ struct WeightStream {
   }
 };
 
-template <int FMT, int BN, int KU, bool PAIR = false>
+template <int FMT, int BN, int KU, bool PAIR = false, bool GATED = false>
 struct Cfg {
   using T = FmtTraits<FMT>;
   // CTA pairs (PAIR): two CTAs of a cluster take adjacent 128-row weight
@@ -335,7 +336,8 @@ struct Cfg {
   static constexpr int kDColBase = kNumA * kAColsPerUnit;      // D(t, d) at + (t*kNumD+d)*BN
   // 128/256-row tiles: 16 output rows x 128 columns of BF16 staged in
   // shared memory, so that C is written in whole 256-byte row segments
-  static constexpr int kStageC = BN >= 128 ? 16 * kTileN * 2 : 0;
+  // (gated: 16 rows x 16 columns for each epilogue warp)
+  static constexpr int kStageC = GATED ? 4 * 512 : BN >= 128 ? 16 * kTileN * 2 : 0;
   static constexpr int kSmemBytes =
       1024 + kXStages * kABytes + kWStages * kWBytes + 1024 + kStageC;
   static constexpr uint32_t kM = PAIR ? 256 : 128;   // MMA M (weight rows of both CTAs)
@@ -373,33 +375,87 @@ __device__ __forceinline__ uint16_t out_bits(float x) {
   else return __bfloat16_as_ushort(__float2bfloat16_rn(x));
 }
 
-// h = act(gate) * up of N rows, for a lane that holds the gate's (even lanes) or
-// the up matrix's (odd) sums x of an output column.  The lanes of a pair
-// exchange halves: even lanes take rows 0 .. N / 2 - 1, odd lanes the rest.
-// act in FP32, through the hardware's exponential (a few units at 2^-23 of a
-// result of which 8 or 11 bits are kept) and the CUDA library's erfc.
-template <int N>
-__device__ __forceinline__ void gate_rows(const float (&x)[N], int act, float (&h)[N / 2]) {
-  const bool odd = threadIdx.x & 1;
-  float gate[N / 2];
-#pragma unroll
-  for (int j = 0; j < N / 2; ++j) {
-    const float other = __shfl_xor_sync(0xffffffffu, odd ? x[j] : x[j + N / 2], 1);
-    gate[j] = odd ? other : x[j];
-    h[j] = odd ? x[j + N / 2] : other;   // up
+// The activations in FP32, through the hardware's exponential and reciprocal: a
+// few units at 2^-23, of a result of which 8 or 11 bits are kept.  (The epilogue
+// of 128- and 256-row tiles delays the next tile's MMAs, so that its instructions
+// count: 1024 rows through 57344 x 8192 took 592 us with divisions, a shuffle for
+// each output and stores through a barrier of four warps, 500 so, and 637 and 620
+// where gelu was the CUDA library's erfc.)
+[[maybe_unused]] __device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+[[maybe_unused]] __device__ __forceinline__ float ex2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+template <int ACT>
+__device__ __forceinline__ float activate(float x) {
+  if constexpr (ACT == kActGelu) {
+    // x Phi(x) by Phi(-a) = t 2^(Q(t) - a^2 log2(e) / 2), t = 1 / (1 + 0.28 a), a =
+    // |x|: Q is the polynomial of degree 6 with the least largest error over a in
+    // 0 .. 15, 2^-18.9 of Phi(-a) (fitted to log Phi; beyond, the power is 0)
+    const float a = fabsf(x), t = rcp_approx(fmaf(0.28f, a, 1.0f));
+    float q = 0.35000796f;
+    q = fmaf(q, t, -1.11917842f);
+    q = fmaf(q, t, 0.93719976f);
+    q = fmaf(q, t, -0.14023395f);
+    q = fmaf(q, t, 0.70263922f);
+    q = fmaf(q, t, 1.43127964f);
+    q = fmaf(q, t, -3.16171128f);
+    const float tail = t * ex2_approx(fmaf(a * -0.72134752f, a, q));
+    return x * (x > 0.0f ? 1.0f - tail : tail);
   }
-  if (act == kActSilu) {
+  // 0.5 (1 + tanh z) = 1 / (1 + e^(-2 z)); e^x = 2^(x log2(e))
+  const float y = ACT == kActSilu ? x : 1.5957691216057308f * fmaf(0.044715f * x * x, x, x);
+  return x * rcp_approx(1.0f + ex2_approx(-1.4426950408889634f * y));
+}
+
+// Two outputs act(gate) * up, rounded and packed.
+template <int FMT, int ACT>
+__device__ __forceinline__ uint32_t gated_pair_as(float g0, float u0, float g1, float u1) {
+  return out_bits<FMT>(activate<ACT>(g0) * u0) | static_cast<uint32_t>(out_bits<FMT>(activate<ACT>(g1) * u1)) << 16;
+}
+
+// The same as one function that every place calls, for 16- and 32-row tiles: at
+// the end of a launch, each line of code that an SM has not run yet is a wait for
+// L2 or memory (one row through 57344 x 8192: 53.8 us inlined, 52.1 called).  From
+// 64 rows on the calls cost more (57.9 us inlined, 60.5 called).
+template <int FMT>
+__device__ __noinline__ uint32_t gated_pair(int act, float g0, float u0, float g1, float u1) {
+  if (act == kActSilu) return gated_pair_as<FMT, kActSilu>(g0, u0, g1, u1);
+  if (act == kActGelu) return gated_pair_as<FMT, kActGelu>(g0, u0, g1, u1);
+  return gated_pair_as<FMT, kActGeluTanh>(g0, u0, g1, u1);
+}
+
+// `N` columns of an accumulator: element i is column i of this thread's weight
+// row; gated, elements 4b .. 4b + 3 of thread 4r + c are column 4b + c of the
+// gate's row r and the up matrix's, then of the gate's row r + 8 and the other's
+// (rows of the warp's 16 output columns).
+template <bool GATED>
+__device__ __forceinline__ void load_columns(uint32_t taddr, uint32_t (&v)[16]) {
+  if constexpr (GATED) {
+    uint32_t a[8], b[8];
+    tmem_ld_16x128_x4(taddr, a);
+    tmem_ld_16x128_x4(taddr + (16u << 16), b);
 #pragma unroll
-    for (int j = 0; j < N / 2; ++j) h[j] *= gate[j] / (1.0f + __expf(-gate[j]));
-  } else if (act == kActGelu) {
-#pragma unroll
-    for (int j = 0; j < N / 2; ++j) h[j] *= 0.5f * gate[j] * erfcf(-0.70710678118654752f * gate[j]);
-  } else {   // 0.5 (1 + tanh z) = 1 / (1 + e^(-2 z))
-#pragma unroll
-    for (int j = 0; j < N / 2; ++j) {
-      const float z2 = 1.5957691216057308f * (gate[j] + 0.044715f * gate[j] * gate[j] * gate[j]);
-      h[j] *= gate[j] / (1.0f + __expf(-z2));
+    for (int i = 0; i < 4; ++i) {
+      v[4 * i] = a[2 * i], v[4 * i + 1] = a[2 * i + 1];
+      v[4 * i + 2] = b[2 * i], v[4 * i + 3] = b[2 * i + 1];
     }
+  } else {
+    tmem_ld_x16(taddr, v);
+  }
+}
+template <bool GATED>
+__device__ __forceinline__ void load_columns(uint32_t taddr, uint32_t (&v)[4]) {
+  if constexpr (GATED) {
+    tmem_ld_16x128(taddr, v[0], v[1]);
+    tmem_ld_16x128(taddr + (16u << 16), v[2], v[3]);
+  } else {
+    tmem_ld_x4(taddr, v);
   }
 }
 
@@ -426,10 +482,10 @@ __device__ __forceinline__ int32_t cta_of_unit(const Params& p, int64_t u) {
 }
 
 template <int FMT, int BN, int KU, bool PAIR, bool GATED>
-__global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR>::kThreads), 1)
+__global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
     gemm_kernel(const __grid_constant__ std::conditional_t<GATED, GatedParams, Params> p,
                 const __grid_constant__ CUtensorMap tmap_a) {
-  using C = Cfg<FMT, BN, KU, PAIR>;
+  using C = Cfg<FMT, BN, KU, PAIR, GATED>;
   using T = FmtTraits<FMT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -564,6 +620,43 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR>::kThreads), 1)
   };
   auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, wait(bar, parity));
+  };
+
+  [[maybe_unused]] constexpr bool kGateCall = BN <= 32;
+  // Gated: the outputs of load_columns' sums v, one row a column of the
+  // accumulator and 16 columns of C a warp, from row0 and col on.  They pass
+  // through the warp's own 512 bytes of shared memory and leave as 32-byte row
+  // pieces: no barrier between the warps.
+  [[maybe_unused]] auto put_gated = [&](const auto& v, float gate, float up, uint16_t* stage, uint16_t* c_g, int64_t row0,
+                                        int64_t col, int64_t g_rows) {
+    if constexpr (GATED) {
+      constexpr int kBlocks = sizeof(v) / (4 * sizeof(v[0]));
+      auto fill = [&](auto pair) {
+#pragma unroll
+        for (int i = 0; i < kBlocks; ++i) {
+          const uint32_t h = pair(gate * v[4 * i], up * v[4 * i + 1], gate * v[4 * i + 2], up * v[4 * i + 3]);
+          uint16_t* at = stage + (4 * i + (lane & 3)) * 16 + (lane >> 2);
+          at[0] = static_cast<uint16_t>(h);
+          at[8] = static_cast<uint16_t>(h >> 16);
+        }
+      };
+      if constexpr (kGateCall)
+        fill([&](float g0, float u0, float g1, float u1) { return gated_pair<FMT>(p.act, g0, u0, g1, u1); });
+      else if (p.act == kActSilu)
+        fill(gated_pair_as<FMT, kActSilu>);
+      else if (p.act == kActGelu)
+        fill(gated_pair_as<FMT, kActGelu>);
+      else
+        fill(gated_pair_as<FMT, kActGeluTanh>);
+      __syncwarp();
+      const int64_t mrow = row0 + (lane >> 1);
+      if (lane < 8 * kBlocks && mrow < g_rows) {
+        const int64_t at = mrow * c_cols + col + (lane & 1) * 8;
+        if (PETIT_CHECK(col + 16 <= c_cols && (c_g - p.c) + at + 8 <= p.chk_c_elems))
+          *reinterpret_cast<uint4*>(c_g + at) = *reinterpret_cast<const uint4*>(stage + lane * 8);
+      }
+      __syncwarp();   // before it is filled again
+    }
   };
 
   if (warp == kProducerWarp) {
@@ -826,6 +919,10 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR>::kThreads), 1)
         }
       }
     }
+    if constexpr (GATED && kGateCall) {   // (its code is then here when the first tile is done)
+      const uint32_t none = gated_pair<FMT>(p.act, 0.0f, 0.0f, 0.0f, 0.0f);
+      asm volatile("" ::"r"(none));
+    }
     // C, the partials and the counters may be in use by the previous kernel
     // on the stream until it has completed
     grid_dependency_wait();
@@ -851,21 +948,7 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR>::kThreads), 1)
     // against 2 us to drain a 256-row tile of the gate_up projection).
     auto put_rows = [&](const float (&val)[16], uint16_t* c_g, int64_t row0, int64_t col0,
                         int64_t g_rows, float alpha) {
-      if constexpr (GATED && C::kStageC > 0) {
-        // (16 rows x 64 columns: a vector for each of the 128 threads)
-        constexpr int kCols = kTileN / 2;
-        float h[8];
-        gate_rows(val, p.act, h);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) stage_c[(j + 8 * (r & 1)) * kCols + (r >> 1)] = out_bits<FMT>(h[j]);
-        if (!epi_sync()) return false;
-        const int64_t mrow = row0 + 4 * q + (lane >> 3), col = (col0 >> 1) + (lane & 7) * 8;
-        if (mrow < g_rows &&
-            PETIT_CHECK(col + 8 <= c_cols && (c_g - p.c) + mrow * c_cols + col + 8 <= p.chk_c_elems))
-          *reinterpret_cast<uint4*>(c_g + mrow * c_cols + col) =
-              *reinterpret_cast<const uint4*>(stage_c + (4 * q + (lane >> 3)) * kCols + (lane & 7) * 8);
-        return epi_sync();   // before the buffer is written again
-      } else if constexpr (C::kStageC > 0) {
+      if constexpr (C::kStageC > 0) {
 #pragma unroll
         for (int j = 0; j < 16; ++j) stage_c[j * kTileN + r] = out_bits<FMT>(alpha * val[j]);
         if (!epi_sync()) return false;
@@ -885,19 +968,6 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR>::kThreads), 1)
         return false;
       }
     };
-    // gated, smaller tiles: 16 rows of this lane's output column, stored directly
-    [[maybe_unused]] auto put_gated = [&](const float (&val)[16], uint16_t* c_g, int64_t row0, int64_t col, int64_t g_rows) {
-      if constexpr (GATED) {
-        float h[8];
-        gate_rows(val, p.act, h);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int64_t mrow = row0 + j + 8 * (r & 1);
-          if (mrow < g_rows && PETIT_CHECK(col < c_cols && (c_g - p.c) + mrow * c_cols + col < p.chk_c_elems))
-            c_g[mrow * c_cols + col] = out_bits<FMT>(h[j]);
-        }
-      }
-    };
     for (int64_t u = u0; u < u1; ++seg) {
       const int64_t tile = u / KS;
       const int64_t seg_end = (tile + 1) * KS < u1 ? (tile + 1) * KS : u1;
@@ -908,8 +978,6 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR>::kThreads), 1)
       const float alpha = p.alpha_dev ? alpha_dev : p.group_alpha[ec.g];
       float alpha_up = alpha;
       if constexpr (GATED) alpha_up = p.group_up[ec.g];
-      // the factor of this lane's weight row
-      [[maybe_unused]] const float row_alpha = GATED && (r & 1) ? alpha_up : alpha;
       cursor_next<BN>(p, ec);
       const int d = static_cast<int>(seg % C::kNumD);
       // split tile: its contributors and their partial slots (every
@@ -974,6 +1042,7 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR>::kThreads), 1)
       const uint32_t tbase =
           tmem + (static_cast<uint32_t>(32 * q) << 16) + C::kDColBase + d * BN;
       const int64_t ncol = (static_cast<int64_t>(nt) * wmul + rank) * kTileN + r;
+      [[maybe_unused]] const int64_t ccol = (ncol - r) / 2 + 16 * q;   // gated: this warp's 16 columns of C
       const int64_t slot = 2 * sid(cta) + (tile == first_tile_of_cta ? 0 : 1);
       float* my_slot = p.partials + static_cast<size_t>(slot) * (BN * kTileN);
       // (a partial slot holds BN x 128 floats; r < 128)
@@ -988,7 +1057,7 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR>::kThreads), 1)
         for (int t = 0; t < C::kMmaThreads; ++t) {
           if (has & (1u << t)) {
             uint32_t w[16];
-            tmem_ld_x16(tbase + (t * C::kNumD) * BN + c0, w);
+            load_columns<GATED>(tbase + (t * C::kNumD) * BN + c0, w);
             tmem_wait_ld();
 #pragma unroll
             for (int j = 0; j < 16; ++j)
@@ -996,19 +1065,19 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR>::kThreads), 1)
             have = true;
           }
         }
-        if (full_tile && C::kStageC > 0) {
+        if (GATED && full_tile) {
           float fv[16];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) fv[j] = GATED ? row_alpha * __uint_as_float(v[j]) : __uint_as_float(v[j]);
+          for (int j = 0; j < 16; ++j) fv[j] = __uint_as_float(v[j]);
+          put_gated(fv, alpha, alpha_up, stage_c + q * 256, c_g, static_cast<int64_t>(mt) * BN + c0, ccol, g_rows);
+        } else if (full_tile && C::kStageC > 0) {
+          float fv[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) fv[j] = __uint_as_float(v[j]);
           if (!put_rows(fv, c_g, static_cast<int64_t>(mt) * BN + c0, ncol - r, g_rows, alpha)) {
             c_ok = false;
             break;
           }
-        } else if (GATED && full_tile) {
-          float fv[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) fv[j] = row_alpha * __uint_as_float(v[j]);
-          put_gated(fv, c_g, static_cast<int64_t>(mt) * BN + c0, ncol >> 1, g_rows);
         } else if (full_tile) {
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
@@ -1096,9 +1165,7 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR>::kThreads), 1)
             // (stored directly: here the partial loads set the pace, and
             // staging, with its barriers between the warps, was slower)
             if constexpr (GATED) {
-#pragma unroll
-              for (int j = 0; j < 16; ++j) acc[j] *= row_alpha;
-              put_gated(acc, c_g, static_cast<int64_t>(mt) * BN + c0, ncol >> 1, g_rows);
+              put_gated(acc, alpha, alpha_up, stage_c + q * 256, c_g, static_cast<int64_t>(mt) * BN + c0, ccol, g_rows);
             } else {
 #pragma unroll
               for (int j = 0; j < 16; ++j) {
@@ -1263,7 +1330,7 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR>::kThreads), 1)
   // at consecutive addresses), adds them in CTA order and writes C.  The
   // epilogue's acquire of the arrival counter reaches every thread through
   // the barrier above.
-  if constexpr (C::kStageC > 0) {
+  if constexpr (C::kStageC > 0 && !GATED) {
     // 128/256-row tiles: the same sum, written through a shared-memory stage
     // in 256-byte row segments (as the epilogue writes whole tiles); the
     // activation ring is free by now and holds one 16-row stage per group.
@@ -1333,28 +1400,11 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR>::kThreads), 1)
               }
             }
           }
-          if constexpr (GATED) {
-            float h[8];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) acc[j] *= r & 1 ? f.alpha_up : f.alpha;
-            gate_rows(acc, p.act, h);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              gst[(j + 8 * (r & 1)) * (kTileN / 2) + (r >> 1)] = out_bits<FMT>(h[j]);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) gst[j * kTileN + r] = out_bits<FMT>(f.alpha * acc[j]);
-          }
+          for (int j = 0; j < 16; ++j) gst[j * kTileN + r] = out_bits<FMT>(f.alpha * acc[j]);
         }
         __syncthreads();
-        if (GATED && mine) {
-          const int row = 4 * q + (lane >> 3);   // warp q writes rows 4q .. 4q + 3
-          const int64_t mrow = f.row0 + m0 + row, col = (f.col0 >> 1) + (lane & 7) * 8;
-          if (mrow < f.g_rows &&
-              PETIT_CHECK(col + 8 <= c_cols && (f.c_g - p.c) + mrow * c_cols + col + 8 <= p.chk_c_elems))
-            *reinterpret_cast<uint4*>(f.c_g + mrow * c_cols + col) =
-                *reinterpret_cast<const uint4*>(gst + row * (kTileN / 2) + (lane & 7) * 8);
-        } else if (mine) {
+        if (mine) {
 #pragma unroll
           for (int s2 = 0; s2 < 2; ++s2) {
             const int row = 4 * q + 2 * s2 + (lane >> 4);   // warp q writes rows 4q .. 4q + 3
@@ -1374,7 +1424,10 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR>::kThreads), 1)
       tc_fence_after();
     }
   } else {
-    if (fix->valid && !*abort_flag) {
+    const bool run_fix = fix->valid && !*abort_flag;
+    // (gated: as above, no check raises the flag before all threads have read it)
+    if constexpr (GATED) __syncthreads();
+    if (run_fix) {
       const FixJob f = *fix;
       constexpr int kFixGroups = C::kThreads / 32 >= 16 ? 4 : 2;
       constexpr int kCols = BN / kFixGroups;               // activation rows per group
@@ -1398,11 +1451,7 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR>::kThreads), 1)
           for (int t = 0; t < C::kMmaThreads; ++t) {
             if (f.has & (1u << t)) {
               uint32_t x[kLd];
-              if constexpr (kLd == 16) {
-                tmem_ld_x16(tbase + (t * C::kNumD) * BN + c0, x);
-              } else {
-                tmem_ld_x4(tbase + (t * C::kNumD) * BN + c0, x);
-              }
+              load_columns<GATED>(tbase + (t * C::kNumD) * BN + c0, x);
               tmem_wait_ld();
   #pragma unroll
               for (int j = 0; j < kLd; ++j) own[j] = have ? own[j] + __uint_as_float(x[j]) : __uint_as_float(x[j]);
@@ -1438,18 +1487,9 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR>::kThreads), 1)
             }
           }
           if constexpr (GATED) {
-            float h[kLd / 2];
-  #pragma unroll
-            for (int j = 0; j < kLd; ++j) acc[j] *= r & 1 ? f.alpha_up : f.alpha;
-            gate_rows(acc, p.act, h);
-            const int64_t col = (f.col0 + r) >> 1;
-  #pragma unroll
-            for (int j = 0; j < kLd / 2; ++j) {
-              const int64_t mrow = f.row0 + m0 + j + (r & 1 ? kLd / 2 : 0);
-              if (mrow < f.g_rows &&
-                  PETIT_CHECK(col < c_cols && (f.c_g - p.c) + mrow * c_cols + col < p.chk_c_elems))
-                f.c_g[mrow * c_cols + col] = out_bits<FMT>(h[j]);
-            }
+            // (the activation ring is free by now: each warp has its part of it)
+            put_gated(acc, f.alpha, f.alpha_up, reinterpret_cast<uint16_t*>(sm_a) + warp * 256, f.c_g, f.row0 + m0,
+                      f.col0 / 2 + 16 * q, f.g_rows);
           } else {
   #pragma unroll
             for (int j = 0; j < kLd; ++j) {
@@ -1497,7 +1537,7 @@ using LaunchParams = Params;
 
 template <int FMT, int BN, int KU, bool PAIR = false>
 cudaError_t launch_t(const LaunchParams& prm, const CUtensorMap& tmap, cudaStream_t stream, int dev) {
-  using C = Cfg<FMT, BN, KU, PAIR>;
+  using C = Cfg<FMT, BN, KU, PAIR, kGated>;
   // the dynamic shared-memory limit is raised once per device
   static std::atomic<bool> attr_done[64];
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
@@ -1754,7 +1794,7 @@ bool set_tile_override(int bn, int ku) {
 }
 
 GemmPlan plan_grouped(const int64_t* row_off, int num_groups, int64_t n, int64_t k, int fmt,
-                      int num_sms, int pair_cap) {
+                      int num_sms, int pair_cap, bool gated) {
   GemmPlan pl{};
   pl.fmt = fmt;
   pl.num_groups = num_groups;
@@ -1774,7 +1814,11 @@ GemmPlan plan_grouped(const int64_t* row_off, int num_groups, int64_t n, int64_t
     for (int bn = 16; bn <= 256; bn *= 2) {
       int64_t tiles = 0;
       for (int g = 0; g < num_groups; ++g) tiles += (row_off[g + 1] - row_off[g] + bn - 1) / bn;
-      const int64_t cost = tiles * (bn > 128 ? bn / 128 : 1);
+      // (gated, in sixths of a 64-row tile's pass, as measured with 8 experts of
+      // 28672 x 4096 in MXFP4 and 512 rows, [39, 27, 94, 30, 25, 188, 39, 70] and
+      // others: 12.4, 14.8, 15, 24.4 and 37.6 us a pass; 167 us, 220 with 128-row tiles)
+      const int64_t cost = gated ? tiles * (bn == 16 ? 5 : bn <= 64 ? 6 : bn == 128 ? 10 : 15)
+                                 : tiles * (bn > 128 ? bn / 128 : 1);
       if (best < 0 || cost < best) {
         best = cost;
         pl.bn = bn;

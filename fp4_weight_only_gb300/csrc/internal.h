@@ -78,9 +78,10 @@ void check_limits(int64_t* weight_bytes, int64_t* c_elems);
 // Checks that the current device can run this library's kernels and gives its
 // SM count and index; returns a petit_status_t.
 int usable_device(int* sms, int* dev = nullptr);
-// row_off: num_groups + 1 non-decreasing offsets starting at 0
+// row_off: num_groups + 1 non-decreasing offsets starting at 0; gated: for
+// launch_gated
 GemmPlan plan_grouped(const int64_t* row_off, int num_groups, int64_t n, int64_t k, int fmt,
-                      int num_sms, int pair_cap);
+                      int num_sms, int pair_cap, bool gated = false);
 // Resident CTA pairs of the pair kernels on the current device (0 if none).
 int pair_capacity();
 // 0: CTA pairs where the planner expects them to pay, 1: never, 2: wherever
@@ -109,8 +110,8 @@ struct GemmArgs {
 cudaError_t launch_gemm(const GemmPlan& plan, const GemmArgs& args, const CUtensorMap& tmap_a,
                         cudaStream_t stream);
 
-// The gated product (gemm_gated.cu): weight rows 2j and 2j + 1 are the gate's
-// and the up matrix's row j, a.n counts both, C has n / 2 columns.
+// The gated product (gemm_gated.cu): weight rows 16b + i and 16b + 8 + i are the
+// gate's and the up matrix's row 8b + i, a.n counts both, C has n / 2 columns.
 enum : int { kActSilu = 0, kActGelu = 1, kActGeluTanh = 2 };
 struct GatedArgs {
   int act;

@@ -341,6 +341,19 @@ __device__ __forceinline__ void tmem_ld_x4(uint32_t taddr, uint32_t (&r)[4]) {
                : "memory");
 }
 
+// 16 lanes x 4 columns: thread 4r + c receives column c of lanes r and r + 8 (the
+// address's lane is a multiple of 16).
+__device__ __forceinline__ void tmem_ld_16x128(uint32_t taddr, uint32_t& lo, uint32_t& hi) {
+  asm volatile("tcgen05.ld.sync.aligned.16x128b.x1.b32 {%0, %1}, [%2];" : "=r"(lo), "=r"(hi) : "r"(taddr) : "memory");
+}
+// 16 lanes x 16 columns: registers 2b and 2b + 1 hold columns 4b .. 4b + 3 so.
+__device__ __forceinline__ void tmem_ld_16x128_x4(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x128b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+}
+
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }

@@ -431,9 +431,10 @@ petit_status_t petit_kv_attention(const petit_kv_cache_t* cache, const petit_kv_
  * product in one kernel:
  *     C[m][n] = act(gate_scale * A . Wg^T) * (up_scale * A . Wu^T)
  * with FP32 sums, from which act and the product are formed (FP32) and rounded
- * once.  Wg and Wu are n x k; `rep` holds them as one matrix of 2 n rows, row 2 j
- * the gate's row j and row 2 j + 1 the other's: interleave the rows of the packed
- * codes and of the scale bytes and give that to petit_repack_*(2 n, k).
+ * once.  Wg and Wu are n x k; `rep` holds them as one matrix of 2 n rows in which
+ * eight rows of the gate and eight of the other alternate (rows 16 b + i and
+ * 16 b + 8 + i are rows 8 b + i, i < 8): put the rows of the packed codes and of
+ * the scale bytes in that order and give them to petit_repack_*(2 n, k).
  * n counts C's columns: n % 64 == 0, k % 128 == 0.  fmt: the repacked format;
  * PETIT_FMT_NVFP4_F16 takes and gives FP16, the others BF16.  The two scales are
  * NVFP4's global scales (MXFP4: 1).  workspace: at least
@@ -451,7 +452,9 @@ petit_status_t petit_gated_gemm(int fmt, const void* A, const uint8_t* rep, floa
  * petit_moe_gemm_bf16_*, each expert's matrix laid out as above, C [T][n].
  * gate_scales, up_scales: host arrays of num_experts positive floats (MXFP4: may
  * be NULL).  fmt: PETIT_FMT_NVFP4 or PETIT_FMT_MXFP4.  workspace: at least
- * petit_moe_workspace_bytes(expert_offsets, num_experts, 2 n, k, fmt) bytes. */
+ * petit_moe_gated_workspace_bytes(...) bytes. */
+size_t petit_moe_gated_workspace_bytes(const int64_t* expert_offsets, int64_t num_experts, int64_t n,
+                                       int64_t k, int fmt);
 petit_status_t petit_moe_gated_gemm(int fmt, const void* A, const uint8_t* rep, const float* gate_scales,
                                     const float* up_scales, const int64_t* expert_offsets,
                                     int64_t num_experts, int act, void* C, int64_t n, int64_t k,
