@@ -82,7 +82,9 @@ class RmsNormArgs(ctypes.Structure):
 
 class RotaryArgs(ctypes.Structure):
     """petit_rotary_t"""
-    _fields_ = [("q", Rows), ("k", Rows), ("q_out", Rows), ("k_out", Rows), ("turns", _c_p), ("positions", _c_p),
+    # (petit_rows_t's members in place: one call makes it all)
+    _fields_ = [(f"{rows}_{name}", kind) for rows in ("q", "k", "q_out", "k_out") for name, kind in Rows._fields_]
+    _fields_ += [("turns", _c_p), ("positions", _c_p),
                 ("num_tokens", _c_i64), ("num_q_heads", ctypes.c_int32), ("num_k_heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("interleaved", ctypes.c_int32), ("positions_32", ctypes.c_int32), ("magnitude", ctypes.c_float)]
@@ -223,7 +225,7 @@ def _stream_on(index):
     """The current stream's handle, for calls on tensors of device `index`, which has to be the current one."""
     if torch.cuda.current_device() != index:
         raise ValueError(f"need tensors on the current device ({torch.cuda.current_device()}), got device {index}")
-    return _stream()
+    return _stream() if _raw_stream is None else _raw_stream(index)
 
 
 def _ptr(t):
@@ -648,25 +650,31 @@ def gated_repack(gate_packed, gate_scales, up_packed, up_scales, fmt="nvfp4"):
     return repack(*both, fmt)
 
 
-def _gated_args(A, rep, n, fmt, act, out, rows_k):
+@functools.lru_cache(maxsize=1024)
+def _repacked_bytes(n, k, fmt):
+    return int(load().petit_repacked_bytes(n, k, FORMATS[fmt]))
+
+
+def _gated_args(A, rep, n, fmt, act, out, groups, m, k):
     """(activation number, output) after the checks that the dense and the grouped call share."""
     dtype = torch.float16 if fmt == "nvfp4_f16" else torch.bfloat16
     _need(A, dtype, "A")
     _need(rep, torch.uint8, "rep")
-    if act not in ACTIVATIONS:
+    number = ACTIVATIONS.get(act)
+    if number is None:
         raise ValueError(f"act: need one of {', '.join(ACTIVATIONS)}")
-    groups, k = rows_k
-    if A.dim() != 2 or rep.numel() < groups * load().petit_repacked_bytes(2 * n, k, FORMATS[fmt]):
+    if rep.numel() < groups * _repacked_bytes(2 * n, k, fmt):
         raise ValueError(f"rep: need {groups} repacked matrices of {2 * n} x {k}")
+    device = A.get_device()
     if out is None:
-        out = torch.empty((A.shape[0], n), dtype=dtype, device=A.device)
+        out = torch.empty((m, n), dtype=dtype, device=A.device)
     else:
         _need(out, dtype, "out")
-        if tuple(out.shape) != (A.shape[0], n):
-            raise ValueError(f"out: need shape ({A.shape[0]}, {n})")
-    if rep.get_device() != A.get_device() or out.get_device() != A.get_device():
-        raise ValueError("rep, out: need A's device")
-    return ACTIVATIONS[act], out
+        if out.shape != (m, n) or out.get_device() != device:
+            raise ValueError(f"out: need shape ({m}, {n}) on A's device")
+    if rep.get_device() != device:
+        raise ValueError("rep: need A's device")
+    return number, out
 
 
 def gated_gemm(A, rep, n, fmt="nvfp4", global_scales=(1.0, 1.0), act="silu", workspace=None, out=None):
@@ -674,7 +682,7 @@ def gated_gemm(A, rep, n, fmt="nvfp4", global_scales=(1.0, 1.0), act="silu", wor
     as A), with FP32 sums and one rounding.  rep: :func:`gated_repack`'s;
     global_scales: (g, u), floats (MXFP4: ones); act: "silu", "gelu" or "gelu_tanh"."""
     m, k = A.shape
-    number, C = _gated_args(A, rep, n, fmt, act, out, (1, k))
+    number, C = _gated_args(A, rep, n, fmt, act, out, 1, m, k)
     need = workspace_bytes(m, 2 * n, k, fmt)
     if need == 0:
         raise PetitError(2, "gated workspace size")
@@ -694,7 +702,7 @@ def moe_gated_gemm(A, rep, expert_offsets, n, fmt="mxfp4", global_scales=None, a
     off = (ctypes.c_int64 * (E + 1))(*[int(x) for x in expert_offsets])
     if int(off[E]) != T:
         raise ValueError("expert_offsets[-1] must equal A.shape[0]")
-    number, C = _gated_args(A, rep, n, fmt, act, out, (E, k))
+    number, C = _gated_args(A, rep, n, fmt, act, out, E, T, k)
     L = load()
     need = int(L.petit_moe_gated_workspace_bytes(off, E, n, k, FORMATS[fmt]))
     if need == 0 and T > 0:
@@ -710,35 +718,57 @@ def moe_gated_gemm(A, rep, expert_offsets, n, fmt="mxfp4", global_scales=None, a
 
 
 # ----------------------------------------- around a decoder layer's products
-def _matrix(t, like, dtype, shape, name):
-    """(address, row stride) of a matrix on like's device whose rows are contiguous."""
-    # (of a dimension of one, torch's stride says nothing)
-    if (t.dtype is dtype and t.shape == shape and t.get_device() == like.get_device()
-            and (t.stride(1) == 1 or shape[1] == 1)):
-        return t.data_ptr(), t.stride(0) if shape[0] > 1 else 0
+def _matrix(t, dtype, shape, device, name):
+    """(address, row stride) of a matrix whose rows are contiguous."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device:
+        stride, one = t.stride()
+        if one == 1 or shape[1] == 1:
+            return t.data_ptr(), stride
     raise ValueError(f"{name}: need a {dtype} tensor {list(shape)} on x's device, contiguous in its last dimension")
 
 
 def _rms_norm(x, weight, eps, residual, sum_out, out, scales, group, where):
-    dtype = _DTYPES.get(x.dtype)
-    if dtype is None or x.dim() != 2 or not x.is_cuda or x.stride(1) != 1:
+    """(out, scales, sum) after the call; an output that is None is made (scales: where group is not None)."""
+    dtype = x.dtype
+    number = _DTYPES.get(dtype)
+    device = x.get_device()
+    if number is None or x.dim() != 2 or device < 0:
         raise ValueError("x: need a BF16 or FP16 CUDA tensor [rows, dim], contiguous in its last dimension")
     shape = x.shape
     rows, dim = shape
-    xp, xs = _matrix(x, x, x.dtype, shape, "x")
-    rp, rs = (None, 0) if residual is None else _matrix(residual, x, x.dtype, shape, "residual")
-    sp, ss = (None, 0) if sum_out is None else _matrix(sum_out, x, x.dtype, shape, "sum_out")
+    xp, xs = _matrix(x, dtype, shape, device, "x")
     f32, wp = 0, None
     if weight is not None:
         f32 = int(weight.dtype is torch.float32)
-        if ((not f32 and weight.dtype is not x.dtype) or weight.shape != (dim,) or not weight.is_contiguous()
-                or weight.get_device() != x.get_device()):
-            raise ValueError(f"weight: need a contiguous {x.dtype} or FP32 tensor [{dim}] on x's device")
+        if ((not f32 and weight.dtype is not dtype) or weight.shape != shape[1:] or not weight.is_contiguous()
+                or weight.get_device() != device):
+            raise ValueError(f"weight: need a contiguous {dtype} or FP32 tensor [{dim}] on x's device")
         wp = weight.data_ptr()
-    op, os_ = _matrix(out, x, x.dtype if scales is None else torch.float8_e4m3fn, shape, "out")
-    cp, cs = (None, 0) if scales is None else _matrix(scales, x, torch.float32, (rows, dim // (group or dim)), "scales")
-    args = RmsNormArgs(xp, rp, wp, sp, op, cp, rows, dim, xs, rs, ss, os_, cs, dtype, f32, eps, group)
-    _check(load().petit_rms_norm(ctypes.byref(args), _stream_on(x.get_device())), where)
+    rp = sp = cp = None
+    rs = ss = cs = 0
+    if residual is not None:
+        rp, rs = _matrix(residual, dtype, shape, device, "residual")
+        if sum_out is None:   # (new ones: empty_like's rows are contiguous or as x's)
+            sum_out = torch.empty_like(x)
+            sp, ss = sum_out.data_ptr(), sum_out.stride(0)
+    if sp is None and sum_out is not None:
+        sp, ss = _matrix(sum_out, dtype, shape, device, "sum_out")
+    out_type = dtype if group is None else torch.float8_e4m3fn
+    if out is None:
+        out = torch.empty_like(x) if group is None else torch.empty_like(x, dtype=out_type)
+        op, os_ = out.data_ptr(), out.stride(0)
+    else:
+        op, os_ = _matrix(out, out_type, shape, device, "out")
+    if group is not None:
+        columns = dim // (group or dim)
+        if scales is None:
+            scales = torch.empty((rows, columns), dtype=torch.float32, device=x.device)
+            cp, cs = scales.data_ptr(), columns
+        else:
+            cp, cs = _matrix(scales, torch.float32, (rows, columns), device, "scales")
+    args = RmsNormArgs(xp, rp, wp, sp, op, cp, rows, dim, xs, rs, ss, os_, cs, number, f32, eps, group or 0)
+    _check(load().petit_rms_norm(ctypes.byref(args), _stream_on(device)), where)
+    return out, scales, sum_out
 
 
 def rms_norm(x, weight=None, eps=1e-6, residual=None, out=None, sum_out=None):
@@ -747,11 +777,7 @@ def rms_norm(x, weight=None, eps=1e-6, residual=None, out=None, sum_out=None):
     8; dim a multiple of 8, at most 32768), computed in FP32 and rounded once.
     `weight`: x's type or FP32, [dim]; None: ones.  Returns y, or (y, s rounded)
     if there is a residual.  `out` may be x, `sum_out` x or residual."""
-    if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    if sum_out is None and residual is not None:
-        sum_out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    _rms_norm(x, weight, eps, residual, sum_out, out, None, 0, "rms_norm")
+    out, _, sum_out = _rms_norm(x, weight, eps, residual, sum_out, out, None, None, "rms_norm")
     return out if residual is None else (out, sum_out)
 
 
@@ -762,13 +788,7 @@ def rms_norm_e4m3(x, weight=None, eps=1e-6, residual=None, group=128, out=None, 
     whole row), the largest |y| of the group / 448; y is about code * scale."""
     if x.dim() != 2 or group < 0 or (group and x.shape[1] % group):
         raise ValueError(f"x, group: need [rows, dim] with dim a multiple of the group, got {tuple(x.shape)}, {group}")
-    if out is None:
-        out = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
-    if scales is None:
-        scales = torch.empty((x.shape[0], x.shape[1] // (group or x.shape[1])), dtype=torch.float32, device=x.device)
-    if sum_out is None and residual is not None:
-        sum_out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    _rms_norm(x, weight, eps, residual, sum_out, out, scales, group, "rms_norm_e4m3")
+    out, scales, sum_out = _rms_norm(x, weight, eps, residual, sum_out, out, scales, group, "rms_norm_e4m3")
     return (out, scales) if residual is None else (out, scales, sum_out)
 
 
@@ -818,20 +838,21 @@ class Rotary:
         self.turns = torch.tensor([turns(f) for f in frequencies], dtype=torch.int64,
                                   device=torch.device(device or "cuda"))
         self.rot_dim, self.interleaved, self.magnitude = rot_dim, bool(interleaved), float(magnitude)
-        self.device_index = self.turns.get_device()
+        self.device_index, self.turns_address = self.turns.get_device(), self.turns.data_ptr()
 
     def __call__(self, q, k, positions, out=None):
         return rotary(self, q, k, positions, out)
 
 
-def _heads(t, rope, like, name):
-    """petit_rows_t of [tokens, heads, head_dim] on the frequencies' device, contiguous in its last dimension."""
-    if (t.dim() == 3 and t.dtype is like.dtype and t.shape[0] == like.shape[0] and t.shape[2] == like.shape[2]
-            and t.stride(2) == 1 and t.get_device() == rope.device_index):
-        # (of a dimension of one, torch's stride says nothing)
-        return Rows(t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0)
-    raise ValueError(f"{name}: need a {like.dtype} tensor [{like.shape[0]}, heads, {like.shape[2]}] on the "
-                     f"frequencies' device, contiguous in its last dimension")
+def _heads(t, dtype, tokens, head_dim, device, name):
+    """(address, token stride, head stride) of [tokens, heads, head_dim] that is contiguous in its last dimension."""
+    if t.dtype is dtype and t.get_device() == device and t.dim() == 3:
+        n, _, d = t.shape
+        token, head, one = t.stride()
+        if n == tokens and d == head_dim and one == 1:
+            return t.data_ptr(), token, head
+    raise ValueError(f"{name}: need a {dtype} tensor [{tokens}, heads, {head_dim}] on the frequencies' device, "
+                     f"contiguous in its last dimension")
 
 
 def rotary(rope, q, k, positions, out=None):
@@ -840,25 +861,30 @@ def rotary(rope, q, k, positions, out=None):
     `positions` (int64 or int32 [tokens]).  `rope`: a :class:`Rotary`.  Returns
     (q, k) as new tensors, or in `out`, a pair of such tensors: (q, k) itself
     turns them in place."""
-    if q.dtype not in _DTYPES or q.dim() != 3:
+    dtype, device = q.dtype, rope.device_index
+    number = _DTYPES.get(dtype)
+    if number is None or q.dim() != 3:
         raise ValueError("q: need a BF16 or FP16 tensor [tokens, heads, head_dim]")
-    n = q.shape[0]
+    n, q_heads, d = q.shape
+    rows = _heads(q, dtype, n, d, device, "q")
+    rows_k = (None, 0, 0) if k is None else _heads(k, dtype, n, d, device, "k")
     if out is None:
-        out = tuple(None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k))
-    rq, ro = _heads(q, rope, q, "q"), _heads(out[0], rope, q, "out[0]")
-    rk = rko = Rows()
-    if k is not None:
-        rk, rko = _heads(k, rope, q, "k"), _heads(out[1], rope, q, "out[1]")
-    if out[0].shape != q.shape or (k is not None and out[1].shape != k.shape):
-        raise ValueError("out: need tensors of q's and k's shapes")
+        out = torch.empty_like(q), None if k is None else torch.empty_like(k)
+    if out[0] is q and out[1] is k:
+        rows_out, rows_k_out = rows, rows_k
+    else:
+        if out[0].shape != q.shape or (k is not None and out[1].shape != k.shape):
+            raise ValueError("out: need tensors of q's and k's shapes")
+        rows_out = _heads(out[0], dtype, n, d, device, "out[0]")
+        rows_k_out = rows_k if k is None else _heads(out[1], dtype, n, d, device, "out[1]")
     wide = positions.dtype is torch.int64
     if ((not wide and positions.dtype is not torch.int32) or positions.shape != (n,) or not positions.is_contiguous()
-            or positions.get_device() != rope.device_index):
+            or positions.get_device() != device):
         raise ValueError(f"positions: need a contiguous int64 or int32 tensor [{n}] on the frequencies' device")
-    args = RotaryArgs(rq, rk, ro, rko, rope.turns.data_ptr(), positions.data_ptr(), n, q.shape[1],
-                      0 if k is None else k.shape[1], q.shape[2], rope.rot_dim, _DTYPES[q.dtype], rope.interleaved,
-                      not wide, rope.magnitude)
-    _check(load().petit_rotary(ctypes.byref(args), _stream_on(rope.device_index)), "rotary")
+    args = RotaryArgs(*rows, *rows_k, *rows_out, *rows_k_out, rope.turns_address, positions.data_ptr(), n, q_heads,
+                      0 if k is None else k.shape[1], d, rope.rot_dim, number, rope.interleaved, not wide,
+                      rope.magnitude)
+    _check(load().petit_rotary(ctypes.byref(args), _stream_on(device)), "rotary")
     return out
 
 

@@ -16,22 +16,23 @@ bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 
 petit_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? PETIT_OK : PETIT_ERR_CUDA; }
 
-petit_status_t check_rows(const petit_rows_t& r, petit::KvRows* out) {
+// (the stride of a dimension of one is not looked at)
+petit_status_t check_rows(const petit_rows_t& r, int64_t tokens, int64_t heads, petit::KvRows* out) {
+  *out = {r.data, tokens > 1 ? r.token_stride : 0, heads > 1 ? r.head_stride : 0};
   if (!r.data) return PETIT_ERR_INVALID_ARG;
-  if (!aligned(r.data, 16) || r.token_stride % 8 || r.head_stride % 8) return PETIT_ERR_MISALIGNED;
-  *out = {r.data, r.token_stride, r.head_stride};
+  if (!aligned(r.data, 16) || out->token_stride % 8 || out->head_stride % 8) return PETIT_ERR_MISALIGNED;
   return PETIT_OK;
 }
 
 // Rows to read and rows to write: `out` has rows of its own, or is `in` itself.
 petit_status_t check_turned(const petit_rows_t& in, const petit_rows_t& out, const petit_rotary_t& r, int32_t heads,
                             petit::KvRows* in_rows, petit::KvRows* out_rows) {
-  if (petit_status_t st = check_rows(in, in_rows)) return st;
-  if (petit_status_t st = check_rows(out, out_rows)) return st;
+  if (petit_status_t st = check_rows(in, r.num_tokens, heads, in_rows)) return st;
+  if (petit_status_t st = check_rows(out, r.num_tokens, heads, out_rows)) return st;
   auto apart = [&](int64_t stride, int64_t count) { return count <= 1 || stride >= r.head_dim || stride <= -r.head_dim; };
   if (!apart(out.token_stride, r.num_tokens) || !apart(out.head_stride, heads)) return PETIT_ERR_INVALID_ARG;
-  if (in.data == out.data && ((r.num_tokens > 1 && in.token_stride != out.token_stride) ||
-                              (heads > 1 && in.head_stride != out.head_stride)))
+  if (in.data == out.data &&
+      (in_rows->token_stride != out_rows->token_stride || in_rows->head_stride != out_rows->head_stride))
     return PETIT_ERR_INVALID_ARG;
   return PETIT_OK;
 }
@@ -69,11 +70,13 @@ petit_status_t petit_rms_norm(const petit_rms_norm_t* args, petit_stream_t strea
       (args->scales && (args->out == args->x || args->out == args->residual)))
     return PETIT_ERR_INVALID_ARG;
   if (!aligned(args->x, 16) || !aligned(args->residual, 16) || !aligned(args->weight, 16) || !aligned(args->sum, 16) ||
-      !aligned(args->out, 16) || !aligned(args->scales, 4) || args->x_stride % 8 ||
-      (args->residual && args->residual_stride % 8) || (args->sum && args->sum_stride % 8) || args->out_stride % 8)
+      !aligned(args->out, 16) || !aligned(args->scales, 4))
     return PETIT_ERR_MISALIGNED;
-  if (int st = petit::usable_device(nullptr)) return static_cast<petit_status_t>(st);
+  if (args->rows > 1 && (args->x_stride % 8 || (args->residual && args->residual_stride % 8) ||
+                         (args->sum && args->sum_stride % 8) || args->out_stride % 8))
+    return PETIT_ERR_MISALIGNED;
   petit::NormArgs a{};
+  if (int st = petit::usable_device(nullptr)) return static_cast<petit_status_t>(st);
   a.x = static_cast<const uint16_t*>(args->x);
   a.residual = static_cast<const uint16_t*>(args->residual);
   a.weight = args->weight;
@@ -87,7 +90,7 @@ petit_status_t petit_rms_norm(const petit_rms_norm_t* args, petit_stream_t strea
   a.out_stride = args->out_stride;
   a.scale_stride = args->scale_stride;
   a.dim = static_cast<int32_t>(args->dim);
-  a.group = static_cast<int32_t>(group);
+  for (int64_t v = group / 8; args->group != 0 && v > 1; v /= 2) ++a.group_shift;
   a.eps = args->eps;
   a.weight_f32 = args->weight_f32 != 0;
   return from_cuda(petit::launch_rms_norm(a, args->dtype == PETIT_BF16, reinterpret_cast<cudaStream_t>(stream)));

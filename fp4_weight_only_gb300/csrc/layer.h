@@ -19,7 +19,7 @@ struct NormArgs {
   int64_t rows;
   int64_t x_stride, residual_stride, sum_stride, out_stride, scale_stride;   // elements
   int32_t dim;
-  int32_t group;              // elements a scale; dim: a scale a row
+  int32_t group_shift;        // a scale holds 2^group_shift vectors of 8 elements; 0: a row
   float eps;
   bool weight_f32;
 };

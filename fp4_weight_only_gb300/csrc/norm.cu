@@ -5,8 +5,6 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
-#include <type_traits>
-
 #include "layer.h"
 #include "ptx.cuh"
 #include "rows16.cuh"
@@ -15,141 +13,185 @@ namespace petit {
 namespace {
 
 constexpr int kWarp = 32;
+constexpr int kRowsPerBlock = 4;   // where a row is a warp's
 
-template <int TPR, typename F>
+// f over a row's values: a warp's, or those of a block's warps (`shared`: one each).
+template <bool WARP_ROW, typename F>
 __device__ __forceinline__ float row_reduce(float v, float* shared, F&& f) {
 #pragma unroll
   for (int o = kWarp / 2; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-  if constexpr (TPR > kWarp) {
-    constexpr int kWarps = TPR / kWarp;
+  if constexpr (!WARP_ROW) {
     const int lane = threadIdx.x & (kWarp - 1);
     if (lane == 0) shared[threadIdx.x / kWarp] = v;
     __syncthreads();
-    v = shared[lane & (kWarps - 1)];
+    v = lane < static_cast<int>(blockDim.x) / kWarp ? shared[lane] : 0.0f;   // (sums, and maxima of magnitudes)
 #pragma unroll
-    for (int o = kWarps / 2; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    for (int o = kWarp / 2; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
   }
   return v;
 }
 
-// TPR threads a row (a block holds one row, or as many as warps where a row is
-// a warp's), VPT vectors of 8 elements a thread.
-template <int TPR, int VPT, bool BF16, bool E4M3>
-__global__ void __launch_bounds__(TPR > kWarp ? TPR : 4 * kWarp) norm_kernel(const __grid_constant__ NormArgs a) {
-  __shared__ float part[2][TPR / kWarp];
-  const int64_t row = TPR > kWarp ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / kWarp;
-  const int t = TPR > kWarp ? threadIdx.x : threadIdx.x & (kWarp - 1);
+// A row is a warp's (kRowsPerBlock rows a block) or a block's of at most THREADS
+// threads; each thread holds VPT vectors of 8 elements.  One pass: a row stays in
+// registers between its two uses.  FP32 steps are taken two at a time.
+template <bool WARP_ROW, int THREADS, int VPT, bool BF16, bool E4M3>
+__global__ void __launch_bounds__(THREADS) norm_kernel(const __grid_constant__ NormArgs a) {
+  __shared__ float part[2][kWarp];
+  const int TPR = WARP_ROW ? kWarp : blockDim.x;   // threads a row
+  const int t = WARP_ROW ? threadIdx.x & (kWarp - 1) : threadIdx.x;
+  const int vectors = a.dim / 8;
+  const int64_t row = WARP_ROW ? static_cast<int64_t>(blockIdx.x) * kRowsPerBlock + threadIdx.x / kWarp : blockIdx.x;
   grid_dependency_wait();
   // (only now: what a kernel before this one wrote is in memory before the next one may begin)
   grid_launch_dependents();
   if (row >= a.rows) return;
-  const int vectors = a.dim / 8;
-  float s[VPT][8];
-  float squares = 0.0f;
+  const uint16_t* x_row = a.x + row * a.x_stride + t * 8;
+  const uint16_t* r_row = a.residual + row * a.residual_stride + t * 8;
+  float2 s[VPT][4];
+  if (a.residual) {
+    uint4 x[VPT], r[VPT];
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int v = i * TPR + t;
-    uint4 x = make_uint4(0, 0, 0, 0), r = x;
-    if (v < vectors) {
-      x = *reinterpret_cast<const uint4*>(a.x + row * a.x_stride + v * 8);
-      if (a.residual) r = *reinterpret_cast<const uint4*>(a.residual + row * a.residual_stride + v * 8);
-    }
-    unpack8<BF16>(x, s[i]);
-    if (a.residual) {
-      float f[8];
-      unpack8<BF16>(r, f);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s[i][j] += f[j];
+    for (int i = 0; i < VPT; ++i) {
+      x[i] = r[i] = make_uint4(0, 0, 0, 0);
+      if (i * TPR + t < vectors) {
+        x[i] = *reinterpret_cast<const uint4*>(x_row + i * (TPR * 8));
+        r[i] = *reinterpret_cast<const uint4*>(r_row + i * (TPR * 8));
+      }
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) squares += s[i][j] * s[i][j];
+    for (int i = 0; i < VPT; ++i) {
+      float2 f[4];
+      unpack8<BF16>(x[i], s[i]);
+      unpack8<BF16>(r[i], f);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[i][j] = add2(s[i][j], f[j]);
+    }
+  } else {
+    uint4 x[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+      x[i] = i * TPR + t < vectors ? *reinterpret_cast<const uint4*>(x_row + i * (TPR * 8)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) unpack8<BF16>(x[i], s[i]);
   }
-  squares = row_reduce<TPR>(squares, part[0], [](float p, float q) { return p + q; });
-  const float norm = rsqrtf(squares / static_cast<float>(a.dim) + a.eps);
-  float top = 0.0f;   // of the row (fmaxf leaves NaN out)
+  float2 squares = make_float2(0.0f, 0.0f);
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int v = i * TPR + t;
-    if (v < vectors && a.sum)
-      *reinterpret_cast<uint4*>(a.sum + row * a.sum_stride + v * 8) = pack8<BF16>(s[i]);
-    if (v < vectors) {
-      float w[8];
-      if (!a.weight) {
+  for (int i = 0; i < VPT; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = 1.0f;
-      } else if (a.weight_f32) {
-        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.weight) + v * 8);
+    for (int j = 0; j < 4; ++j) squares = fma2(s[i][j], s[i][j], squares);
+  const float total = row_reduce<WARP_ROW>(squares.x + squares.y, part[0], [](float p, float q) { return p + q; });
+  const float norm = rsqrtf(total / static_cast<float>(a.dim) + a.eps);
+  const float2 norm2 = make_float2(norm, norm);
+  if (a.sum) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+      if (i * TPR + t < vectors)
+        *reinterpret_cast<uint4*>(a.sum + row * a.sum_stride + (i * TPR + t) * 8) = pack8<BF16>(s[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < VPT; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[i][j] = mul2(s[i][j], norm2);
+  if (a.weight) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      float2 f[4];
+      if (i * TPR + t >= vectors) break;
+      if (a.weight_f32) {
+        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.weight) + (i * TPR + t) * 8);
         const float4 lo = p[0], hi = p[1];
-        w[0] = lo.x, w[1] = lo.y, w[2] = lo.z, w[3] = lo.w, w[4] = hi.x, w[5] = hi.y, w[6] = hi.z, w[7] = hi.w;
+        f[0] = make_float2(lo.x, lo.y), f[1] = make_float2(lo.z, lo.w);
+        f[2] = make_float2(hi.x, hi.y), f[3] = make_float2(hi.z, hi.w);
       } else {
-        unpack8<BF16>(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.weight) + v * 8), w);
+        unpack8<BF16>(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.weight) + (i * TPR + t) * 8), f);
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s[i][j] = s[i][j] * norm * w[j];
-    }
-    if constexpr (!E4M3) {
-      if (v < vectors)
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row * a.out_stride + v * 8) = pack8<BF16>(s[i]);
-    } else if (a.group != a.dim) {
-      // a scale's elements lie in group / 8 neighbouring lanes
-      float m = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(s[i][j]));
-      for (int o = a.group / 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-      const float scale = fmaxf(m, 1e-8f) / 448.0f;
-      if (v < vectors) {
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + row * a.out_stride + v * 8) = e4m3x8(s[i], scale);
-        if (v % (a.group / 8) == 0) a.scales[row * a.scale_stride + v / (a.group / 8)] = scale;
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(s[i][j]));
+      for (int j = 0; j < 4; ++j) s[i][j] = mul2(s[i][j], f[j]);
     }
   }
-  if constexpr (E4M3) {
-    if (a.group == a.dim) {
-      top = row_reduce<TPR>(top, part[1], [](float p, float q) { return fmaxf(p, q); });
-      const float scale = fmaxf(top, 1e-8f) / 448.0f;
-      if (t == 0) a.scales[row * a.scale_stride] = scale;
+  if constexpr (!E4M3) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+      if (i * TPR + t < vectors)
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row * a.out_stride + (i * TPR + t) * 8) = pack8<BF16>(s[i]);
+  } else {
+    float top[VPT];   // (fmaxf leaves NaN out)
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      top[i] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) top[i] = fmaxf(top[i], fmaxf(fabsf(s[i][j].x), fabsf(s[i][j].y)));
+    }
+    uint8_t* codes = static_cast<uint8_t*>(a.out) + row * a.out_stride;
+    float* scales = a.scales + row * a.scale_stride;
+    // vectors a scale: a power of two of neighbouring lanes', or the row's
+    const int shift = a.group_shift;
+    if (shift == 0) {
+#pragma unroll
+      for (int i = 1; i < VPT; ++i) top[0] = fmaxf(top[0], top[i]);
+      const E4M3Scale scale =
+          e4m3_scale(row_reduce<WARP_ROW>(top[0], part[1], [](float p, float q) { return fmaxf(p, q); }));
+      if (t == 0) scales[0] = scale.scale;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+        if (i * TPR + t < vectors) *reinterpret_cast<uint2*>(codes + (i * TPR + t) * 8) = e4m3x8(s[i], scale);
+    } else {
+      for (int o = 1 << (shift - 1); o > 0; o >>= 1) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], o));
+      }
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         const int v = i * TPR + t;
-        if (v < vectors)
-          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + row * a.out_stride + v * 8) = e4m3x8(s[i], scale);
+        const E4M3Scale scale = e4m3_scale(top[i]);
+        if (v < vectors) {
+          *reinterpret_cast<uint2*>(codes + v * 8) = e4m3x8(s[i], scale);
+          if ((v & ((1 << shift) - 1)) == 0) scales[v >> shift] = scale.scale;
+        }
       }
     }
   }
 }
 
-template <int TPR, int VPT, bool BF16, bool E4M3>
+template <bool WARP_ROW, int THREADS, int VPT, bool BF16, bool E4M3>
 cudaError_t launch(const NormArgs& a, cudaStream_t stream) {
+  const int64_t blocks = WARP_ROW ? (a.rows + kRowsPerBlock - 1) / kRowsPerBlock : a.rows;
+  const int threads = (a.dim / 8 + VPT - 1) / VPT;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(TPR > kWarp ? a.rows : (a.rows + 3) / 4));
-  cfg.blockDim = dim3(TPR > kWarp ? TPR : 4 * kWarp);
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(WARP_ROW ? THREADS : (threads + kWarp - 1) / kWarp * kWarp);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, norm_kernel<TPR, VPT, BF16, E4M3>, a);
+  return cudaLaunchKernelEx(&cfg, norm_kernel<WARP_ROW, THREADS, VPT, BF16, E4M3>, a);
 }
 
-template <int TPR, int VPT>
+template <bool WARP_ROW, int THREADS, int VPT>
 cudaError_t launch_as(const NormArgs& a, bool bf16, cudaStream_t s) {
-  if (a.scales) return bf16 ? launch<TPR, VPT, true, true>(a, s) : launch<TPR, VPT, false, true>(a, s);
-  return bf16 ? launch<TPR, VPT, true, false>(a, s) : launch<TPR, VPT, false, false>(a, s);
+  if (a.scales)
+    return bf16 ? launch<WARP_ROW, THREADS, VPT, true, true>(a, s) : launch<WARP_ROW, THREADS, VPT, false, true>(a, s);
+  return bf16 ? launch<WARP_ROW, THREADS, VPT, true, false>(a, s) : launch<WARP_ROW, THREADS, VPT, false, false>(a, s);
 }
 
 }  // namespace
 
 cudaError_t launch_rms_norm(const NormArgs& a, bool bf16, cudaStream_t stream) {
   const int vectors = a.dim / 8;
-  if (vectors <= 32) return launch_as<32, 1>(a, bf16, stream);
-  if (vectors <= 128) return launch_as<32, 4>(a, bf16, stream);
-  if (vectors <= 1024) return launch_as<256, 4>(a, bf16, stream);
-  if (vectors <= 4096) return launch_as<1024, 4>(a, bf16, stream);
-  return cudaErrorInvalidValue;
+  constexpr int kWarps = kRowsPerBlock * kWarp;
+  if (vectors <= kWarp) return launch_as<true, kWarps, 1>(a, bf16, stream);
+  // Few elements: the widest blocks, one vector a thread, since a row's latency
+  // is all there is.  Many: four vectors a thread, so that loads cover the wait
+  // for memory and a row's two barriers and shuffles are shared by more of it.
+  // (8192 elements, us with one vector and with four: 1 row 2.2 and 2.6, 152 rows
+  // 2.6 and 3.1, 333 rows 4.7 and 4.6, 8192 rows 88 and 78, in E4M3 76 and 44;
+  // 1024 elements, 1024 rows: 2.5 and 3.0)
+  if (vectors <= 1024 && a.rows * a.dim <= int64_t(1) << 21) return launch_as<false, 1024, 1>(a, bf16, stream);
+  if (vectors <= 4 * kWarp) return launch_as<true, kWarps, 4>(a, bf16, stream);
+  if (vectors <= 4 * 512) return launch_as<false, 512, 4>(a, bf16, stream);
+  return launch_as<false, 1024, 4>(a, bf16, stream);
 }
 
 }  // namespace petit

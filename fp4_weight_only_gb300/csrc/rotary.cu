@@ -30,9 +30,9 @@ template <> struct Vec<4> { using T = uint2; };
 template <> struct Vec<2> { using T = uint32_t; };
 template <> struct Vec<1> { using T = uint16_t; };
 
+// The V elements of a vector, to and from FP32.
 template <int V, bool BF16>
-__device__ __forceinline__ void load(const uint16_t* p, float* x) {
-  const typename Vec<V>::T v = *reinterpret_cast<const typename Vec<V>::T*>(p);
+__device__ __forceinline__ void unpack(const typename Vec<V>::T& v, float (&x)[V]) {
   if constexpr (V == 1) {
     x[0] = unpack16<BF16>(v).x;
   } else {
@@ -45,9 +45,8 @@ __device__ __forceinline__ void load(const uint16_t* p, float* x) {
     }
   }
 }
-
 template <int V, bool BF16>
-__device__ __forceinline__ void store(uint16_t* p, const float* x) {
+__device__ __forceinline__ typename Vec<V>::T pack(const float (&x)[V]) {
   typename Vec<V>::T v;
   if constexpr (V == 1) {
     v = static_cast<uint16_t>(pack16<BF16>(x[0], 0.0f));
@@ -56,119 +55,135 @@ __device__ __forceinline__ void store(uint16_t* p, const float* x) {
 #pragma unroll
     for (int i = 0; i < V / 2; ++i) w[i] = pack16<BF16>(x[2 * i], x[2 * i + 1]);
   }
-  *reinterpret_cast<typename Vec<V>::T*>(p) = v;
+  return v;
 }
 
-// A thread turns V pairs (two vectors) of HPT heads of a token, `groups` heads
-// apart; threads past the pairs copy the head's other elements.
-template <int V, int HPT, bool INTER, bool BF16>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryArgs a, uint32_t units,
-                                                          uint32_t groups) {
-  const uint64_t index = static_cast<uint64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const uint32_t row = static_cast<uint32_t>(index / units);   // (below 2^32: checked by the host)
-  const uint32_t u = static_cast<uint32_t>(index - static_cast<uint64_t>(row) * units);
-  const int64_t token = row / groups;
-  const int group = static_cast<int>(row - static_cast<uint32_t>(token) * groups);
+// A thread takes the same place of HEADS heads of a token, `groups` heads apart,
+// so that an angle's sine and cosine are taken once for them, while all their
+// loads are on their way: two vectors of V elements rot_dim / 2 apart, or (INTER)
+// one vector of neighbouring pairs.  Threads past the turned elements copy the
+// rest.  Blocks are [places in a head][rows], a row a token's group of heads.
+template <int V, int HEADS, bool INTER, bool BF16>
+__global__ void __launch_bounds__(V >= 4 ? kThreads : 1024) rotary_kernel(const __grid_constant__ RotaryArgs a, uint32_t groups) {
+  using T = typename Vec<V>::T;
+  constexpr int kVectors = INTER ? 1 : 2;
+  constexpr int kPairs = kVectors * V / 2;
+  const int u = threadIdx.x;
+  const uint32_t row = blockIdx.x * blockDim.y + threadIdx.y;   // (below 2^32: checked by the host)
+  const uint32_t token = row / groups;
+  const int first = static_cast<int>(row - token * groups);
   grid_dependency_wait();
   // (only now: what a kernel before this one wrote is in memory before the next one may begin)
   grid_launch_dependents();
   if (token >= a.tokens) return;
-  const int turning = a.rot_dim / (2 * V);
-  const bool rotate = static_cast<int>(u) < turning;
-  // the two vectors' places in a head
-  const int half = a.rot_dim / 2;
-  int at0, at1;
-  if (rotate) {
-    at0 = INTER ? u * 2 * V : u * V;
-    at1 = INTER ? at0 + V : at0 + half;
-  } else {
-    at0 = a.rot_dim + (u - turning) * 2 * V;
-    at1 = at0 + V;
-  }
-  const bool second = at1 < a.head_dim;
-  float x[HPT][2 * V];
-  const uint16_t* src[HPT];
-  uint16_t* dst[HPT];
+  const int turning = a.rot_dim / (kVectors * V);
+  const bool rotate = u < turning;
+  // the vectors' places in a head
+  const int at0 = rotate ? u * V : a.rot_dim + (u - turning) * kVectors * V;
+  const int at1 = rotate ? at0 + a.rot_dim / 2 : at0 + V;
+  const bool second = !INTER && at1 < a.head_dim;
+  float c[kPairs], s[kPairs];
+  T v[HEADS][kVectors];
 #pragma unroll
-  for (int i = 0; i < HPT; ++i) {
-    const int h = group + i * static_cast<int>(groups);
-    const bool is_q = h < a.q_heads;
-    const int hh = is_q ? h : h - a.q_heads;
-    const KvRows& in = is_q ? a.q : a.k;
-    const KvRows& out = is_q ? a.q_out : a.k_out;
-    src[i] = static_cast<const uint16_t*>(in.data) + token * in.token_stride + hh * in.head_stride;
-    dst[i] = static_cast<uint16_t*>(out.data) + token * out.token_stride + hh * out.head_stride;
-    if (h < a.heads) {
-      load<V, BF16>(src[i] + at0, x[i]);
-      if (second) load<V, BF16>(src[i] + at1, x[i] + V);
-    }
+  for (int i = 0; i < HEADS; ++i) {
+    const int h = first + i * static_cast<int>(groups);
+    if (h >= a.heads) break;
+    const KvRows& in = h < a.q_heads ? a.q : a.k;
+    const uint16_t* src = static_cast<const uint16_t*>(in.data) + static_cast<int64_t>(token) * in.token_stride +
+                          (h < a.q_heads ? h : h - a.q_heads) * in.head_stride;
+    v[i][0] = *reinterpret_cast<const T*>(src + at0);
+    if (second) v[i][kVectors - 1] = *reinterpret_cast<const T*>(src + at1);
   }
-  float c[V], s[V];
   if (rotate) {
-    const uint64_t p = a.positions_32 ? static_cast<uint64_t>(static_cast<int64_t>(static_cast<const int32_t*>(a.positions)[token]))
-                                      : static_cast<uint64_t>(static_cast<const int64_t*>(a.positions)[token]);
+    const uint64_t p = a.positions_32
+                           ? static_cast<uint64_t>(static_cast<int64_t>(static_cast<const int32_t*>(a.positions)[token]))
+                           : static_cast<uint64_t>(static_cast<const int64_t*>(a.positions)[token]);
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int32_t part = static_cast<int32_t>((p * a.turns[u * V + j]) >> 32);
+    for (int j = 0; j < kPairs; ++j) {
+      const int32_t part = static_cast<int32_t>((p * a.turns[u * kPairs + j]) >> 32);
       const float angle = static_cast<float>(part) * 1.46291807926715968e-9f;   // 2 pi / 2^32
       c[j] = a.magnitude * __cosf(angle);
       s[j] = a.magnitude * __sinf(angle);
     }
   }
 #pragma unroll
-  for (int i = 0; i < HPT; ++i) {
-    if (group + i * static_cast<int>(groups) >= a.heads) break;
+  for (int i = 0; i < HEADS; ++i) {
+    const int h = first + i * static_cast<int>(groups);
+    if (h >= a.heads) break;
     if (rotate) {
-      float y[2 * V];
+      float x[kVectors][V], y[kVectors][V];
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int ia = INTER ? 2 * j : j, ib = INTER ? 2 * j + 1 : j + V;
-        y[ia] = x[i][ia] * c[j] - x[i][ib] * s[j];
-        y[ib] = x[i][ib] * c[j] + x[i][ia] * s[j];
+      for (int k = 0; k < kVectors; ++k) unpack<V, BF16>(v[i][k], x[k]);
+#pragma unroll
+      for (int j = 0; j < kPairs; ++j) {
+        // the pair's elements: neighbours, or one of each vector
+        constexpr int kSecond = kVectors - 1;
+        const int ia = INTER ? 2 * j : j, ib = INTER ? 2 * j + 1 : j;
+        y[0][ia] = x[0][ia] * c[j] - x[kSecond][ib] * s[j];
+        y[kSecond][ib] = x[kSecond][ib] * c[j] + x[0][ia] * s[j];
       }
-      store<V, BF16>(dst[i] + at0, y);
-      store<V, BF16>(dst[i] + at1, y + V);
-    } else {
-      store<V, BF16>(dst[i] + at0, x[i]);
-      if (second) store<V, BF16>(dst[i] + at1, x[i] + V);
+#pragma unroll
+      for (int k = 0; k < kVectors; ++k) v[i][k] = pack<V, BF16>(y[k]);
     }
+    const KvRows& out = h < a.q_heads ? a.q_out : a.k_out;
+    uint16_t* dst = static_cast<uint16_t*>(out.data) + static_cast<int64_t>(token) * out.token_stride +
+                    (h < a.q_heads ? h : h - a.q_heads) * out.head_stride;
+    *reinterpret_cast<T*>(dst + at0) = v[i][0];
+    if (second) *reinterpret_cast<T*>(dst + at1) = v[i][kVectors - 1];
   }
 }
 
-template <int V, int HPT, bool INTER, bool BF16>
+template <int V, int HEADS, bool INTER, bool BF16>
 cudaError_t launch(const RotaryArgs& a, cudaStream_t stream) {
-  const uint32_t rest = a.copy_rest ? (a.head_dim - a.rot_dim + 2 * V - 1) / (2 * V) : 0;
-  const uint32_t units = a.rot_dim / (2 * V) + rest;
-  const uint32_t groups = (a.heads + HPT - 1) / HPT;
-  const uint64_t work = static_cast<uint64_t>(a.tokens) * groups * units;
+  constexpr int kUnit = INTER ? V : 2 * V;   // elements a thread and head
+  const uint32_t rest = a.copy_rest ? (a.head_dim - a.rot_dim + kUnit - 1) / kUnit : 0;
+  const uint32_t units = a.rot_dim / kUnit + rest;
+  const uint32_t groups = (a.heads + HEADS - 1) / HEADS;
+  const uint32_t rows = units < kThreads ? kThreads / units : 1;   // a block
+  const uint64_t all = static_cast<uint64_t>(a.tokens) * groups;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((work + kThreads - 1) / kThreads));
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3(static_cast<unsigned>((all + rows - 1) / rows));
+  cfg.blockDim = dim3(units, rows);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, rotary_kernel<V, HPT, INTER, BF16>, a, units, groups);
+  return cudaLaunchKernelEx(&cfg, rotary_kernel<V, HEADS, INTER, BF16>, a, groups);
 }
 
-template <int V>
-cudaError_t launch_as(const RotaryArgs& a, bool interleaved, bool bf16, cudaStream_t s) {
-  if (interleaved) return bf16 ? launch<V, 2, true, true>(a, s) : launch<V, 2, true, false>(a, s);
-  return bf16 ? launch<V, 2, false, true>(a, s) : launch<V, 2, false, false>(a, s);
+template <int V, int HEADS, bool INTER>
+cudaError_t launch_typed(const RotaryArgs& a, bool bf16, cudaStream_t s) {
+  return bf16 ? launch<V, HEADS, INTER, true>(a, s) : launch<V, HEADS, INTER, false>(a, s);
+}
+
+template <int V, bool INTER>
+cudaError_t launch_as(const RotaryArgs& a, bool bf16, cudaStream_t s) {
+  // Few heads over all tokens: one a thread, since latency is all there is.  Many:
+  // four, which share their angles.  (us with one, two, four and eight, 72 heads of
+  // 128: 16 tokens 1.9, 2.2, 2.6 and 3.4, 333 tokens 4.1, 3.4, 3.6 and 3.8, 8192
+  // tokens 52, 45, 45 and 46; 40 heads of 64, half of each: 333 tokens 2.2, 2.3, 2.8
+  // and 3.9)
+  if (a.tokens * a.heads <= 16384) return launch_typed<V, 1, INTER>(a, bf16, s);
+  return launch_typed<V, 4, INTER>(a, bf16, s);
 }
 
 }  // namespace
 
 cudaError_t launch_rotary(const RotaryArgs& a, bool interleaved, bool bf16, cudaStream_t stream) {
-  // the widest vector that a pair's two elements allow (rows begin at 16-byte
-  // boundaries, and so does every vector that divides rot_dim / 2)
+  // the widest vector that the turned elements allow (rows begin at 16-byte
+  // boundaries, and so does every vector that divides rot_dim, or its half)
+  if (interleaved) {
+    if (a.rot_dim % 8 == 0) return launch_as<8, true>(a, bf16, stream);
+    if (a.rot_dim % 4 == 0) return launch_as<4, true>(a, bf16, stream);
+    return launch_as<2, true>(a, bf16, stream);
+  }
   const int half = a.rot_dim / 2;
-  if (half % 8 == 0) return launch_as<8>(a, interleaved, bf16, stream);
-  if (half % 4 == 0) return launch_as<4>(a, interleaved, bf16, stream);
-  if (half % 2 == 0) return launch_as<2>(a, interleaved, bf16, stream);
-  return launch_as<1>(a, interleaved, bf16, stream);
+  if (half % 8 == 0) return launch_as<8, false>(a, bf16, stream);
+  if (half % 4 == 0) return launch_as<4, false>(a, bf16, stream);
+  if (half % 2 == 0) return launch_as<2, false>(a, bf16, stream);
+  return launch_as<1, false>(a, bf16, stream);
 }
 
 }  // namespace petit

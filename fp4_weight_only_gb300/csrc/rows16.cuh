@@ -24,36 +24,82 @@ __device__ __forceinline__ uint32_t pack16(float x, float y) {
   return w;
 }
 
+// Two FP32 operations in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(r)
+      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
+  return reinterpret_cast<const float2&>(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(r)
+      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
+  return reinterpret_cast<const float2&>(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(r)
+      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)),
+        "l"(reinterpret_cast<const uint64_t&>(c)));
+  return reinterpret_cast<const float2&>(r);
+}
+
 template <bool BF16>
-__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ void unpack8(const uint4& v, float2 (&x)[4]) {
+  x[0] = unpack16<BF16>(v.x), x[1] = unpack16<BF16>(v.y), x[2] = unpack16<BF16>(v.z), x[3] = unpack16<BF16>(v.w);
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint4 pack8(const float2 (&x)[4]) {
+  return make_uint4(pack16<BF16>(x[0].x, x[0].y), pack16<BF16>(x[1].x, x[1].y), pack16<BF16>(x[2].x, x[2].y),
+                    pack16<BF16>(x[3].x, x[3].y));
+}
+
+// The scale max(top, 1e-8) / 448 of E4M3 codes and its reciprocal, both rounded
+// as a division's: a product with the divisor's reciprocal and a correction by
+// the remainder (Markstein's division).
+struct E4M3Scale {
+  float scale, inverse, remainder;   // remainder: -scale, or 0 where the scale is infinite
+};
+
+__device__ __forceinline__ E4M3Scale e4m3_scale(float top) {
+  constexpr float kInv448 = 1.0f / 448.0f;
+  const float m = fmaxf(top, 1e-8f);
+  E4M3Scale s;
+  s.scale = m * kInv448;
+  s.inverse = s.remainder = 0.0f;
+  if (m < INFINITY) {
+    s.scale = fmaf(fmaf(s.scale, -448.0f, m), kInv448, s.scale);
+    s.inverse = 1.0f / s.scale;
+    s.remainder = -s.scale;
+  }
+  return s;
+}
+
+// E4M3 codes of x / scale: nearest even, at most 448, NaN stays NaN.  The
+// quotient is the correctly rounded one, as above, so that codes are those of
+// the definition.
+__device__ __forceinline__ uint2 e4m3x8(const float2 (&x)[4], const E4M3Scale& s) {
+  const float2 inv = make_float2(s.inverse, s.inverse), back = make_float2(s.remainder, s.remainder);
+  float2 q[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 f = unpack16<BF16>(w[i]);
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
+    q[i] = mul2(x[i], inv);
+    q[i] = fma2(fma2(q[i], back, x[i]), inv, q[i]);
   }
-}
-
-template <bool BF16>
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  return make_uint4(pack16<BF16>(x[0], x[1]), pack16<BF16>(x[2], x[3]), pack16<BF16>(x[4], x[5]),
-                    pack16<BF16>(x[6], x[7]));
-}
-
-// E4M3 codes of x / scale: nearest even, at most 448, NaN stays NaN.
-__device__ __forceinline__ uint2 e4m3x8(const float (&x)[8], float scale) {
   uint32_t r[2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float* y = x + 4 * i;
+  for (int i = 0; i < 2; ++i)
     asm("{\n\t.reg .b16 lo, hi;\n\t"
         "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
         "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
         "mov.b32 %0, {lo, hi};\n\t}"
         : "=r"(r[i])
-        : "f"(y[0] / scale), "f"(y[1] / scale), "f"(y[2] / scale), "f"(y[3] / scale));
-  }
+        : "f"(q[2 * i].x), "f"(q[2 * i].y), "f"(q[2 * i + 1].x), "f"(q[2 * i + 1].y));
   return make_uint2(r[0], r[1]);
 }
 

@@ -484,7 +484,8 @@ typedef struct petit_rms_norm {
   float* scales;         /* (device) [rows][dim / group], or NULL: 16-bit output */
   int64_t rows;          /* 0..2^24; 0 enqueues nothing */
   int64_t dim;           /* a multiple of 8, at most 32768 */
-  int64_t x_stride;      /* elements between rows, multiples of 8 (scale_stride: any) */
+  int64_t x_stride;      /* elements between rows, multiples of 8 (scale_stride: any);
+                            with one row not looked at */
   int64_t residual_stride;
   int64_t sum_stride;
   int64_t out_stride;
@@ -508,7 +509,8 @@ petit_status_t petit_rms_norm(const petit_rms_norm_t* args, petit_stream_t strea
  * Frequencies are given in 2^-64 turns a position (petit_rotary_turns), so that
  * angles are exact modulo a turn at any position, negative ones too.
  * q_out and k_out are q and k themselves (in place) or rows that do not overlap
- * them.  Either may have no heads; its rows are then not looked at. */
+ * them.  Either may have no heads; its rows are then not looked at, nor is the
+ * token stride of one token, or the head stride of one head. */
 typedef struct petit_rotary {
   petit_rows_t q;         /* [num_tokens][num_q_heads][head_dim] */
   petit_rows_t k;         /* [num_tokens][num_k_heads][head_dim] */

@@ -41,7 +41,7 @@ def norm(**k):
     (dict(scales=C, group=128), SHAPE), (dict(scales=C, group=-16), SHAPE), (dict(scales=C + 2, group=16, scale_stride=4), ALIGN),
     (dict(scales=C, group=16, scale_stride=3), INVALID), (dict(scales=C, scale_stride=0), INVALID),
     (dict(sum=0x50000), INVALID),                                                        # two outputs in one place
-    (dict(sum=B, sum_stride=72), INVALID), (dict(out=A, out_stride=72), INVALID), (dict(out=A, scales=C), INVALID)])
+    (dict(rows=1, x_stride=3, out_stride=0, sum_stride=1, eps=NAN), INVALID), (dict(sum=B, sum_stride=72), INVALID), (dict(out=A, out_stride=72), INVALID), (dict(out=A, scales=C), INVALID)])
 def test_norm_refusals(lib, change, want):
     a = norm(**change)
     assert lib.petit_rms_norm(ctypes.addressof(a), None) == want
@@ -53,15 +53,15 @@ def test_norm_without_arguments(lib):
 
 
 def rotary(**k):
-    r = binding.Rows(A, 512, 64)
-    o = binding.Rows(B, 512, 64)
+    r, o = (A, 512, 64), (B, 512, 64)
     d = dict(q=r, k=r, q_out=o, k_out=o, turns=A, positions=A, num_tokens=3, num_q_heads=6, num_k_heads=2, head_dim=64,
              rot_dim=64, dtype=0, interleaved=0, positions_32=0, magnitude=1.0)
     d.update(k)
-    return binding.RotaryArgs(*d.values())
+    return binding.RotaryArgs(*(v for x in d.values() for v in (x if isinstance(x, tuple) else (x,))))
 
 
-R = binding.Rows
+def R(*rows):
+    return rows
 
 
 @pytest.mark.parametrize("change,want", [
@@ -75,7 +75,8 @@ R = binding.Rows
     (dict(positions=A + 2, positions_32=1), ALIGN), (dict(q=R(None, 512, 64)), INVALID), (dict(k_out=R(None, 512, 64)), INVALID),
     (dict(q=R(ODD, 512, 64)), ALIGN), (dict(k=R(A, 516, 64)), ALIGN), (dict(q_out=R(B, 512, 68)), ALIGN),
     (dict(q_out=R(B, 0, 64)), INVALID), (dict(k_out=R(B, 512, 0)), INVALID), (dict(k_out=R(B, 512, 56)), INVALID),
-    (dict(q_out=R(A, 1024, 64)), INVALID), (dict(q_out=R(A, 512, 72)), INVALID)])
+    (dict(q_out=R(A, 1024, 64)), INVALID), (dict(q_out=R(A, 512, 72)), INVALID),
+    (dict(num_tokens=1, num_q_heads=1, q=R(A, 3, 5), q_out=R(B, 1, 0), positions=None), INVALID)])   # (strides of one row)
 def test_rotary_refusals(lib, change, want):
     a = rotary(**change)
     assert lib.petit_rotary(ctypes.addressof(a), None) == want
