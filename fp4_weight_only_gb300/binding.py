@@ -137,6 +137,9 @@ SIGNATURES = {
     "petit_kv_attention": (ctypes.c_int, [_c_p, _c_p, _c_p, _c_sz, _c_p]),
     "petit_gated_gemm": (ctypes.c_int, [ctypes.c_int, _c_p, _c_p, ctypes.c_float, ctypes.c_float, ctypes.c_int, _c_p,
                                         _c_i64, _c_i64, _c_i64, _c_p, _c_sz, _c_p]),
+    "petit_gated_workspace_bytes": (_c_sz, [_c_i64, _c_i64, _c_i64, ctypes.c_int]),
+    "petit_plan_gated": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_i64, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                        ctypes.POINTER(PlanInfo), _c_p, _c_i64]),
     "petit_moe_gated_workspace_bytes": (_c_sz, [_c_p, _c_i64, _c_i64, _c_i64, ctypes.c_int]),
     "petit_moe_gated_gemm": (ctypes.c_int, [ctypes.c_int, _c_p, _c_p, _c_p, _c_p, _c_p, _c_i64, ctypes.c_int, _c_p,
                                             _c_i64, _c_i64, _c_p, _c_sz, _c_p]),
@@ -390,6 +393,7 @@ def set_tile_config(bn=0, ku=0):
     unit) for later calls in this process; (0, 0) restores the planner."""
     _check(load().petit_set_tile_config(int(bn), int(ku)), "set_tile_config")
     workspace_bytes.cache_clear()
+    gated_workspace_bytes.cache_clear()
 
 
 def set_pair_mode(mode=0):
@@ -398,6 +402,7 @@ def set_pair_mode(mode=0):
     apply."""
     _check(load().petit_set_pair_mode(int(mode)), "set_pair_mode")
     workspace_bytes.cache_clear()
+    gated_workspace_bytes.cache_clear()
 
 
 _MAX_RANGES = 1025   # kernel grids have at most 1024 work ranges
@@ -443,6 +448,19 @@ def moe_plan(expert_offsets, n, k, fmt="mxfp4", num_sms=None, pair_capacity=None
     starts = (ctypes.c_int64 * _MAX_RANGES)()
     _check(L.petit_plan_moe(off, E, int(n), int(k), FORMATS[fmt], num_sms, pair_capacity,
                             ctypes.byref(info), starts, _MAX_RANGES), "plan_moe")
+    return _plan_result(info, starts)
+
+
+def gated_plan(expert_offsets, n, k, fmt="nvfp4", num_sms=None, pair_capacity=None):
+    """:func:`plan` for the gated products: E + 1 row offsets, (0, m) for :func:`gated_gemm`."""
+    L = load()
+    num_sms, pair_capacity = _limits(num_sms, pair_capacity)
+    E = len(expert_offsets) - 1
+    off = (ctypes.c_int64 * (E + 1))(*[int(x) for x in expert_offsets])
+    info = PlanInfo()
+    starts = (ctypes.c_int64 * _MAX_RANGES)()
+    _check(L.petit_plan_gated(off, E, int(n), int(k), FORMATS[fmt], num_sms, pair_capacity,
+                              ctypes.byref(info), starts, _MAX_RANGES), "plan_gated")
     return _plan_result(info, starts)
 
 
@@ -651,6 +669,11 @@ def gated_repack(gate_packed, gate_scales, up_packed, up_scales, fmt="nvfp4"):
 
 
 @functools.lru_cache(maxsize=1024)
+def gated_workspace_bytes(m, n, k, fmt="nvfp4"):
+    return int(load().petit_gated_workspace_bytes(m, n, k, FORMATS[fmt]))
+
+
+@functools.lru_cache(maxsize=1024)
 def _repacked_bytes(n, k, fmt):
     return int(load().petit_repacked_bytes(n, k, FORMATS[fmt]))
 
@@ -683,7 +706,7 @@ def gated_gemm(A, rep, n, fmt="nvfp4", global_scales=(1.0, 1.0), act="silu", wor
     global_scales: (g, u), floats (MXFP4: ones); act: "silu", "gelu" or "gelu_tanh"."""
     m, k = A.shape
     number, C = _gated_args(A, rep, n, fmt, act, out, 1, m, k)
-    need = workspace_bytes(m, 2 * n, k, fmt)
+    need = gated_workspace_bytes(m, n, k, fmt)
     if need == 0:
         raise PetitError(2, "gated workspace size")
     buf = (workspace or Workspace(A.device)).ensure(need)

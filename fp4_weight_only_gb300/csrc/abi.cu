@@ -266,7 +266,7 @@ petit_status_t gated_common(int fmt, const void* A, const uint8_t* rep, const fl
   if (petit_status_t st = current_device(&sms, &dev, &pair_cap)) return st;
   const int64_t rows = off[groups];
   const petit::GemmPlan plan =
-      petit::plan_grouped(off, static_cast<int>(groups), 2 * n, k, fmt, sms, pair_cap, true);
+      petit::plan_gated(off, static_cast<int>(groups), 2 * n, k, fmt, sms, pair_cap);
   if (plan.units >= kMaxUnits) return PETIT_ERR_UNSUPPORTED_SHAPE;
   if (ws_bytes < plan.ws.total) return PETIT_ERR_WORKSPACE;
   CUtensorMap map;
@@ -386,18 +386,45 @@ petit_status_t petit_moe_gemm_bf16_nvfp4(const void* A, const uint8_t* rep,
                     workspace_bytes, stream);
 }
 
-size_t petit_moe_gated_workspace_bytes(const int64_t* expert_offsets, int64_t num_experts, int64_t n,
-                                       int64_t k, int fmt) {
-  if (check_offsets(expert_offsets, num_experts) != PETIT_OK || n > kMaxDim ||
-      check_tiled_shape(2 * n, k) != PETIT_OK)
-    return 0;
-  if (fmt != PETIT_FMT_NVFP4 && fmt != PETIT_FMT_MXFP4) return 0;
+// n * 2 weight rows for the gated products: 0 where they cannot be laid out
+static size_t gated_workspace(const int64_t* off, int64_t groups, int64_t n, int64_t k, int fmt) {
+  if (n > kMaxDim || check_tiled_shape(2 * n, k) != PETIT_OK) return 0;
   int sms = 0;
   int pair_cap = 0;
   if (current_device(&sms, nullptr, &pair_cap) != PETIT_OK) return 0;
-  return petit::plan_grouped(expert_offsets, static_cast<int>(num_experts), 2 * n, k, fmt, sms,
-                             pair_cap, true)
-      .ws.total;
+  return petit::plan_gated(off, static_cast<int>(groups), 2 * n, k, fmt, sms, pair_cap).ws.total;
+}
+
+size_t petit_gated_workspace_bytes(int64_t m, int64_t n, int64_t k, int fmt) {
+  if (fmt != PETIT_FMT_NVFP4 && fmt != PETIT_FMT_MXFP4 && fmt != PETIT_FMT_NVFP4_F16) return 0;
+  if (m < 1 || m > kMaxDim) return 0;
+  const int64_t off[2] = {0, m};
+  return gated_workspace(off, 1, n, k, fmt);
+}
+
+size_t petit_moe_gated_workspace_bytes(const int64_t* expert_offsets, int64_t num_experts, int64_t n,
+                                       int64_t k, int fmt) {
+  if (fmt != PETIT_FMT_NVFP4 && fmt != PETIT_FMT_MXFP4) return 0;
+  if (check_offsets(expert_offsets, num_experts) != PETIT_OK || expert_offsets[num_experts] == 0) return 0;
+  return gated_workspace(expert_offsets, num_experts, n, k, fmt);
+}
+
+petit_status_t petit_plan_gated(const int64_t* expert_offsets, int64_t num_experts, int64_t n, int64_t k,
+                                int fmt, int num_sms, int pair_capacity, petit_plan_info_t* info,
+                                int64_t* range_starts, int64_t max_ranges) {
+  if (petit_status_t st = check_plan_args(num_sms, pair_capacity, info)) return st;
+  if (fmt != PETIT_FMT_NVFP4 && fmt != PETIT_FMT_MXFP4 && fmt != PETIT_FMT_NVFP4_F16)
+    return PETIT_ERR_INVALID_ARG;
+  if (petit_status_t st = check_offsets(expert_offsets, num_experts)) return st;
+  if (n > kMaxDim) return PETIT_ERR_UNSUPPORTED_SHAPE;
+  if (petit_status_t st = check_tiled_shape(2 * n, k)) return st;
+  if (expert_offsets[num_experts] == 0) {   // nothing is launched
+    std::memset(info, 0, sizeof(*info));
+    return PETIT_OK;
+  }
+  return describe_plan(petit::plan_gated(expert_offsets, static_cast<int>(num_experts), 2 * n, k, fmt,
+                                         num_sms, pair_capacity),
+                       info, range_starts, max_ranges);
 }
 
 petit_status_t petit_gated_gemm(int fmt, const void* A, const uint8_t* rep, float gate_scale,

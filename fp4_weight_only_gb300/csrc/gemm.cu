@@ -1793,11 +1793,41 @@ bool set_tile_override(int bn, int ku) {
   return true;
 }
 
+namespace {
+
+// A plan's tiles, with its tile shape chosen; returns how many.
+int64_t lay_tiles(GemmPlan& pl, const int64_t* row_off, int num_groups, int64_t n, int64_t k) {
+  pl.num_groups = num_groups;
+  // work tiles: 128 weight rows, or 256 (a tile pair) with CTA pairs
+  pl.n_tiles = static_cast<int>(n / (kTileN * (pl.pair ? 2 : 1)));
+  pl.k_stages = static_cast<int>(k / kStageK);
+  int64_t tiles = 0;
+  for (int g = 0; g <= num_groups; ++g) {
+    pl.row_off[g] = static_cast<int32_t>(row_off[g]);
+    pl.tile_base[g] = static_cast<int32_t>(tiles);
+    if (g == num_groups) break;
+    const int64_t mt = (row_off[g + 1] - row_off[g] + pl.bn - 1) / pl.bn;
+    if (mt > 1) pl.weights_reused = true;
+    tiles += mt * pl.n_tiles;
+  }
+  pl.units = tiles * (pl.k_stages / pl.ku);
+  return tiles;
+}
+
+void lay_workspace(GemmPlan& pl) {
+  pl.ws.counters_off = kWsHeaderBytes;
+  pl.ws.partials_off = align_up(kWsHeaderBytes + kWsCountersBytes, 256);
+  // two partial slots per CTA (a work range has two CTAs with CTA pairs)
+  pl.ws.total = pl.ws.partials_off + sizeof(float) * 2ull * static_cast<size_t>(pl.num_ctas) *
+                                         (pl.pair ? 2 : 1) * pl.bn * kTileN;
+}
+
+}  // namespace
+
 GemmPlan plan_grouped(const int64_t* row_off, int num_groups, int64_t n, int64_t k, int fmt,
-                      int num_sms, int pair_cap, bool gated) {
+                      int num_sms, int pair_cap) {
   GemmPlan pl{};
   pl.fmt = fmt;
-  pl.num_groups = num_groups;
   int64_t max_rows = 0;
   for (int g = 0; g < num_groups; ++g) {
     const int64_t r = row_off[g + 1] - row_off[g];
@@ -1814,11 +1844,7 @@ GemmPlan plan_grouped(const int64_t* row_off, int num_groups, int64_t n, int64_t
     for (int bn = 16; bn <= 256; bn *= 2) {
       int64_t tiles = 0;
       for (int g = 0; g < num_groups; ++g) tiles += (row_off[g + 1] - row_off[g] + bn - 1) / bn;
-      // (gated, in sixths of a 64-row tile's pass, as measured with 8 experts of
-      // 28672 x 4096 in MXFP4 and 512 rows, [39, 27, 94, 30, 25, 188, 39, 70] and
-      // others: 12.4, 14.8, 15, 24.4 and 37.6 us a pass; 167 us, 220 with 128-row tiles)
-      const int64_t cost = gated ? tiles * (bn == 16 ? 5 : bn <= 64 ? 6 : bn == 128 ? 10 : 15)
-                                 : tiles * (bn > 128 ? bn / 128 : 1);
+      const int64_t cost = tiles * (bn > 128 ? bn / 128 : 1);
       if (best < 0 || cost < best) {
         best = cost;
         pl.bn = bn;
@@ -1854,19 +1880,7 @@ GemmPlan plan_grouped(const int64_t* row_off, int num_groups, int64_t n, int64_t
                                ((m + pl.bn - 1) / pl.bn);
     pl.pair = pair_mode == 2 || pl.bn == 256 || pair_units >= 100 * static_cast<int64_t>(pair_cap);
   }
-  // work tiles: 128 weight rows, or 256 (a tile pair) with CTA pairs
-  pl.n_tiles = static_cast<int>(n / (kTileN * (pl.pair ? 2 : 1)));
-  pl.k_stages = static_cast<int>(k / kStageK);
-  int64_t tiles = 0;
-  for (int g = 0; g <= num_groups; ++g) {
-    pl.row_off[g] = static_cast<int32_t>(row_off[g]);
-    pl.tile_base[g] = static_cast<int32_t>(tiles);
-    if (g == num_groups) break;
-    const int64_t mt = (row_off[g + 1] - row_off[g] + pl.bn - 1) / pl.bn;
-    if (mt > 1) pl.weights_reused = true;
-    tiles += mt * pl.n_tiles;
-  }
-  pl.units = tiles * (pl.k_stages / pl.ku);
+  const int64_t tiles = lay_tiles(pl, row_off, num_groups, n, k);
   // work ranges: one per SM, or one per resident CTA pair
   const int64_t ranges = pl.pair ? pair_cap : num_sms;
   pl.num_ctas = static_cast<int>(pl.units < ranges ? pl.units : ranges);
@@ -1897,11 +1911,90 @@ GemmPlan plan_grouped(const int64_t* row_off, int num_groups, int64_t n, int64_t
     }
   }
   if (pl.units < (int64_t(1) << 31)) plan_bounds(pl, late_start_ns());
-  pl.ws.counters_off = kWsHeaderBytes;
-  pl.ws.partials_off = align_up(kWsHeaderBytes + kWsCountersBytes, 256);
-  // two partial slots per CTA (a work range has two CTAs with CTA pairs)
-  pl.ws.total = pl.ws.partials_off + sizeof(float) * 2ull * static_cast<size_t>(pl.num_ctas) *
-                                         (pl.pair ? 2 : 1) * pl.bn * kTileN;
+  lay_workspace(pl);
+  return pl;
+}
+
+namespace {
+
+// What a launch of the gated kernel costs, in us: a start, a pace for each 128-k
+// chunk of the longest range, a tile's being split and each of its contributors,
+// and each of a range's pieces of tiles (its epilogue; with 128 rows and more the
+// tensor core waits for it).  Fitted to 6900 launches on a GB300 (NVFP4, 1024 to
+// 57344 x 512 to 8192, 16 to 4096 rows, every tile shape): 90 % of them within
+// 18 %, and the shape with the least is within 2 % of the fastest on the average.
+// plan_grouped's rules, made for large matrices, took 1.22 times as long, and with
+// whole tiles for ranges 1.37 times (4096 x 512, 300 rows: 21.4 us with its
+// 256-row tiles, 6.4 with 128 rows, 5.2 with whole tiles of 64).
+struct TileCost {
+  int bn;
+  bool pair;
+  double start, chunk, split, part, piece;
+};
+constexpr TileCost kGatedCosts[] = {
+    {16, false, 3.4, 0.230, 2.0, 0.14, 0.49},  {32, false, 3.0, 0.237, 0.1, 0.62, 1.54},
+    {64, false, 3.5, 0.244, 1.1, 0.83, 0.77},  {128, false, 2.6, 0.413, 0.9, 1.34, 2.04},
+    {128, true, 3.7, 0.392, 1.3, 1.40, 1.13},  {256, false, 2.8, 0.583, 0.0, 2.59, 3.87},
+    {256, true, 2.8, 0.556, 0.0, 2.74, 3.65},
+};
+
+}  // namespace
+
+GemmPlan plan_gated(const int64_t* row_off, int num_groups, int64_t n, int64_t k, int fmt, int num_sms,
+                    int pair_cap) {
+  const int pair_mode = g_pair_mode.load(std::memory_order_relaxed);
+  const int ov = tile_override();   // a forced tile shape, as in plan_grouped
+  const bool pair_ok = pair_cap > 0 && num_groups == 1 && n % (2 * kTileN) == 0 && pair_mode != 1;
+  const int64_t chunks = k / kStageK;
+  GemmPlan best{};
+  double best_us = 0.0;
+  for (const TileCost& c : kGatedCosts) {
+    if (ov != 0 && (ov & 0xFFFF) != c.bn) continue;
+    if (c.pair ? !pair_ok : (pair_ok && pair_mode == 2 && c.bn >= 128)) continue;
+    const int ku = c.bn <= 64 && chunks % 2 == 0 && (ov == 0 || (ov >> 16) == 2) ? 2 : 1;
+    int64_t tiles = 0;
+    for (int g = 0; g < num_groups; ++g) tiles += (row_off[g + 1] - row_off[g] + c.bn - 1) / c.bn;
+    tiles *= n / (kTileN * (c.pair ? 2 : 1));
+    const int64_t per_tile = chunks / ku, units = tiles * per_tile;
+    const int64_t ranges = c.pair ? pair_cap : num_sms;
+    auto consider = [&](int64_t P, bool whole) {
+      const int64_t L = (units + P - 1) / P;
+      const bool split = !(whole && L % per_tile == 0);
+      const double parts = !split ? 0.0 : whole ? static_cast<double>(per_tile / L)
+                                                : static_cast<double>(std::min(P, (per_tile + L - 1) / L + 1));
+      const double pieces = whole ? static_cast<double>(std::max<int64_t>(1, L / per_tile))
+                                  : static_cast<double>((L + per_tile - 1) / per_tile + 1);
+      const double us = c.start + c.chunk * static_cast<double>(L * ku) + (split ? c.split : 0.0) +
+                        c.part * parts + c.piece * pieces;
+      if (best.num_ctas != 0 && us >= best_us) return;
+      best_us = us;
+      best.bn = c.bn;
+      best.ku = ku;
+      best.pair = c.pair;
+      best.num_ctas = static_cast<int>(P);
+      best.use_bounds = !whole;
+    };
+    // every SM, with ranges that cross tiles; or whole tiles, or equal parts of them
+    const int64_t most = std::min<int64_t>(ranges, kMaxCtas / (c.pair ? 2 : 1));
+    consider(std::min(units, most), units % std::min(units, most) == 0 &&
+                                        ((units / std::min(units, most)) % per_tile == 0 ||
+                                         per_tile % (units / std::min(units, most)) == 0) &&
+                                        c.bn > 64);
+    for (int64_t parts = 1; parts <= 8 && tiles * parts <= most; ++parts)
+      if (per_tile % parts == 0) consider(tiles * parts, true);
+    const int64_t least = (tiles + most - 1) / most;   // whole tiles a range, at least
+    for (int64_t each = std::max<int64_t>(least, 2); each <= 2 * least; ++each)
+      if (tiles % each == 0) consider(tiles / each, true);
+  }
+  GemmPlan pl{};
+  pl.fmt = fmt;
+  pl.bn = best.bn;
+  pl.ku = best.ku;
+  pl.pair = best.pair;
+  lay_tiles(pl, row_off, num_groups, n, k);
+  pl.num_ctas = best.num_ctas;
+  if (best.use_bounds && pl.units < (int64_t(1) << 31)) plan_bounds(pl, late_start_ns());
+  lay_workspace(pl);
   return pl;
 }
 

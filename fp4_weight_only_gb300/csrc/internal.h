@@ -78,10 +78,12 @@ void check_limits(int64_t* weight_bytes, int64_t* c_elems);
 // Checks that the current device can run this library's kernels and gives its
 // SM count and index; returns a petit_status_t.
 int usable_device(int* sms, int* dev = nullptr);
-// row_off: num_groups + 1 non-decreasing offsets starting at 0; gated: for
-// launch_gated
+// row_off: num_groups + 1 non-decreasing offsets starting at 0
 GemmPlan plan_grouped(const int64_t* row_off, int num_groups, int64_t n, int64_t k, int fmt,
-                      int num_sms, int pair_cap, bool gated = false);
+                      int num_sms, int pair_cap);
+// The same for launch_gated (n: the weight rows of both matrices; some rows).
+GemmPlan plan_gated(const int64_t* row_off, int num_groups, int64_t n, int64_t k, int fmt,
+                    int num_sms, int pair_cap);
 // Resident CTA pairs of the pair kernels on the current device (0 if none).
 int pair_capacity();
 // 0: CTA pairs where the planner expects them to pay, 1: never, 2: wherever

@@ -438,12 +438,13 @@ petit_status_t petit_kv_attention(const petit_kv_cache_t* cache, const petit_kv_
  * n counts C's columns: n % 64 == 0, k % 128 == 0.  fmt: the repacked format;
  * PETIT_FMT_NVFP4_F16 takes and gives FP16, the others BF16.  The two scales are
  * NVFP4's global scales (MXFP4: 1).  workspace: at least
- * petit_gemm_workspace_bytes(m, 2 n, k, fmt) bytes, used and kept as a GEMM's.
+ * petit_gated_workspace_bytes(...) bytes, used and kept as a GEMM's.
  *     silu x / (1 + e^-x),  gelu x Phi(x),  gelu_tanh x / (1 + e^(-2 z)),
  *     z = sqrt(2 / pi) (x + 0.044715 x^3)
  * Errors and everything else as petit_gemm_bf16_nvfp4. */
 typedef enum petit_act { PETIT_ACT_SILU = 0, PETIT_ACT_GELU = 1, PETIT_ACT_GELU_TANH = 2 } petit_act_t;
 
+size_t petit_gated_workspace_bytes(int64_t m, int64_t n, int64_t k, int fmt);
 petit_status_t petit_gated_gemm(int fmt, const void* A, const uint8_t* rep, float gate_scale,
                                 float up_scale, int act, void* C, int64_t m, int64_t n, int64_t k,
                                 void* workspace, size_t workspace_bytes, petit_stream_t stream);
@@ -459,6 +460,15 @@ petit_status_t petit_moe_gated_gemm(int fmt, const void* A, const uint8_t* rep, 
                                     const float* up_scales, const int64_t* expert_offsets,
                                     int64_t num_experts, int act, void* C, int64_t n, int64_t k,
                                     void* workspace, size_t workspace_bytes, petit_stream_t stream);
+
+/* The plan of a gated product, as petit_plan_gemm and petit_plan_moe give them
+ * for the others: offsets {0, m} and one expert for petit_gated_gemm.  Tiles are
+ * of both matrices' rows (128 of them, or 256 with CTA pairs, hold 64 or 128
+ * columns of C). */
+struct petit_plan_info;
+petit_status_t petit_plan_gated(const int64_t* expert_offsets, int64_t num_experts, int64_t n, int64_t k,
+                                int fmt, int num_sms, int pair_capacity, struct petit_plan_info* info,
+                                int64_t* range_starts, int64_t max_ranges);
 
 /* ------------------------------------- around a decoder layer's products */
 
