@@ -59,9 +59,10 @@ __device__ __forceinline__ uint4 pack8(const float2 (&x)[4]) {
                     pack16<BF16>(x[3].x, x[3].y));
 }
 
-// The scale max(top, 1e-8) / 448 of E4M3 codes and its reciprocal, both rounded
-// as a division's: a product with the divisor's reciprocal and a correction by
-// the remainder (Markstein's division).
+// The scale max(top, 1e-8) / 448 of E4M3 codes and its reciprocal, without the
+// general division: a product with the divisor's reciprocal and a correction by
+// the remainder (Markstein's division, which rounds as the division does), and the
+// hardware's reciprocal after one of Newton's steps.
 struct E4M3Scale {
   float scale, inverse, remainder;   // remainder: -scale, or 0 where the scale is infinite
 };
@@ -69,14 +70,14 @@ struct E4M3Scale {
 __device__ __forceinline__ E4M3Scale e4m3_scale(float top) {
   constexpr float kInv448 = 1.0f / 448.0f;
   const float m = fmaxf(top, 1e-8f);
+  const bool finite = m < INFINITY;
   E4M3Scale s;
   s.scale = m * kInv448;
-  s.inverse = s.remainder = 0.0f;
-  if (m < INFINITY) {
-    s.scale = fmaf(fmaf(s.scale, -448.0f, m), kInv448, s.scale);
-    s.inverse = 1.0f / s.scale;
-    s.remainder = -s.scale;
-  }
+  s.scale = finite ? fmaf(fmaf(s.scale, -448.0f, m), kInv448, s.scale) : m;
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(s.scale));
+  s.inverse = finite ? fmaf(fmaf(-s.scale, r, 1.0f), r, r) : 0.0f;
+  s.remainder = finite ? -s.scale : 0.0f;
   return s;
 }
 
