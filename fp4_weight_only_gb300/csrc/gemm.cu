@@ -380,7 +380,8 @@ __device__ __forceinline__ uint16_t out_bits(float x) {
 // of 128- and 256-row tiles delays the next tile's MMAs, so that its instructions
 // count: 1024 rows through 57344 x 8192 took 592 us with divisions, a shuffle for
 // each output and stores through a barrier of four warps, 500 so, and 637 and 620
-// where gelu was the CUDA library's erfc.)
+// where gelu was the CUDA library's erfc.  So does its code: 32 rows at a time,
+// with twice the loads in flight, took 549.)
 [[maybe_unused]] __device__ __forceinline__ float rcp_approx(float x) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -1947,9 +1948,9 @@ namespace {
 // What a launch of the gated kernel costs, in us: a start, a pace for each 128-k
 // chunk of the longest range, a tile's being split and each of its contributors,
 // and each of a range's pieces of tiles (its epilogue; with 128 rows and more the
-// tensor core waits for it).  Fitted to 6900 launches on a GB300 (NVFP4, 1024 to
+// tensor core waits for it).  Fitted to 7100 launches on a GB300 (NVFP4, 1024 to
 // 57344 x 512 to 8192, 16 to 4096 rows, every tile shape): 90 % of them within
-// 18 %, and the shape with the least is within 2 % of the fastest on the average.
+// 20 %, and the shape with the least is within 1 % of the fastest on the average.
 // plan_grouped's rules, made for large matrices, took 1.22 times as long, and with
 // whole tiles for ranges 1.37 times (4096 x 512, 300 rows: 21.4 us with its
 // 256-row tiles, 6.4 with 128 rows, 5.2 with whole tiles of 64).
@@ -1960,9 +1961,9 @@ struct TileCost {
 };
 constexpr TileCost kGatedCosts[] = {
     {16, false, 3.4, 0.230, 2.0, 0.14, 0.49},  {32, false, 3.0, 0.237, 0.1, 0.62, 1.54},
-    {64, false, 3.5, 0.244, 1.1, 0.83, 0.77},  {128, false, 2.6, 0.413, 0.9, 1.34, 2.04},
-    {128, true, 3.7, 0.392, 1.3, 1.40, 1.13},  {256, false, 2.8, 0.583, 0.0, 2.59, 3.87},
-    {256, true, 2.8, 0.556, 0.0, 2.74, 3.65},
+    {64, false, 3.2, 0.250, 1.7, 0.47, 0.83},  {128, false, 1.6, 0.408, 0.0, 1.32, 2.49},
+    {128, true, 3.4, 0.400, 0.4, 1.31, 1.19},  {256, false, 1.2, 0.563, 0.1, 2.33, 4.74},
+    {256, true, 2.4, 0.546, 0.3, 2.29, 4.10},
 };
 
 }  // namespace
