@@ -270,8 +270,7 @@ petit_status_t gated_common(int fmt, const void* A, const uint8_t* rep, const fl
   if (plan.units >= kMaxUnits) return PETIT_ERR_UNSUPPORTED_SHAPE;
   if (ws_bytes < plan.ws.total) return PETIT_ERR_WORKSPACE;
   CUtensorMap map;
-  if (petit_status_t st = cached_a_map(&map, A, rows, k, plan.pair ? plan.bn / 2 : plan.bn, plan.ku,
-                                       fmt == kNVFP4F16, dev))
+  if (petit_status_t st = cached_a_map(&map, A, rows, k, plan.a_rows, plan.ku, fmt == kNVFP4F16, dev))
     return st;
   petit::GemmArgs args{A, rep, C, rows, 2 * n, k, gate[0], static_cast<uint8_t*>(ws), kGemmTimeoutNs};
   args.device = dev;

@@ -128,10 +128,21 @@ struct Params {
 
 // What the gated epilogue needs beside it: group_alpha is the gate's factor,
 // group_up the other matrix's.
+// Its tiles have a height of their own, the group's rows in equal parts, so that
+// MMAs, activation copies and epilogues take no more rows than there are.
 struct GatedParams : Params {
   float group_up[kMaxGroups];
-  int32_t act;   // kActSilu, ...
+  int32_t act;      // kActSilu, ...
+  int32_t a_rows;   // rows of an activation copy: the largest height, or half of it in pairs
+  int32_t height[kMaxGroups + 1];   // activation rows a tile (the last: past the last group)
 };
+
+// Rows of the tiles of group g.
+template <int BN, typename P>
+__device__ __forceinline__ int32_t tile_height(const P& p, int g) {
+  if constexpr (std::is_same_v<P, GatedParams>) return p.height[g];
+  else return BN;
+}
 
 // Split tiles.  A contributor stores its FP32 partial and then arrives on
 // the tile's counter (acq_rel); the last to arrive adds all partials in CTA
@@ -153,6 +164,7 @@ struct FixJob {
   float alpha, alpha_up;                // (gated: the gate's and the up matrix's)
   int32_t d;                            // accumulator buffer of the segment
   uint32_t has;                         // bit t: issuer t's accumulator contributes
+  int32_t height;                       // activation rows of the tile
   int32_t valid;
 };
 
@@ -295,7 +307,8 @@ struct Cfg {
   // epilogue overlaps the next tile's MMAs (measured on GB300: gate_up at
   // m = 64 12 % faster than with two issuers and one accumulator each); at
   // N = 128 two issuers stay faster.
-  static constexpr int kMmaThreads = PAIR ? 1 : BN <= 32 ? 3 : BN == 128 ? 2 : 1;
+  // (Two chunks a unit at N = 128, gated only, leave room for one accumulator.)
+  static constexpr int kMmaThreads = PAIR ? 1 : BN <= 32 ? 3 : BN == 128 && KU == 1 ? 2 : 1;
   // dequantiser groups (four warps each) taking units round-robin
   static constexpr int kDeqGroups = 2;
   static constexpr int kMmaWarpX = kDeqWarp0 + kDeqGroupWarps * kDeqGroups - 1;  // issuer t>=1: +t
@@ -344,7 +357,8 @@ struct Cfg {
   static constexpr uint32_t kIdesc =
       FMT == kNVFP4F16 ? idesc_f16_f32(kM, BN) : idesc_bf16_f32(kM, BN);
   static_assert(BN % 16 == 0 && BN >= 16 && BN <= 256, "MMA N");
-  static_assert(!PAIR || (BN >= 128 && KU == 1), "CTA pairs: 128- or 256-row tiles, 128-k units");
+  static_assert(!PAIR || (BN >= 128 && (KU == 1 || (GATED && BN == 128))),
+                "CTA pairs: 128- or 256-row tiles, 128-k units (gated: two chunks with 128 rows)");
   static_assert(kNumA >= 2, "tensor memory");
   static_assert(kDColBase + kMmaThreads * kNumD * BN <= static_cast<int>(kTmemCols),
                 "tensor memory");
@@ -535,6 +549,10 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
   const int32_t wmul = PAIR ? 2 : 1;   // weight tile of work tile nt: nt * wmul + rank
   // columns of C: one a weight row, or one for each pair of them
   const int32_t c_cols = GATED ? p.n / 2 : p.n;
+  // bytes of an activation stage's 64-k slabs, and of all of them
+  uint32_t a_half_bytes = C::kAHalfBytes;
+  if constexpr (GATED) a_half_bytes = static_cast<uint32_t>(p.a_rows) * 128;
+  const uint32_t a_bytes = 2 * KU * a_half_bytes;
   const int64_t u0 = cta_lo(p, static_cast<int32_t>(cta));
   const int64_t u1 = cta_lo(p, static_cast<int32_t>(cta) + 1);
   const int64_t KS = p.k_units;
@@ -688,8 +706,13 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
       TileCursor xc = cursor_at<BN>(p, tile0);
       // first activation row of this CTA's part of the tile (CTA pairs: the
       // odd CTA holds the second half)
-      const int32_t xhalf = PAIR ? static_cast<int32_t>(rank) * C::kARows : 0;
-      int32_t xrow = xc.row0 + xc.mt * BN + xhalf, xk = x_ku * 2 * KU;
+      int32_t xhalf = 0, xrow = 0, xk = x_ku * 2 * KU;
+      auto tile_rows = [&]() {
+        const int32_t h = tile_height<BN>(p, xc.g);
+        xhalf = PAIR ? static_cast<int32_t>(rank) * (h / 2) : 0;
+        xrow = xc.row0 + xc.mt * h + xhalf;
+      };
+      tile_rows();
       const uint32_t xdst0 = smem_u32(sm_a);
       const uint32_t wfree0 = smem_u32(&wfree[0]);
       const uint32_t mdone0 = smem_u32(&mdone[0]), xfull0 = smem_u32(&xfull[0]);
@@ -720,7 +743,7 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
             ++xi;
             break;
           }
-          mbar_arrive_expect_tx(xfull0 + xbar, C::kABytes);
+          mbar_arrive_expect_tx(xfull0 + xbar, a_bytes);
           tma_load_3d(xdst, &tmap_a, 0, xrow, xk, xfull0 + xbar);
           ++xi;
           xk += 2 * KU;
@@ -735,7 +758,7 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
             x_ku = 0;
             xk = 0;
             cursor_next<BN>(p, xc);
-            xrow = xc.row0 + xc.mt * BN + xhalf;
+            tile_rows();
           }
           progress = true;
         }
@@ -804,7 +827,14 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
       int st = t, b = t;   // t < kMmaThreads <= kNumA <= kXStages
       uint32_t ph = 0, pb = 0;
       bool ok = true;
+      [[maybe_unused]] TileCursor ic{};
+      if constexpr (GATED) ic = cursor_at<BN>(p, tile0_32);
       for (int32_t s0 = 0; s0 < nu && ok;) {
+        uint32_t idesc = C::kIdesc;
+        if constexpr (GATED) {   // N: the tile's rows
+          idesc = (C::kIdesc & ~idesc_n(BN)) | idesc_n(tile_height<BN>(p, ic.g));
+          cursor_next<BN>(p, ic);
+        }
         const int32_t s1 = min(nu, s0 + (ks - (ku0 + s0) % ks));   // next tile boundary
         const int d = seg % C::kNumD;
         // Every issuer waits here, owning a unit of the segment or not: its
@@ -831,13 +861,13 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
 #pragma unroll
             for (int j = 0; j < KU * (kStageK / 16); ++j) {
               // K16 step j: slab j / 4 of A, 32-byte offset inside its swizzled rows
-              const uint64_t bdesc = smem_desc_kmajor_sw128(a_smem + (j >> 2) * C::kAHalfBytes) +
+              const uint64_t bdesc = smem_desc_kmajor_sw128(a_smem + (j >> 2) * a_half_bytes) +
                                      (((j & 3) * 32) >> 4);
               if constexpr (PAIR)
-                mma_ts_f16_pair(d_tmem, a_tmem + j * 8, bdesc, C::kIdesc,
+                mma_ts_f16_pair(d_tmem, a_tmem + j * 8, bdesc, idesc,
                                 (!seg_started && j == 0) ? 0u : 1u);
               else
-                mma_ts_f16(d_tmem, a_tmem + j * 8, bdesc, C::kIdesc,
+                mma_ts_f16(d_tmem, a_tmem + j * 8, bdesc, idesc,
                            (!seg_started && j == 0) ? 0u : 1u);
             }
             if constexpr (PAIR) {
@@ -974,7 +1004,10 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
       const int64_t seg_end = (tile + 1) * KS < u1 ? (tile + 1) * KS : u1;
       const bool full_tile = (u == tile * KS) && (seg_end == (tile + 1) * KS);
       const int64_t nt = ec.nt, mt = ec.mt;
-      const int64_t g_rows = p.row_off[ec.g + 1] - p.row_off[ec.g];  // this group's activation rows
+      const int32_t height = tile_height<BN>(p, ec.g);
+      // this group's activation rows (gated: up to the tile's end)
+      int64_t g_rows = p.row_off[ec.g + 1] - p.row_off[ec.g];
+      if constexpr (GATED) g_rows = min(g_rows, (mt + 1) * height);
       uint16_t* const c_g = p.c + static_cast<int64_t>(p.row_off[ec.g]) * c_cols;
       const float alpha = p.alpha_dev ? alpha_dev : p.group_alpha[ec.g];
       float alpha_up = alpha;
@@ -1027,13 +1060,14 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
             fix->c_first = c_first;
             fix->c_last = c_last;
             fix->first_slot = first_slot;
-            fix->row0 = static_cast<int64_t>(mt) * BN;
+            fix->row0 = static_cast<int64_t>(mt) * height;
             fix->col0 = (static_cast<int64_t>(nt) * wmul + rank) * kTileN;
             fix->g_rows = g_rows;
             fix->alpha = alpha;
             fix->alpha_up = alpha_up;
             fix->d = d;
             fix->has = has;
+            fix->height = height;
             fix->valid = 1;
           }
           u = seg_end;
@@ -1050,13 +1084,14 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
             fix->c_g = c_g;
             fix->c_first = fix->c_last = cta;
             fix->first_slot = 2 * sid(cta);
-            fix->row0 = static_cast<int64_t>(mt) * BN;
+            fix->row0 = static_cast<int64_t>(mt) * height;
             fix->col0 = (static_cast<int64_t>(nt) * wmul + rank) * kTileN;
             fix->g_rows = g_rows;
             fix->alpha = alpha;
             fix->alpha_up = alpha_up;
             fix->d = d;
             fix->has = has;
+            fix->height = height;
             fix->valid = 1;
           }
           u = seg_end;
@@ -1073,7 +1108,7 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
       if (!full_tile && !PETIT_CHECK(slot >= 0 && slot < 2 * NS)) break;
       bool c_ok = true;
 #pragma unroll 1
-      for (int c0 = 0; c0 < BN; c0 += 16) {
+      for (int c0 = 0; c0 < height; c0 += 16) {
         // the contributing accumulators, added in issuer order
         uint32_t v[16];
         bool have = false;
@@ -1093,7 +1128,7 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
           float fv[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) fv[j] = __uint_as_float(v[j]);
-          put_gated(fv, alpha, alpha_up, stage_c + q * 256, c_g, static_cast<int64_t>(mt) * BN + c0, ccol, g_rows);
+          put_gated(fv, alpha, alpha_up, stage_c + q * 256, c_g, static_cast<int64_t>(mt) * height + c0, ccol, g_rows);
         } else if (full_tile && C::kStageC > 0) {
           float fv[16];
 #pragma unroll
@@ -1145,13 +1180,14 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
             fix->c_first = c_first;
             fix->c_last = c_last;
             fix->first_slot = first_slot;
-            fix->row0 = static_cast<int64_t>(mt) * BN;
+            fix->row0 = static_cast<int64_t>(mt) * height;
             fix->col0 = (static_cast<int64_t>(nt) * wmul + rank) * kTileN;
             fix->g_rows = g_rows;
             fix->alpha = alpha;
             fix->alpha_up = alpha_up;
             fix->d = d;
             fix->has = has;
+            fix->height = height;
             fix->valid = 1;
           }
         } else if (*epi_flag) {
@@ -1159,7 +1195,7 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
           // loads are batched (kFixBatch contributors x 16 columns in flight),
           // so the reduction costs a few L2 round trips, not one per value
 #pragma unroll 1
-          for (int c0 = 0; c0 < BN; c0 += 16) {
+          for (int c0 = 0; c0 < height; c0 += 16) {
             float acc[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) acc[j] = 0.0f;
@@ -1189,7 +1225,7 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
             // (stored directly: here the partial loads set the pace, and
             // staging, with its barriers between the warps, was slower)
             if constexpr (GATED) {
-              put_gated(acc, alpha, alpha_up, stage_c + q * 256, c_g, static_cast<int64_t>(mt) * BN + c0, ccol, g_rows);
+              put_gated(acc, alpha, alpha_up, stage_c + q * 256, c_g, static_cast<int64_t>(mt) * height + c0, ccol, g_rows);
             } else {
 #pragma unroll
               for (int j = 0; j < 16; ++j) {
@@ -1470,7 +1506,7 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
         const uint32_t tbase = tmem + (static_cast<uint32_t>(32 * q) << 16) + C::kDColBase +
                                f.d * BN + row_base;
   #pragma unroll 1
-        for (int c0 = 0; c0 < (kStrided ? BN - row_base : kCols); c0 += kStep) {
+        for (int c0 = 0; c0 < (kStrided ? f.height - row_base : kCols); c0 += kStep) {
           float own[kLd];
   #pragma unroll
           for (int j = 0; j < kLd; ++j) own[j] = 0.0f;
@@ -1598,6 +1634,9 @@ template <int FMT>
 cudaError_t launch_fmt(int bn, int ku, bool pair, const LaunchParams& prm, const CUtensorMap& tmap,
                        cudaStream_t s, int dev) {
   if (pair) {
+    if constexpr (kGated) {
+      if (bn == 128 && ku == 2) return launch_t<FMT, 128, 2, true>(prm, tmap, s, dev);
+    }
     if (ku != 1) return cudaErrorInvalidValue;
     switch (bn) {
       case 128: return launch_t<FMT, 128, 1, true>(prm, tmap, s, dev);
@@ -1610,8 +1649,12 @@ cudaError_t launch_fmt(int bn, int ku, bool pair, const LaunchParams& prm, const
       case 16: return launch_t<FMT, 16, 2>(prm, tmap, s, dev);
       case 32: return launch_t<FMT, 32, 2>(prm, tmap, s, dev);
       case 64: return launch_t<FMT, 64, 2>(prm, tmap, s, dev);
-      default: return cudaErrorInvalidValue;
+      default: break;
     }
+    if constexpr (kGated) {
+      if (bn == 128) return launch_t<FMT, 128, 2>(prm, tmap, s, dev);
+    }
+    return cudaErrorInvalidValue;
   }
   switch (bn) {
     case 16: return launch_t<FMT, 16, 1>(prm, tmap, s, dev);
@@ -1948,23 +1991,66 @@ namespace {
 // What a launch of the gated kernel costs, in us: a start, a pace for each 128-k
 // chunk of the longest range, a tile's being split and each of its contributors,
 // and each of a range's pieces of tiles (its epilogue; with 128 rows and more the
-// tensor core waits for it).  Fitted to 7100 launches on a GB300 (NVFP4, 1024 to
-// 57344 x 512 to 8192, 16 to 4096 rows, every tile shape): 90 % of them within
-// 20 %, and the shape with the least is within 1 % of the fastest on the average.
-// plan_grouped's rules, made for large matrices, took 1.22 times as long, and with
-// whole tiles for ranges 1.37 times (4096 x 512, 300 rows: 21.4 us with its
-// 256-row tiles, 6.4 with 128 rows, 5.2 with whole tiles of 64).
+// tensor core waits for it).  The pace is `chunk` for a tile of bn rows and `slope`
+// less for each row that its height falls short, down to `least`.
 struct TileCost {
-  int bn;
+  int bn, ku;
   bool pair;
-  double start, chunk, split, part, piece;
+  double start, chunk, slope, least, split, part, piece;
+  double pace(int height) const { return std::max(least, chunk - slope * (bn - height)); }
 };
 constexpr TileCost kGatedCosts[] = {
-    {16, false, 3.4, 0.230, 2.0, 0.14, 0.49},  {32, false, 3.0, 0.237, 0.1, 0.62, 1.54},
-    {64, false, 3.2, 0.250, 1.7, 0.47, 0.83},  {128, false, 1.6, 0.408, 0.0, 1.32, 2.49},
-    {128, true, 3.4, 0.400, 0.4, 1.31, 1.19},  {256, false, 1.2, 0.563, 0.1, 2.33, 4.74},
-    {256, true, 2.4, 0.546, 0.3, 2.29, 4.10},
+    {16, 2, false, 3.4, 0.230, 0.0, 0.230, 2.0, 0.14, 0.49},
+    {32, 2, false, 3.0, 0.237, 0.0, 0.237, 0.1, 0.62, 1.54},
+    {64, 2, false, 3.2, 0.250, 0.0, 0.250, 1.7, 0.47, 0.83},
+    {128, 1, false, 1.6, 0.408, 0.0, 0.40, 0.0, 1.32, 2.49},
+    {128, 2, false, 1.8, 0.400, 0.0022, 0.25, 0.0, 1.32, 2.49},
+    {128, 2, true, 3.4, 0.345, 0.0014, 0.25, 0.4, 1.31, 1.19},
+    {256, 1, false, 1.2, 0.563, 0.0011, 0.40, 0.1, 2.33, 4.74},
+    {256, 1, true, 2.4, 0.546, 0.0019, 0.36, 0.3, 2.29, 4.10},
 };
+
+const TileCost& cost_of(const GemmPlan& pl) {
+  const TileCost* found = kGatedCosts;
+  for (const TileCost& c : kGatedCosts)
+    if (c.bn == pl.bn && c.pair == pl.pair && (c.ku == pl.ku || found->bn != pl.bn || found->pair != pl.pair)) found = &c;
+  return *found;
+}
+
+// Ranges of equal time over groups whose tiles have different heights.
+void plan_group_bounds(GemmPlan& pl) {
+  const int P = pl.num_ctas;
+  if (P < 2 || P > kMaxBoundCtas) return;
+  const TileCost& cost = cost_of(pl);
+  const int64_t per_tile = pl.k_stages / pl.ku;
+  double total = 0.0;
+  for (int g = 0; g < pl.num_groups; ++g)
+    total += static_cast<double>(pl.tile_base[g + 1] - pl.tile_base[g]) * per_tile * cost.pace(pl.height[g]);
+  int g = 0;
+  double before = 0.0;   // the time of the groups before g
+  pl.bound[0] = 0;
+  for (int c = 1; c < P; ++c) {
+    const double at = total * c / P;
+    auto of_group = [&]() {
+      return static_cast<double>(pl.tile_base[g + 1] - pl.tile_base[g]) * per_tile * cost.pace(pl.height[g]);
+    };
+    while (g + 1 < pl.num_groups && before + of_group() <= at) before += of_group(), ++g;
+    const int64_t unit = static_cast<int64_t>(pl.tile_base[g]) * per_tile +
+                         std::llround((at - before) / cost.pace(pl.height[g]));
+    pl.bound[c] = static_cast<int32_t>(
+        std::min<int64_t>(std::max<int64_t>(unit, pl.bound[c - 1] + 1), pl.units - (P - c)));
+  }
+  pl.bound[P] = static_cast<int32_t>(pl.units);
+  pl.use_bounds = true;
+}
+
+// The height of the tiles of `rows` activation rows in tiles of at most bn: equal
+// parts, in whole steps of the MMA's N.
+int gated_height(int64_t rows, int bn, bool pair) {
+  if (rows <= 0) return 0;
+  const int64_t tiles = (rows + bn - 1) / bn, step = pair ? 32 : 16;
+  return static_cast<int>(((rows + tiles - 1) / tiles + step - 1) / step * step);
+}
 
 }  // namespace
 
@@ -1972,16 +2058,31 @@ GemmPlan plan_gated(const int64_t* row_off, int num_groups, int64_t n, int64_t k
                     int pair_cap) {
   const int pair_mode = g_pair_mode.load(std::memory_order_relaxed);
   const int ov = tile_override();   // a forced tile shape, as in plan_grouped
-  const bool pair_ok = pair_cap > 0 && num_groups == 1 && n % (2 * kTileN) == 0 && pair_mode != 1;
+  const bool pair_ok = pair_cap > 0 && n % (2 * kTileN) == 0 && pair_mode != 1;
   const int64_t chunks = k / kStageK;
   GemmPlan best{};
   double best_us = 0.0;
   for (const TileCost& c : kGatedCosts) {
-    if (ov != 0 && (ov & 0xFFFF) != c.bn) continue;
+    // two chunks a unit where k holds pairs of them (and the forced shape has them:
+    // none of 128 rows has)
+    int ku = c.ku;
+    if (ku == 2 && chunks % 2 != 0) {
+      if (c.bn == 128 && !c.pair) continue;   // listed with one
+      ku = 1;
+    }
+    if (ov != 0) {
+      if ((ov & 0xFFFF) != c.bn || (c.bn == 128 && !c.pair && c.ku == 2)) continue;
+      if ((ov >> 16) == 1) ku = 1;
+    }
     if (c.pair ? !pair_ok : (pair_ok && pair_mode == 2 && c.bn >= 128)) continue;
-    const int ku = c.bn <= 64 && chunks % 2 == 0 && (ov == 0 || (ov >> 16) == 2) ? 2 : 1;
     int64_t tiles = 0;
-    for (int g = 0; g < num_groups; ++g) tiles += (row_off[g + 1] - row_off[g] + c.bn - 1) / c.bn;
+    double paces = 0.0;
+    for (int g = 0; g < num_groups; ++g) {
+      const int64_t rows = row_off[g + 1] - row_off[g], t = (rows + c.bn - 1) / c.bn;
+      tiles += t;
+      if (t > 0) paces += static_cast<double>(t) * c.pace(gated_height(rows, c.bn, c.pair));
+    }
+    const double pace = paces / static_cast<double>(tiles);   // the mean (ranges are weighted by it)
     tiles *= n / (kTileN * (c.pair ? 2 : 1));
     const int64_t per_tile = chunks / ku, units = tiles * per_tile;
     const int64_t ranges = c.pair ? pair_cap : num_sms;
@@ -1992,7 +2093,7 @@ GemmPlan plan_gated(const int64_t* row_off, int num_groups, int64_t n, int64_t k
                                                 : static_cast<double>(std::min(P, (per_tile + L - 1) / L + 1));
       const double pieces = whole ? static_cast<double>(std::max<int64_t>(1, L / per_tile))
                                   : static_cast<double>((L + per_tile - 1) / per_tile + 1);
-      const double us = c.start + c.chunk * static_cast<double>(L * ku) + (split ? c.split : 0.0) +
+      const double us = c.start + pace * static_cast<double>(L * ku) + (split ? c.split : 0.0) +
                         c.part * parts + c.piece * pieces;
       if (best.num_ctas != 0 && us >= best_us) return;
       best_us = us;
@@ -2020,8 +2121,15 @@ GemmPlan plan_gated(const int64_t* row_off, int num_groups, int64_t n, int64_t k
   pl.ku = best.ku;
   pl.pair = best.pair;
   lay_tiles(pl, row_off, num_groups, n, k);
+  for (int g = 0; g < num_groups; ++g) {
+    pl.height[g] = gated_height(row_off[g + 1] - row_off[g], pl.bn, pl.pair);
+    pl.a_rows = std::max(pl.a_rows, pl.height[g] / (pl.pair ? 2 : 1));
+  }
   pl.num_ctas = best.num_ctas;
-  if (best.use_bounds && pl.units < (int64_t(1) << 31)) plan_bounds(pl, late_start_ns());
+  if (best.use_bounds && pl.units < (int64_t(1) << 31)) {
+    if (num_groups == 1) plan_bounds(pl, late_start_ns());
+    else plan_group_bounds(pl);
+  }
   lay_workspace(pl);
   return pl;
 }

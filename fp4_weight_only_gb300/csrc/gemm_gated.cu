@@ -11,7 +11,11 @@ cudaError_t launch_gated(const GemmPlan& pl, const GemmArgs& a, const GatedArgs&
   GatedParams prm{};
   fill_params(pl, a, prm);
   prm.act = g.act;
-  for (int i = 0; i < pl.num_groups; ++i) prm.group_up[i] = g.group_up[i];
+  prm.a_rows = pl.a_rows;
+  for (int i = 0; i < pl.num_groups; ++i) {
+    prm.group_up[i] = g.group_up[i];
+    prm.height[i] = pl.height[i];
+  }
   return launch_planned(pl, a, prm, tmap, stream);
 }
 

@@ -58,6 +58,10 @@ struct GemmPlan {
   int32_t row_off[kMaxGroups + 1];
   int32_t tile_base[kMaxGroups + 1];
   WsLayout ws;
+  // gated products only: the rows of each group's tiles (at most bn), and of an
+  // activation copy (the largest of them, or half of it with CTA pairs)
+  int32_t height[kMaxGroups];
+  int32_t a_rows;
 };
 
 // pair_cap: CTA pairs that can be resident at once (pair_capacity()), 0 to

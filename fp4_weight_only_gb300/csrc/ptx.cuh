@@ -377,6 +377,9 @@ __device__ __forceinline__ uint64_t smem_desc_kmajor_sw128(uint32_t saddr) {
   return d;
 }
 
+// The bits of N (a multiple of 16 here) in an instruction descriptor.
+__host__ __device__ constexpr uint32_t idesc_n(uint32_t N) { return (N >> 3) << 17; }
+
 // Instruction descriptor, kind::f16: FP32 accumulator, BF16 A and B, both
 // K-major, shape M x N.
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(uint32_t M, uint32_t N) {
