@@ -161,11 +161,14 @@ struct FixJob {
   uint16_t* c_g;                        // output rows of the tile's group
   int64_t c_first, c_last, first_slot;  // contributing CTAs, slot of the first
   int64_t row0, col0, g_rows;           // tile origin in C; rows of the group
-  float alpha, alpha_up;                // (gated: the gate's and the up matrix's)
+  float alpha;
   int32_t d;                            // accumulator buffer of the segment
   uint32_t has;                         // bit t: issuer t's accumulator contributes
-  int32_t height;                       // activation rows of the tile
   int32_t valid;
+};
+struct GatedFixJob : FixJob {
+  float alpha_up;    // (alpha: the gate's)
+  int32_t height;    // activation rows of the tile
 };
 
 // Position of a tile: group, weight tile, activation tile (tile-major in a
@@ -378,7 +381,7 @@ struct Cfg {
   // barriers, tensor-memory holder, flags and the deferred fix-up job fit in
   // the 1024 bytes after the rings
   static_assert((2 * kWStages + 3 * kXStages + kNumA + 2 * kNumD + kMaxMmaThreads + 1) * 8 + 16 +
-                        sizeof(FixJob) + 16 <= 1024,
+                        sizeof(GatedFixJob) + 16 <= 1024,
                 "barrier region");
 };
 
@@ -530,7 +533,8 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(xpeer + (PAIR ? C::kXStages : 0));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   volatile int* epi_flag = abort_flag + 1;
-  FixJob* fix = reinterpret_cast<FixJob*>(
+  using Job = std::conditional_t<GATED, GatedFixJob, FixJob>;
+  Job* fix = reinterpret_cast<Job*>(
       (reinterpret_cast<uintptr_t>(epi_flag + 1) + 15) & ~static_cast<uintptr_t>(15));
   // output staging (kStageC bytes) after the 1024-byte barrier region
   uint16_t* stage_c = reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(bars) + 1024);
@@ -1010,7 +1014,7 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
       if constexpr (GATED) g_rows = min(g_rows, (mt + 1) * height);
       uint16_t* const c_g = p.c + static_cast<int64_t>(p.row_off[ec.g]) * c_cols;
       const float alpha = p.alpha_dev ? alpha_dev : p.group_alpha[ec.g];
-      float alpha_up = alpha;
+      [[maybe_unused]] float alpha_up = alpha;
       if constexpr (GATED) alpha_up = p.group_up[ec.g];
       cursor_next<BN>(p, ec);
       const int d = static_cast<int>(seg % C::kNumD);
@@ -1064,10 +1068,9 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
             fix->col0 = (static_cast<int64_t>(nt) * wmul + rank) * kTileN;
             fix->g_rows = g_rows;
             fix->alpha = alpha;
-            fix->alpha_up = alpha_up;
             fix->d = d;
             fix->has = has;
-            fix->height = height;
+            if constexpr (GATED) fix->alpha_up = alpha_up, fix->height = height;
             fix->valid = 1;
           }
           u = seg_end;
@@ -1088,10 +1091,9 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
             fix->col0 = (static_cast<int64_t>(nt) * wmul + rank) * kTileN;
             fix->g_rows = g_rows;
             fix->alpha = alpha;
-            fix->alpha_up = alpha_up;
             fix->d = d;
             fix->has = has;
-            fix->height = height;
+            if constexpr (GATED) fix->alpha_up = alpha_up, fix->height = height;
             fix->valid = 1;
           }
           u = seg_end;
@@ -1184,10 +1186,9 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
             fix->col0 = (static_cast<int64_t>(nt) * wmul + rank) * kTileN;
             fix->g_rows = g_rows;
             fix->alpha = alpha;
-            fix->alpha_up = alpha_up;
             fix->d = d;
             fix->has = has;
-            fix->height = height;
+            if constexpr (GATED) fix->alpha_up = alpha_up, fix->height = height;
             fix->valid = 1;
           }
         } else if (*epi_flag) {
@@ -1400,7 +1401,7 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
     const bool run_fix = fix->valid && !*abort_flag;
     __syncthreads();
     if (run_fix) {
-      const FixJob f = *fix;
+      const Job f = *fix;
       constexpr int kFixGroups = C::kThreads / 32 >= 16 ? 4 : 2;
       constexpr int kCols = BN / kFixGroups;   // activation rows per group (>= 32)
       const int fg = warp >> 2;
@@ -1488,7 +1489,7 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
     // (gated: as above, no check raises the flag before all threads have read it)
     if constexpr (GATED) __syncthreads();
     if (run_fix) {
-      const FixJob f = *fix;
+      const Job f = *fix;
       // (gated, 128 rows and more: the groups there are take every kFixGroups-th 16 rows)
       constexpr bool kStrided = GATED && BN >= 128;
       constexpr int kFixGroups = kStrided ? C::kThreads / 128 : C::kThreads / 32 >= 16 ? 4 : 2;
@@ -1497,6 +1498,8 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
       constexpr int kStep = kStrided ? kLd * kFixGroups : kLd;
       const int fg = warp >> 2;
       const int row_base = fg * (kStrided ? kLd : kCols);
+      int rows_here = kCols;
+      if constexpr (kStrided) rows_here = f.height - row_base;
       if (fg < kFixGroups && (GATED || !*abort_flag) &&
           PETIT_CHECK(f.d >= 0 && f.d < C::kNumD && f.c_first >= 0 && f.c_first <= cta &&
                       cta <= f.c_last && f.c_last < P && f.first_slot >= 0 &&
@@ -1506,7 +1509,7 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
         const uint32_t tbase = tmem + (static_cast<uint32_t>(32 * q) << 16) + C::kDColBase +
                                f.d * BN + row_base;
   #pragma unroll 1
-        for (int c0 = 0; c0 < (kStrided ? f.height - row_base : kCols); c0 += kStep) {
+        for (int c0 = 0; c0 < rows_here; c0 += kStep) {
           float own[kLd];
   #pragma unroll
           for (int j = 0; j < kLd; ++j) own[j] = 0.0f;
