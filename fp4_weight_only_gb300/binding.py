@@ -888,6 +888,8 @@ def rotary(rope, q, k, positions, out=None):
     number = _DTYPES.get(dtype)
     if number is None or q.dim() != 3:
         raise ValueError("q: need a BF16 or FP16 tensor [tokens, heads, head_dim]")
+    if device < 0:
+        raise ValueError("rope: need frequencies on a CUDA device")
     n, q_heads, d = q.shape
     rows = _heads(q, dtype, n, d, device, "q")
     rows_k = (None, 0, 0) if k is None else _heads(k, dtype, n, d, device, "k")

@@ -133,3 +133,5 @@ def test_binding_refuses_before_the_library(lib):
                 dict(positions=torch.zeros(3, dtype=torch.int64)), dict(positions=torch.zeros(2)), dict(out=(q[:, :2], q))):
         with pytest.raises(ValueError):
             binding.rotary(rope, **{**dict(q=q, k=q, positions=torch.zeros(2, dtype=torch.int64)), **bad})
+    with pytest.raises(ValueError, match="CUDA"):
+        binding.rotary(rope, q, q, torch.zeros(2, dtype=torch.int64))
