@@ -134,6 +134,7 @@ struct GatedParams : Params {
   float group_up[kMaxGroups];
   int32_t act;      // kActSilu, ...
   int32_t a_rows;   // rows of an activation copy: the largest height, or half of it in pairs
+  int32_t spread;   // tiles of a range's consecutive pieces that lie num_ctas apart (0: adjacent)
   int32_t height[kMaxGroups + 1];   // activation rows a tile (the last: past the last group)
 };
 
@@ -211,6 +212,47 @@ __device__ __forceinline__ void cursor_next(const Params& p, TileCursor& c) {
   c.row0 = c.g < p.num_groups ? p.row_off[c.g] : 0;
 }
 
+// The gated kernel's cursor.  With several activation tiles a weight tile, adjacent
+// tiles for a range would read its weights again for each of them, long after the
+// others have driven them out of L2.  So the tiles are dealt out: the i-th of the
+// `spread` whole tiles that range c begins with is tile i * num_ctas + c of the
+// order above, so that all ranges work on few weight tiles at a time and one
+// reading from HBM serves all activation tiles (4096 rows through 57344 x 8192,
+// back to back: 2365 us without, 2190 so; what HBM does not draw, the tensor cores
+// may).
+struct GatedCursor : TileCursor {
+  int32_t tile;   // as ranges count them
+};
+
+[[maybe_unused]] __device__ __forceinline__ void place_tile(const GatedParams& p, GatedCursor& c) {
+  int32_t t = c.tile;
+  if (t < p.spread * p.num_ctas) {
+    const int32_t range = t / p.spread;
+    t = (t - range * p.spread) * p.num_ctas + range;
+  }
+  c.nt = t / c.m_tiles;
+  c.mt = t - c.nt * c.m_tiles;
+}
+
+template <int BN>
+__device__ __forceinline__ GatedCursor cursor_at(const GatedParams& p, int64_t tile) {
+  GatedCursor c;
+  static_cast<TileCursor&>(c) = cursor_at<BN>(static_cast<const Params&>(p), tile);
+  c.tile = static_cast<int32_t>(tile);
+  if (p.spread > 0) place_tile(p, c);
+  return c;
+}
+
+template <int BN>
+__device__ __forceinline__ void cursor_next(const GatedParams& p, GatedCursor& c) {
+  ++c.tile;
+  if (p.spread > 0) place_tile(p, c);
+  else cursor_next<BN>(static_cast<const Params&>(p), static_cast<TileCursor&>(c));
+}
+
+template <typename P>
+using Cursor = std::conditional_t<std::is_same_v<P, GatedParams>, GatedCursor, TileCursor>;
+
 // The weight-chunk stream of a CTA: unit by unit, the unit's KU repacked
 // chunks (contiguous codes + scales) by one bulk copy into the next weight
 // stage.  Addresses advance incrementally (a runtime 64-bit division costs
@@ -218,21 +260,21 @@ __device__ __forceinline__ void cursor_next(const Params& p, TileCursor& c) {
 // are adjacent chunks, so the source moves on by one unit's bytes and is
 // recomputed only at a tile boundary; stage addresses move on by one stage
 // and wrap.
-template <int FMT, int BN, int KU>
+template <int FMT, int BN, int KU, typename P>
 struct WeightStream {
   static constexpr uint32_t kBytes = KU * FmtTraits<FMT>::kChunkBytes;
   const uint8_t* src;
   int32_t KS;            // units per tile
   int32_t ku;            // unit index inside the tile
   int32_t wmul, wadd;    // weight tile of work tile nt: nt * wmul + wadd (CTA pairs: 2 nt + rank)
-  TileCursor cur;
+  Cursor<P> cur;
   uint32_t dst, dst0;    // shared-memory stage, first stage
   uint32_t bar, full0;   // stage * 8, address of the stage-0 full barrier
   uint32_t ph;           // phase of the stage's free barrier to wait for, ^ 1
   int32_t stages;
 
   // starting at unit ku of tile `tile`
-  __device__ __forceinline__ void init(const Params& p, int32_t tile, int32_t ku0, int32_t ks,
+  __device__ __forceinline__ void init(const P& p, int32_t tile, int32_t ku0, int32_t ks,
                                        uint32_t sm_w, uint32_t wfull0, int32_t nstages,
                                        int32_t tile_mul = 1, int32_t tile_add = 0) {
     KS = ks;
@@ -248,7 +290,7 @@ struct WeightStream {
     ph = 0;
     stages = nstages;
   }
-  __device__ __forceinline__ void advance(const Params& p) {
+  __device__ __forceinline__ void advance(const P& p) {
     src += kBytes;
     dst += kBytes;
     bar += 8;
@@ -263,14 +305,14 @@ struct WeightStream {
       src = p.rep + cur.g * p.rep_stride + chunk_offset<FMT>(cur.nt * wmul + wadd, 0, KS * KU);
     }
   }
-  __device__ __forceinline__ void issue(const Params& p, uint64_t policy) {
+  __device__ __forceinline__ void issue(const P& p, uint64_t policy) {
     mbar_arrive_expect_tx(full0 + bar, kBytes);
     bulk_g2s(dst, src, kBytes, full0 + bar, policy);
     advance(p);
   }
   // bounds-checking build: the copy's source lies inside its group's
   // repacked weights and its destination inside the weight ring
-  __device__ __forceinline__ bool in_bounds(const Params& p) const {
+  __device__ __forceinline__ bool in_bounds(const P& p) const {
 #ifdef PETIT_CHECK_BOUNDS
     if (cur.g < 0 || cur.g >= p.num_groups) return false;
     const uint8_t* base = p.rep + cur.g * p.rep_stride;
@@ -282,7 +324,7 @@ struct WeightStream {
 #endif
   }
   // a copy that failed its check: the stage's barrier completes without data
-  __device__ __forceinline__ void skip(const Params& p) {
+  __device__ __forceinline__ void skip(const P& p) {
     mbar_arrive(full0 + bar);
     advance(p);
   }
@@ -505,6 +547,7 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
                 const __grid_constant__ CUtensorMap tmap_a) {
   using C = Cfg<FMT, BN, KU, PAIR, GATED>;
   using T = FmtTraits<FMT>;
+  using P_ = std::conditional_t<GATED, GatedParams, Params>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -699,7 +742,7 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
       const int32_t ku0 = ku0_32;
       // the first ring of weight chunks was issued by an epilogue thread
       // before the grid dependency wait; this stream continues after it
-      WeightStream<FMT, BN, KU> ws;
+      WeightStream<FMT, BN, KU, P_> ws;
       ws.init(p, tile0, ku0, ks, smem_u32(sm_w), smem_u32(&wfull[0]), C::kWStages, wmul,
               static_cast<int32_t>(rank));
       int32_t wi = nu < C::kWStages ? nu : C::kWStages;
@@ -707,7 +750,7 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
       int32_t xi = 0;
       uint32_t xph = 0;
       int32_t x_ku = ku0;
-      TileCursor xc = cursor_at<BN>(p, tile0);
+      Cursor<P_> xc = cursor_at<BN>(p, tile0);
       // first activation row of this CTA's part of the tile (CTA pairs: the
       // odd CTA holds the second half)
       int32_t xhalf = 0, xrow = 0, xk = x_ku * 2 * KU;
@@ -831,7 +874,7 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
       int st = t, b = t;   // t < kMmaThreads <= kNumA <= kXStages
       uint32_t ph = 0, pb = 0;
       bool ok = true;
-      [[maybe_unused]] TileCursor ic{};
+      [[maybe_unused]] Cursor<P_> ic{};
       if constexpr (GATED) ic = cursor_at<BN>(p, tile0_32);
       for (int32_t s0 = 0; s0 < nu && ok;) {
         uint32_t idesc = C::kIdesc;
@@ -928,7 +971,7 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
       // (every stage starts free).  Issuing a bulk copy takes a while, so
       // this idle thread does it and the producer reaches the dependency
       // wait, and the activation copies after it, without delay.
-      WeightStream<FMT, BN, KU> ws;
+      WeightStream<FMT, BN, KU, P_> ws;
       ws.init(p, tile0_32, ku0_32, ks32, smem_u32(sm_w), smem_u32(&wfull[0]), C::kWStages, wmul,
               static_cast<int32_t>(rank));
       const uint64_t policy = p.weights_reused ? l2_policy_evict_normal() : l2_policy_evict_first();
@@ -944,12 +987,12 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
       if (cta + half < p.num_ctas) {
         const int32_t pc = static_cast<int32_t>(cta) + half;
         const int32_t pu0 = cta_lo(p, pc), pn = cta_lo(p, pc + 1) - pu0;
-        WeightStream<FMT, BN, KU> pw;
+        WeightStream<FMT, BN, KU, P_> pw;
         pw.init(p, pu0 / ks32, pu0 % ks32, ks32, 0, 0, C::kWStages, wmul,
                 static_cast<int32_t>(rank));
         for (int32_t j = 0; j < pn && j < C::kWStages; ++j) {
           if (!PETIT_CHECK(pw.in_bounds(p))) break;
-          bulk_prefetch_l2(pw.src, WeightStream<FMT, BN, KU>::kBytes);
+          bulk_prefetch_l2(pw.src, WeightStream<FMT, BN, KU, P_>::kBytes);
           pw.advance(p);
         }
       }
@@ -964,7 +1007,7 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
     // epilogue factor: a device-resident global scale is read here, after the
     // grid dependency wait, so a preceding kernel may have produced it
     const float alpha_dev = p.alpha_dev ? p.alpha_scale * *p.alpha_dev : 0.0f;
-    TileCursor ec = cursor_at<BN>(p, first_tile_of_cta);   // advances one tile per segment
+    Cursor<P_> ec = cursor_at<BN>(p, first_tile_of_cta);   // advances one tile per segment
     uint32_t epi_phase = 0;
     // bounded barrier among the four epilogue warps (a hardware named
     // barrier has no time limit)
@@ -2132,6 +2175,14 @@ GemmPlan plan_gated(const int64_t* row_off, int num_groups, int64_t n, int64_t k
     pl.a_rows = std::max(pl.a_rows, pl.height[g] / (pl.pair ? 2 : 1));
   }
   pl.num_ctas = best.num_ctas;
+  // Tiles dealt out (see GatedCursor) where weights that L2 does not hold meet four
+  // activation tiles or more: 4096 rows through 57344 x 8192 2365 us without and 2190
+  // with, through 28672 x 4096 581 and 563, 1024 rows through 57344 x 8192 548 and
+  // 539; through 8192 x 8192 332 and 341, 300 rows through 28672 x 4096 55.8 and 57.0.
+  constexpr int64_t kSpreadWeights = int64_t(48) << 20;
+  const int64_t all_tiles = static_cast<int64_t>(pl.tile_base[num_groups]);
+  if (num_groups == 1 && n * k / 2 > kSpreadWeights && all_tiles >= 4 * static_cast<int64_t>(pl.n_tiles))
+    pl.spread = static_cast<int>(all_tiles / pl.num_ctas);
   if (best.use_bounds && pl.units < (int64_t(1) << 31)) {
     if (num_groups == 1) plan_bounds(pl, late_start_ns());
     else plan_group_bounds(pl);

@@ -62,6 +62,7 @@ struct GemmPlan {
   // activation copy (the largest of them, or half of it with CTA pairs)
   int32_t height[kMaxGroups];
   int32_t a_rows;
+  int32_t spread;   // whole tiles a range that are dealt out num_ctas apart (0: none)
 };
 
 // pair_cap: CTA pairs that can be resident at once (pair_capacity()), 0 to

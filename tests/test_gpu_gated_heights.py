@@ -94,3 +94,25 @@ def test_bounds_checking_build(cuda_lib, m):
             assert ws.status() == 8
         finally:
             chk.petit_check_set_limits(-1, -1)
+
+
+@pytest.mark.parametrize("fmt,m", [("nvfp4", 800), ("mxfp4", 1030)])
+def test_tiles_dealt_out_to_ranges(cuda_lib, fmt, m):
+    """Weights past what L2 holds and four activation tiles or more: ranges begin
+    with tiles that lie apart.  Every column against products of the dequantised
+    weights in 64 bits."""
+    n, k = 14336, 4096
+    g = torch.Generator(device="cuda").manual_seed(m)
+    wg, wu = ((torch.randn((n, k), generator=g, device="cuda") * k ** -0.5).bfloat16() for _ in range(2))
+    one = cuda_lib.GatedWeight(wg, wu, fmt, "amax")
+    a = activations(m, k, fmt, m)
+    got = one(a, "silu").double()
+    both = cuda_lib.dequant(one.rep, 2 * n, k, fmt).unflatten(0, (-1, 2, 8)).transpose(0, 1).flatten(1, 2).double()
+    x = a.double()
+    gate, up = (s * (x @ w.T) for s, w in zip(one.global_scales, both))
+    step = 1.25 * k * 2.0 ** -24
+    dg, du = (step * s * (x.abs() @ w.abs().T) for s, w in zip(one.global_scales, both))
+    act = gate * torch.sigmoid(gate)
+    want = act * up
+    off = (1.13 * dg + act.abs() * 2.0 ** -15 + 2.0 ** -120) * (up.abs() + du) + act.abs() * du
+    assert ((got - want).abs() <= want.abs() * 2.0 ** -8 + off * (1 + 2.0 ** -8) + 2.0 ** -134).all()
