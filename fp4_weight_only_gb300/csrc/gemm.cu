@@ -134,7 +134,7 @@ struct GatedParams : Params {
   float group_up[kMaxGroups];
   int32_t act;      // kActSilu, ...
   int32_t a_rows;   // rows of an activation copy: the largest height, or half of it in pairs
-  int32_t spread;   // tiles of a range's consecutive pieces that lie num_ctas apart (0: adjacent)
+  int32_t spread;   // tiles that begin in a range, rounded down, if they are dealt out (0: they are not)
   int32_t height[kMaxGroups + 1];   // activation rows a tile (the last: past the last group)
 };
 
@@ -214,24 +214,34 @@ __device__ __forceinline__ void cursor_next(const Params& p, TileCursor& c) {
 
 // The gated kernel's cursor.  With several activation tiles a weight tile, adjacent
 // tiles for a range would read its weights again for each of them, long after the
-// others have driven them out of L2.  So the tiles are dealt out: the i-th of the
-// `spread` whole tiles that range c begins with is tile i * num_ctas + c of the
-// order above, so that all ranges work on few weight tiles at a time and one
-// reading from HBM serves all activation tiles (4096 rows through 57344 x 8192,
-// back to back: 2365 us without, 2190 so; what HBM does not draw, the tensor cores
-// may).
+// others have driven them out of L2.  So the tiles are dealt out: of those that
+// begin in range c, the i-th is tile i * num_ctas + c of the order above (the last
+// of the ranges that have one more follow), so that all ranges work on few weight
+// tiles at a time and one reading from HBM serves all activation tiles.  What HBM
+// does not draw, the tensor cores may: 4096 rows through 57344 x 8192, back to back,
+// 2281 us without and 2141 so; 1024
+// rows, 1014 MB of HBM reads without and 312 so.
 struct GatedCursor : TileCursor {
   int32_t tile;   // as ranges count them
 };
 
+__device__ __forceinline__ int32_t cta_lo(const Params& p, int32_t c);
+__device__ __forceinline__ int32_t cta_of_unit(const Params& p, int64_t u);
+
+// (Weight and activation tile of c.tile; a function of its own, since its divisions
+// are long code, which a launch without it would have to step over.)
+[[maybe_unused]] __device__ __noinline__ int2 dealt_tile(const GatedParams& p, int32_t tile, int32_t m_tiles) {
+  const int32_t range = cta_of_unit(p, static_cast<int64_t>(tile) * p.k_units);
+  const int32_t first = (cta_lo(p, range) + p.k_units - 1) / p.k_units;   // tile that begins in it
+  const int32_t i = tile - first;
+  const int32_t t = i < p.spread ? i * p.num_ctas + range : p.spread * p.num_ctas + first - range * p.spread;
+  return make_int2(t / m_tiles, t % m_tiles);
+}
+
 [[maybe_unused]] __device__ __forceinline__ void place_tile(const GatedParams& p, GatedCursor& c) {
-  int32_t t = c.tile;
-  if (t < p.spread * p.num_ctas) {
-    const int32_t range = t / p.spread;
-    t = (t - range * p.spread) * p.num_ctas + range;
-  }
-  c.nt = t / c.m_tiles;
-  c.mt = t - c.nt * c.m_tiles;
+  const int2 at = dealt_tile(p, c.tile, c.m_tiles);
+  c.nt = at.x;
+  c.mt = at.y;
 }
 
 template <int BN>
@@ -2175,18 +2185,19 @@ GemmPlan plan_gated(const int64_t* row_off, int num_groups, int64_t n, int64_t k
     pl.a_rows = std::max(pl.a_rows, pl.height[g] / (pl.pair ? 2 : 1));
   }
   pl.num_ctas = best.num_ctas;
-  // Tiles dealt out (see GatedCursor) where weights that L2 does not hold meet four
-  // activation tiles or more: 4096 rows through 57344 x 8192 2365 us without and 2190
-  // with, through 28672 x 4096 581 and 563, 1024 rows through 57344 x 8192 548 and
-  // 539; through 8192 x 8192 332 and 341, 300 rows through 28672 x 4096 55.8 and 57.0.
-  constexpr int64_t kSpreadWeights = int64_t(48) << 20;
-  const int64_t all_tiles = static_cast<int64_t>(pl.tile_base[num_groups]);
-  if (num_groups == 1 && n * k / 2 > kSpreadWeights && all_tiles >= 4 * static_cast<int64_t>(pl.n_tiles))
-    pl.spread = static_cast<int>(all_tiles / pl.num_ctas);
   if (best.use_bounds && pl.units < (int64_t(1) << 31)) {
     if (num_groups == 1) plan_bounds(pl, late_start_ns());
     else plan_group_bounds(pl);
   }
+  // Tiles dealt out (see GatedCursor) where several activation tiles meet weights
+  // that L2 does not hold.  Us without and with: 57344 x 8192, 4096 rows 2281 and 2141,
+  // 1024 rows 540 and 520, 512 rows 277 and 270; 28672 x 8192, 512 rows 143 and 141;
+  // 28672 x 4096, 4096 rows 577 and 556, but 1024 rows 147.7 and 148.7, 300 rows 56
+  // and 58; 8192 x 8192, 4096 rows 332 and 341.
+  const int64_t codes = n * k / 2, activation_tiles = pl.n_tiles > 0 ? pl.tile_base[num_groups] / pl.n_tiles : 0;
+  if (num_groups == 1 && !pl.use_bounds &&
+      ((codes > int64_t(64) << 20 && activation_tiles >= 2) || (codes > int64_t(48) << 20 && activation_tiles >= 8)))
+    pl.spread = static_cast<int>(pl.tile_base[num_groups] / pl.num_ctas);
   lay_workspace(pl);
   return pl;
 }

@@ -96,12 +96,11 @@ def test_bounds_checking_build(cuda_lib, m):
             chk.petit_check_set_limits(-1, -1)
 
 
-@pytest.mark.parametrize("fmt,m", [("nvfp4", 800), ("mxfp4", 1030)])
-def test_tiles_dealt_out_to_ranges(cuda_lib, fmt, m):
-    """Weights past what L2 holds and four activation tiles or more: ranges begin
-    with tiles that lie apart.  Every column against products of the dequantised
+@pytest.mark.parametrize("fmt,m,k", [("nvfp4", 300, 5120), ("nvfp4", 2100, 4096), ("mxfp4", 700, 5120)])
+def test_tiles_dealt_out_to_ranges(cuda_lib, fmt, m, k):
+    """Weights past what L2 holds and several activation tiles: ranges take tiles that lie apart.  Every column against products of the dequantised
     weights in 64 bits."""
-    n, k = 14336, 4096
+    n = 14336
     g = torch.Generator(device="cuda").manual_seed(m)
     wg, wu = ((torch.randn((n, k), generator=g, device="cuda") * k ** -0.5).bfloat16() for _ in range(2))
     one = cuda_lib.GatedWeight(wg, wu, fmt, "amax")
