@@ -2145,6 +2145,8 @@ GemmPlan plan_gated(const int64_t* row_off, int num_groups, int64_t n, int64_t k
     tiles *= n / (kTileN * (c.pair ? 2 : 1));
     const int64_t per_tile = chunks / ku, units = tiles * per_tile;
     const int64_t ranges = c.pair ? pair_cap : num_sms;
+    // (no arrangement takes less than its share of the chunks)
+    if (best.num_ctas != 0 && c.start + pace * static_cast<double>(units * ku / ranges) >= best_us) continue;
     auto consider = [&](int64_t P, bool whole) {
       const int64_t L = (units + P - 1) / P;
       const bool split = !(whole && L % per_tile == 0);
@@ -2170,8 +2172,9 @@ GemmPlan plan_gated(const int64_t* row_off, int num_groups, int64_t n, int64_t k
                                         c.bn > 64);
     for (int64_t parts = 1; parts <= 8 && tiles * parts <= most; ++parts)
       if (per_tile % parts == 0) consider(tiles * parts, true);
-    const int64_t least = (tiles + most - 1) / most;   // whole tiles a range, at least
-    for (int64_t each = std::max<int64_t>(least, 2); each <= 2 * least; ++each)
+    // whole tiles a range, at least (many of them leave little to even out)
+    const int64_t least = (tiles + most - 1) / most;
+    for (int64_t each = std::max<int64_t>(least, 2); each <= 2 * least && least <= 8; ++each)
       if (tiles % each == 0) consider(tiles / each, true);
   }
   GemmPlan pl{};
