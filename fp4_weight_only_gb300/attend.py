@@ -11,7 +11,7 @@ slots the device advances.  It prints the times, and how far the attention
 lies from one in FP32 over the tokens that `kv_read` gives back.  Weights and
 inputs are random and carry no positions; norms and the MLP are the caller's,
 and so is position encoding, which enters between the product and the cache
-(`position`).
+(`position`); ``layer.DecoderLayer`` brings all three.
 """
 
 import argparse

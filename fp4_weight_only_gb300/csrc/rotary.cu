@@ -9,6 +9,9 @@
 // part of a turn, are the angle in -pi..pi that the hardware's sine and cosine
 // take (2^-20.9 off at most: a sixteenth of FP16's rounding of the result, 2^-11
 // of its size).
+//
+// Bound by memory, each element read and written once: 8192 tokens of 64 + 8 heads
+// of 128 45 us, 6.7 TB/s; one token 1.7 us in a graph, a launch.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
