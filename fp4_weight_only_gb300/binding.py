@@ -861,7 +861,6 @@ class Rotary:
         self.turns = torch.tensor([turns(f) for f in frequencies], dtype=torch.int64,
                                   device=torch.device(device or "cuda"))
         self.rot_dim, self.interleaved, self.magnitude = rot_dim, bool(interleaved), float(magnitude)
-        self.device_index, self.turns_address = self.turns.get_device(), self.turns.data_ptr()
 
     def __call__(self, q, k, positions, out=None):
         return rotary(self, q, k, positions, out)
@@ -884,7 +883,7 @@ def rotary(rope, q, k, positions, out=None):
     `positions` (int64 or int32 [tokens]).  `rope`: a :class:`Rotary`.  Returns
     (q, k) as new tensors, or in `out`, a pair of such tensors: (q, k) itself
     turns them in place."""
-    dtype, device = q.dtype, rope.device_index
+    dtype, device = q.dtype, rope.turns.get_device()
     number = _DTYPES.get(dtype)
     if number is None or q.dim() != 3:
         raise ValueError("q: need a BF16 or FP16 tensor [tokens, heads, head_dim]")
@@ -906,7 +905,7 @@ def rotary(rope, q, k, positions, out=None):
     if ((not wide and positions.dtype is not torch.int32) or positions.shape != (n,) or not positions.is_contiguous()
             or positions.get_device() != device):
         raise ValueError(f"positions: need a contiguous int64 or int32 tensor [{n}] on the frequencies' device")
-    args = RotaryArgs(*rows, *rows_k, *rows_out, *rows_k_out, rope.turns_address, positions.data_ptr(), n, q_heads,
+    args = RotaryArgs(*rows, *rows_k, *rows_out, *rows_k_out, rope.turns.data_ptr(), positions.data_ptr(), n, q_heads,
                       0 if k is None else k.shape[1], d, rope.rot_dim, number, rope.interleaved, not wide,
                       rope.magnitude)
     _check(load().petit_rotary(ctypes.byref(args), _stream_on(device)), "rotary")

@@ -98,8 +98,9 @@ def test_bounds_checking_build(cuda_lib, m):
 
 @pytest.mark.parametrize("fmt,m,k", [("nvfp4", 300, 5120), ("nvfp4", 2100, 4096), ("mxfp4", 700, 5120)])
 def test_tiles_dealt_out_to_ranges(cuda_lib, fmt, m, k):
-    """Weights past what L2 holds and several activation tiles: ranges take tiles that lie apart.  Every column against products of the dequantised
-    weights in 64 bits."""
+    """Weights past what L2 holds and several activation tiles: ranges take tiles
+    that lie apart.  Every column against products of the dequantised weights in 64
+    bits; no index leaves its buffer."""
     n = 14336
     g = torch.Generator(device="cuda").manual_seed(m)
     wg, wu = ((torch.randn((n, k), generator=g, device="cuda") * k ** -0.5).bfloat16() for _ in range(2))
@@ -115,3 +116,8 @@ def test_tiles_dealt_out_to_ranges(cuda_lib, fmt, m, k):
     want = act * up
     off = (1.13 * dg + act.abs() * 2.0 ** -15 + 2.0 ** -120) * (up.abs() + du) + act.abs() * du
     assert ((got - want).abs() <= want.abs() * 2.0 ** -8 + off * (1 + 2.0 ** -8) + 2.0 ** -134).all()
+    if m == 300:
+        with cuda_lib.bounds_checked():
+            ws = cuda_lib.Workspace()
+            checked = one(a, "silu", workspace=ws)
+            assert ws.status() == 0 and torch.equal(checked.double(), got)

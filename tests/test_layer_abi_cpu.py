@@ -127,7 +127,7 @@ def test_binding_refuses_before_the_library(lib):
     with pytest.raises(ValueError, match="finite"):
         binding.Rotary(4, frequencies=[1.0, INF], device="cpu")
     rope = binding.Rotary(64, device="cpu")
-    assert rope.turns.shape == (32,) and rope.device_index == -1
+    assert rope.turns.shape == (32,)
     q = torch.zeros((2, 3, 64), dtype=torch.bfloat16)
     for bad in (dict(q=q.float()), dict(q=q[0]), dict(q=q.transpose(1, 2)), dict(k=q[:1]), dict(k=q.half()),
                 dict(positions=torch.zeros(3, dtype=torch.int64)), dict(positions=torch.zeros(2)), dict(out=(q[:, :2], q))):
