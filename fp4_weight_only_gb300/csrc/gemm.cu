@@ -1319,6 +1319,17 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
     const int i0 = kFirstReuse0 + grp - (kFirstReuse0 - G + grp >= C::kNumA ? G : 0);
     int st2 = (i0 - C::kNumA) % C::kXStages;
     uint32_t ph2 = ((i0 - C::kNumA) / C::kXStages) & 1;
+    // Gives chunk stage s back to the copies.  It stands after the unit's last
+    // stores to tensor memory, whose operands come out of the loads: an arrival
+    // does not wait for loads whose values nothing has used yet, and the chunk of
+    // unit i + kWStages could land before they had read this one.  (So it did with
+    // the arrival before those stores: in one of some 300 launches of 256-row tiles
+    // after a pause, eight or more weight rows had the codes, or the scales, of two
+    // units later.)
+    auto release_chunk = [&](int s) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&wfree[s]));
+    };
     for (int32_t i = grp; i < nu; i += G) {
       if (!PETIT_CHECK(st >= 0 && st < C::kWStages && b >= 0 && b < C::kNumA && st2 >= 0 &&
                        st2 < C::kXStages))
@@ -1351,11 +1362,6 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
                 *reinterpret_cast<const uint16_t*>(chunk + kWChunkBytes + (h * kTileN + r) * 2);
             decode_group<FMT, kFast>(g0, sv & 0xFFu, o[0]);
             decode_group<FMT, kFast>(g1, (sv >> 8) & 0xFFu, o[1]);
-            if (hj == 2 * KU - 1) {
-              // the decode consumed every byte this warp read: release the chunk
-              __syncwarp();
-              if (lane == 0) mbar_arrive(smem_u32(&wfree[st]));
-            }
             if (hj == 0 && i >= C::kNumA) {
               // A-buffer b was last used by unit i - kNumA: wait for its
               // MMAs, and order the stores below after their operand reads
@@ -1369,6 +1375,7 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
                 tmem + lane_base + b * C::kAColsPerUnit + j * (kStageK / 2) + (2 * h) * 16;
             tmem_st_x16(acol, o[0]);
             tmem_st_x16(acol + 16, o[1]);
+            if (hj == 2 * KU - 1) release_chunk(st);
           }
         };
         if (fast) unit(std::true_type{});
@@ -1386,11 +1393,6 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
               *reinterpret_cast<const uint32_t*>(chunk + kWChunkBytes + (h * kTileN + r) * 4);
           decode_group<FMT>(g0, sv & 0xFFFFu, o[0]);
           decode_group<FMT>(g1, sv >> 16, o[1]);
-          if (hj == 2 * KU - 1) {
-            // the decode consumed every byte this warp read: release the chunk
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&wfree[st]));
-          }
           if (hj == 0 && i >= C::kNumA) {
             // A-buffer b was last used by unit i - kNumA: wait for its MMAs,
             // and order the stores below after their operand reads
@@ -1404,6 +1406,7 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
               tmem + lane_base + b * C::kAColsPerUnit + j * (kStageK / 2) + (2 * h) * 16;
           tmem_st_x16(acol, o[0]);
           tmem_st_x16(acol + 16, o[1]);
+          if (hj == 2 * KU - 1) release_chunk(st);
         }
       }
       if (!ok) break;
