@@ -1319,16 +1319,36 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
     const int i0 = kFirstReuse0 + grp - (kFirstReuse0 - G + grp >= C::kNumA ? G : 0);
     int st2 = (i0 - C::kNumA) % C::kXStages;
     uint32_t ph2 = ((i0 - C::kNumA) / C::kXStages) & 1;
-    // Gives chunk stage s back to the copies.  It stands after the unit's last
-    // stores to tensor memory, whose operands come out of the loads: an arrival
-    // does not wait for loads whose values nothing has used yet, and the chunk of
-    // unit i + kWStages could land before they had read this one.  (So it did with
-    // the arrival before those stores: in one of some 300 launches of 256-row tiles
-    // after a pause, eight or more weight rows had the codes, or the scales, of two
-    // units later.)
+    // Gives chunk stage s back to the copies.  An arrival does not wait for loads
+    // whose values nothing has used yet, and the chunk of unit i + kWStages could land
+    // before they had read this one.  (So it did: in one of some 300 launches of
+    // 256-row tiles after a pause, eight or more weight rows had the codes, or the
+    // scales, of two units later.)  So it stands after the unit's last stores to tensor
+    // memory, whose operands come out of the loads.  With two stages, where the next
+    // copy waits for it, the whole unit is loaded first and the arrival made to depend
+    // on it: lane 0's word of all loads is never less than the least.  (200 rows through
+    // 10880 x 2048 in FP16: 16.3 us after the stores, 14.9 so.  With more stages the
+    // minimum costs more than it gives: 107.5 and 108.2 us a decode step.)
+    constexpr bool kLoadAll = C::kWStages == 2 && KU == 1;
     auto release_chunk = [&](int s) {
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&wfree[s]));
+    };
+    [[maybe_unused]] auto release_loaded = [&](int s, uint32_t loaded) {
+      const uint32_t least = __reduce_min_sync(0xffffffffu, loaded);
+      if (lane == 0 && least <= loaded) mbar_arrive(smem_u32(&wfree[s]));
+    };
+    // a half's codes and scales: of 32 k each in g0 and g1
+    struct Half {
+      uint4 g0, g1;
+      uint32_t sv;
+      __device__ __forceinline__ uint32_t word() const { return g0.x ^ g1.x ^ sv; }
+    };
+    auto load_half = [&](const uint8_t* chunk, int h) {
+      using S = std::conditional_t<FMT == kMXFP4, uint16_t, uint32_t>;
+      return Half{*reinterpret_cast<const uint4*>(chunk + ((2 * h) * kTileN + r) * 16),
+                  *reinterpret_cast<const uint4*>(chunk + ((2 * h + 1) * kTileN + r) * 16),
+                  *reinterpret_cast<const S*>(chunk + kWChunkBytes + (h * kTileN + r) * sizeof(S))};
     };
     for (int32_t i = grp; i < nu; i += G) {
       if (!PETIT_CHECK(st >= 0 && st < C::kWStages && b >= 0 && b < C::kNumA && st2 >= 0 &&
@@ -1336,6 +1356,7 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
         break;
       if (!wait_lane(&wfull[st], ph)) break;
       bool ok = true;
+      [[maybe_unused]] Half second;   // kLoadAll: the unit's second half
       if constexpr (FMT == kMXFP4) {
         // The repack's per-chunk flag bytes (warp-uniform), read once per
         // unit: the unit's decode takes one multiply per word when every
@@ -1353,15 +1374,14 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
           for (int hj = 0; hj < 2 * KU; ++hj) {
             const int h = hj / KU, j = hj % KU;
             const uint8_t* chunk = sm_w + st * C::kWBytes + j * T::kChunkBytes;
-            const uint4 g0 =
-                *reinterpret_cast<const uint4*>(chunk + ((2 * h) * kTileN + r) * 16);
-            const uint4 g1 =
-                *reinterpret_cast<const uint4*>(chunk + ((2 * h + 1) * kTileN + r) * 16);
+            const Half w = hj > 0 && kLoadAll ? second : load_half(chunk, h);
+            if (kLoadAll && hj == 0) {
+              second = load_half(chunk, 1);
+              release_loaded(st, w.word() ^ second.word());
+            }
             uint32_t o[2][16];
-            const uint32_t sv =
-                *reinterpret_cast<const uint16_t*>(chunk + kWChunkBytes + (h * kTileN + r) * 2);
-            decode_group<FMT, kFast>(g0, sv & 0xFFu, o[0]);
-            decode_group<FMT, kFast>(g1, (sv >> 8) & 0xFFu, o[1]);
+            decode_group<FMT, kFast>(w.g0, w.sv & 0xFFu, o[0]);
+            decode_group<FMT, kFast>(w.g1, (w.sv >> 8) & 0xFFu, o[1]);
             if (hj == 0 && i >= C::kNumA) {
               // A-buffer b was last used by unit i - kNumA: wait for its
               // MMAs, and order the stores below after their operand reads
@@ -1375,7 +1395,7 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
                 tmem + lane_base + b * C::kAColsPerUnit + j * (kStageK / 2) + (2 * h) * 16;
             tmem_st_x16(acol, o[0]);
             tmem_st_x16(acol + 16, o[1]);
-            if (hj == 2 * KU - 1) release_chunk(st);
+            if (!kLoadAll && hj == 2 * KU - 1) release_chunk(st);
           }
         };
         if (fast) unit(std::true_type{});
@@ -1385,14 +1405,14 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
         for (int hj = 0; hj < 2 * KU; ++hj) {
           const int h = hj / KU, j = hj % KU;
           const uint8_t* chunk = sm_w + st * C::kWBytes + j * T::kChunkBytes;
-          const uint4 g0 = *reinterpret_cast<const uint4*>(chunk + ((2 * h) * kTileN + r) * 16);
-          const uint4 g1 =
-              *reinterpret_cast<const uint4*>(chunk + ((2 * h + 1) * kTileN + r) * 16);
+          const Half w = hj > 0 && kLoadAll ? second : load_half(chunk, h);
+          if (kLoadAll && hj == 0) {
+            second = load_half(chunk, 1);
+            release_loaded(st, w.word() ^ second.word());
+          }
           uint32_t o[2][16];
-          const uint32_t sv =
-              *reinterpret_cast<const uint32_t*>(chunk + kWChunkBytes + (h * kTileN + r) * 4);
-          decode_group<FMT>(g0, sv & 0xFFFFu, o[0]);
-          decode_group<FMT>(g1, sv >> 16, o[1]);
+          decode_group<FMT>(w.g0, w.sv & 0xFFFFu, o[0]);
+          decode_group<FMT>(w.g1, w.sv >> 16, o[1]);
           if (hj == 0 && i >= C::kNumA) {
             // A-buffer b was last used by unit i - kNumA: wait for its MMAs,
             // and order the stores below after their operand reads
@@ -1406,7 +1426,7 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
               tmem + lane_base + b * C::kAColsPerUnit + j * (kStageK / 2) + (2 * h) * 16;
           tmem_st_x16(acol, o[0]);
           tmem_st_x16(acol + 16, o[1]);
-          if (hj == 2 * KU - 1) release_chunk(st);
+          if (!kLoadAll && hj == 2 * KU - 1) release_chunk(st);
         }
       }
       if (!ok) break;
