@@ -2,7 +2,7 @@
 // projections and their product in one kernel.  The main loop is gemm.cu's; its
 // own translation unit, so that the two sets of kernels compile side by side.
 //
-// Bound as the GEMM is: 28672 x 8192 twice in NVFP4, one row 51 us (the weights at
+// Bound as the GEMM is: 28672 x 8192 twice in NVFP4, one row 52 us (the weights at
 // 5.1 TB/s), 128 rows 74 us, 4096 rows 2.15 ms (1.79 PFLOP/s; a long cuBLAS BF16
 // product runs at 1.75).  The [m, 2n] product of two launches would add its write
 // and read: 0.94 GB, 140 us, at 4096 rows.
