@@ -136,6 +136,7 @@ struct GatedParams : Params {
   int32_t a_rows;   // rows of an activation copy: the largest height, or half of it in pairs
   int32_t spread;   // tiles that begin in a range, rounded down, if they are dealt out (0: they are not)
   int32_t height[kMaxGroups + 1];   // activation rows a tile (the last: past the last group)
+  int32_t two_sums;   // 1: two A-buffers and two accumulators (Cfg::kTwoSums)
 };
 
 // Rows of the tiles of group g.
@@ -362,7 +363,8 @@ struct Cfg {
   // epilogue overlaps the next tile's MMAs (measured on GB300: gate_up at
   // m = 64 12 % faster than with two issuers and one accumulator each); at
   // N = 128 two issuers stay faster.
-  // (Two chunks a unit at N = 128, gated only, leave room for one accumulator.)
+  // (Two chunks a unit at N = 128, gated only: the two activation stages that fit keep
+  // two A-buffers in use, beside which there is room for two accumulators.)
   static constexpr int kMmaThreads = PAIR ? 1 : BN <= 32 ? 3 : BN == 128 && KU == 1 ? 2 : 1;
   // dequantiser groups (four warps each) taking units round-robin
   static constexpr int kDeqGroups = 2;
@@ -372,7 +374,12 @@ struct Cfg {
   // accumulator buffers per issuer: two when they fit beside three A-buffers
   // (the epilogue of one tile then overlaps the next tile's MMAs)
   static constexpr int kNumD =
-      kMmaThreads * 2 * BN + 3 * kAColsPerUnit <= static_cast<int>(kTmemCols) ? 2 : 1;
+      kMmaThreads * 2 * BN + (GATED && BN == 128 && KU == 2 && !PAIR ? 2 : 3) * kAColsPerUnit <= static_cast<int>(kTmemCols)
+          ? 2 : 1;
+  // Pairs of 128 rows and two chunks a unit hold three A-buffers and an accumulator,
+  // or (GatedParams::two_sums) two of each.
+  static constexpr bool kTwoSums = GATED && PAIR && BN == 128 && KU == 2;
+  static constexpr int kMaxD = kTwoSums ? 2 : kNumD;
   static constexpr int kNumA0 =
       (static_cast<int>(kTmemCols) - kMmaThreads * kNumD * BN) / kAColsPerUnit;
   // Every mbarrier is waited on by one fixed consumer that waits for each of
@@ -432,7 +439,7 @@ struct Cfg {
   static_assert(2 * kSmemBytes > 228 * 1024, "one CTA per SM");
   // barriers, tensor-memory holder, flags and the deferred fix-up job fit in
   // the 1024 bytes after the rings
-  static_assert((2 * kWStages + 3 * kXStages + kNumA + 2 * kNumD + kMaxMmaThreads + 1) * 8 + 16 +
+  static_assert((2 * kWStages + 3 * kXStages + kNumA + 2 * kMaxD + kMaxMmaThreads + 1) * 8 + 16 +
                         sizeof(GatedFixJob) + 16 <= 1024,
                 "barrier region");
 };
@@ -577,8 +584,8 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
   uint64_t* mdone = xfull + C::kXStages;
   uint64_t* afull = mdone + C::kXStages;
   uint64_t* dfull = afull + C::kNumA;
-  uint64_t* dempty = dfull + C::kNumD;
-  uint64_t* fin = dempty + C::kNumD;   // one per MMA issuer
+  uint64_t* dempty = dfull + C::kMaxD;
+  uint64_t* fin = dempty + C::kMaxD;   // one per MMA issuer
   uint64_t* epi_bar = fin + kMaxMmaThreads;
   // CTA pairs: xpeer[s] (even CTA) -- the odd CTA's half of activation stage
   // s has landed (forwarded by the odd CTA's warp 1)
@@ -610,6 +617,25 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
   uint32_t a_half_bytes = C::kAHalfBytes;
   if constexpr (GATED) a_half_bytes = static_cast<uint32_t>(p.a_rows) * 128;
   const uint32_t a_bytes = 2 * KU * a_half_bytes;
+  // tensor memory: A-buffers, and the accumulators behind them
+  // (constants but for Cfg::kTwoSums)
+  static_assert(!C::kTwoSums || (C::kNumA == 3 && C::kNumD == 1 && C::kAColsPerUnit == BN && 4 * BN == kTmemCols),
+                "two sums");
+#ifdef PETIT_GATED
+  const int32_t num_a = C::kTwoSums ? C::kNumA - p.two_sums : C::kNumA;
+  const int32_t d_cols = C::kTwoSums ? (C::kNumA - p.two_sums) * C::kAColsPerUnit : C::kDColBase;
+#else
+  constexpr int32_t num_a = C::kNumA, d_cols = C::kDColBase;
+#endif
+  // a segment's accumulator, and the parity of its use of it
+  auto sum_of = [&](auto seg) {
+    if constexpr (C::kTwoSums) return static_cast<int>(seg) & p.two_sums;
+    else return static_cast<int>(seg % C::kNumD);
+  };
+  auto sum_parity = [&](auto seg) {
+    if constexpr (C::kTwoSums) return static_cast<uint32_t>(seg >> p.two_sums) & 1u;
+    else return static_cast<uint32_t>((seg / C::kNumD) & 1);
+  };
   const int64_t u0 = cta_lo(p, static_cast<int32_t>(cta));
   const int64_t u1 = cta_lo(p, static_cast<int32_t>(cta) + 1);
   const int64_t KS = p.k_units;
@@ -630,7 +656,7 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
     // dequantiser and epilogue warps)
     for (int i = 0; i < C::kNumA; ++i)
       mbar_init(smem_u32(&afull[i]), kDeqGroupWarps * (PAIR ? 2 : 1));
-    for (int i = 0; i < C::kNumD; ++i) {
+    for (int i = 0; i < C::kMaxD; ++i) {
       mbar_init(smem_u32(&dfull[i]), C::kMmaThreads);
       mbar_init(smem_u32(&dempty[i]), 4 * (PAIR ? 2 : 1));
     }
@@ -893,11 +919,11 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
           cursor_next<BN>(p, ic);
         }
         const int32_t s1 = min(nu, s0 + (ks - (ku0 + s0) % ks));   // next tile boundary
-        const int d = seg % C::kNumD;
+        const int d = sum_of(seg);
         // Every issuer waits here, owning a unit of the segment or not: its
         // dfull arrival for this segment then cannot overtake the other
         // issuer's arrival for the segment that last used accumulator d.
-        if (!uwait(&dempty[d], static_cast<uint32_t>(((seg / C::kNumD) & 1) ^ 1))) break;
+        if (!uwait(&dempty[d], sum_parity(seg) ^ 1u)) break;
         bool seg_started = false;   // this issuer has written its accumulator in this segment
         for (; i < s1; i += C::kMmaThreads) {
           if (!uwait(&xfull[st], ph) || (PAIR && !uwait(&xpeer[st], ph)) ||
@@ -906,13 +932,13 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
             break;
           }
           tc_fence_after();
-          if (!PETIT_CHECK(st >= 0 && st < C::kXStages && b >= 0 && b < C::kNumA && d >= 0 &&
-                           d < C::kNumD)) {
+          if (!PETIT_CHECK(st >= 0 && st < C::kXStages && b >= 0 && b < num_a && d >= 0 &&
+                           d < C::kMaxD)) {
             ok = false;
             break;
           }
           const uint32_t a_smem = smem_u32(sm_a + st * C::kABytes);
-          const uint32_t d_tmem = tmem + C::kDColBase + (t * C::kNumD + d) * BN;
+          const uint32_t d_tmem = tmem + d_cols + (t * C::kNumD + d) * BN;
           const uint32_t a_tmem = tmem + b * C::kAColsPerUnit;
           if (elect_one()) {
 #pragma unroll
@@ -942,8 +968,8 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
             ph ^= 1u;
           }
           b += C::kMmaThreads;
-          if (b >= C::kNumA) {
-            b -= C::kNumA;
+          if (b >= num_a) {
+            b -= num_a;
             pb ^= 1u;
           }
         }
@@ -1070,7 +1096,7 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
       [[maybe_unused]] float alpha_up = alpha;
       if constexpr (GATED) alpha_up = p.group_up[ec.g];
       cursor_next<BN>(p, ec);
-      const int d = static_cast<int>(seg % C::kNumD);
+      const int d = sum_of(seg);
       // split tile: its contributors and their partial slots (every
       // contributor but the first starts inside the tile, slot 2c; the first
       // uses its second slot unless its range starts at the tile)
@@ -1091,8 +1117,8 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
         if (last_seg && epi_tid == 0)
           *epi_flag = ld_acquire_gpu(ctr) == static_cast<uint32_t>(c_last - c_first);
       }
-      if (!PETIT_CHECK(d >= 0 && d < C::kNumD)) break;
-      if (!wait_lane(&dfull[d], static_cast<uint32_t>((seg / C::kNumD) & 1))) break;
+      if (!PETIT_CHECK(d >= 0 && d < C::kMaxD)) break;
+      if (!wait_lane(&dfull[d], sum_parity(seg))) break;
       tc_fence_after();
       // issuer t wrote its accumulator iff the segment holds a unit with
       // CTA-local index i % kMmaThreads == t
@@ -1154,7 +1180,7 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
         }
       }
       const uint32_t tbase =
-          tmem + (static_cast<uint32_t>(32 * q) << 16) + C::kDColBase + d * BN;
+          tmem + (static_cast<uint32_t>(32 * q) << 16) + d_cols + d * BN;
       const int64_t ncol = (static_cast<int64_t>(nt) * wmul + rank) * kTileN + r;
       [[maybe_unused]] const int64_t ccol = (ncol - r) / 2 + 16 * q;   // gated: this warp's 16 columns of C
       const int64_t slot = 2 * sid(cta) + (tile == first_tile_of_cta ? 0 : 1);
@@ -1314,11 +1340,11 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
     const int32_t nu = static_cast<int32_t>(u1 - u0);
     int st = grp, b = grp;
     uint32_t ph = 0;
-    // first own unit that reuses an A-buffer: i0 >= kNumA, i0 = grp (mod G)
-    constexpr int kFirstReuse0 = (C::kNumA + G - 1) / G * G;   // for grp = 0
-    const int i0 = kFirstReuse0 + grp - (kFirstReuse0 - G + grp >= C::kNumA ? G : 0);
-    int st2 = (i0 - C::kNumA) % C::kXStages;
-    uint32_t ph2 = ((i0 - C::kNumA) / C::kXStages) & 1;
+    // first own unit that reuses an A-buffer: i0 >= num_a, i0 = grp (mod G)
+    const int first_reuse0 = (num_a + G - 1) / G * G;   // for grp = 0
+    const int i0 = first_reuse0 + grp - (first_reuse0 - G + grp >= num_a ? G : 0);
+    int st2 = (i0 - num_a) % C::kXStages;
+    uint32_t ph2 = ((i0 - num_a) / C::kXStages) & 1;
     // Gives chunk stage s back to the copies.  An arrival does not wait for loads
     // whose values nothing has used yet, and the chunk of unit i + kWStages could land
     // before they had read this one.  (So it did: in one of some 300 launches of
@@ -1351,7 +1377,7 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
                   *reinterpret_cast<const S*>(chunk + kWChunkBytes + (h * kTileN + r) * sizeof(S))};
     };
     for (int32_t i = grp; i < nu; i += G) {
-      if (!PETIT_CHECK(st >= 0 && st < C::kWStages && b >= 0 && b < C::kNumA && st2 >= 0 &&
+      if (!PETIT_CHECK(st >= 0 && st < C::kWStages && b >= 0 && b < num_a && st2 >= 0 &&
                        st2 < C::kXStages))
         break;
       if (!wait_lane(&wfull[st], ph)) break;
@@ -1382,7 +1408,7 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
             uint32_t o[2][16];
             decode_group<FMT, kFast>(w.g0, w.sv & 0xFFu, o[0]);
             decode_group<FMT, kFast>(w.g1, (w.sv >> 8) & 0xFFu, o[1]);
-            if (hj == 0 && i >= C::kNumA) {
+            if (hj == 0 && i >= num_a) {
               // A-buffer b was last used by unit i - kNumA: wait for its
               // MMAs, and order the stores below after their operand reads
               if (!wait_lane(&mdone[st2], ph2)) {
@@ -1413,7 +1439,7 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
           uint32_t o[2][16];
           decode_group<FMT>(w.g0, w.sv & 0xFFFFu, o[0]);
           decode_group<FMT>(w.g1, w.sv >> 16, o[1]);
-          if (hj == 0 && i >= C::kNumA) {
+          if (hj == 0 && i >= num_a) {
             // A-buffer b was last used by unit i - kNumA: wait for its MMAs,
             // and order the stores below after their operand reads
             if (!wait_lane(&mdone[st2], ph2)) {
@@ -1444,8 +1470,8 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
         ph ^= 1u;
       }
       b += G;
-      if (b >= C::kNumA) b -= C::kNumA;
-      if (i >= C::kNumA) {
+      if (b >= num_a) b -= num_a;
+      if (i >= num_a) {
         st2 += G;
         if (st2 >= C::kXStages) {
           st2 -= C::kXStages;
@@ -1483,12 +1509,12 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
       const int fg = warp >> 2;
       const bool mine =
           fg < kFixGroups &&
-          PETIT_CHECK(f.d >= 0 && f.d < C::kNumD && f.c_first >= 0 && f.c_first <= cta &&
+          PETIT_CHECK(f.d >= 0 && f.d < C::kMaxD && f.c_first >= 0 && f.c_first <= cta &&
                       cta <= f.c_last && f.c_last < P && f.first_slot >= 0 &&
                       f.first_slot < 2 * NS);
       const int q = warp & 3;
       const int r = 32 * q + lane;
-      const uint32_t tbase = tmem + (static_cast<uint32_t>(32 * q) << 16) + C::kDColBase +
+      const uint32_t tbase = tmem + (static_cast<uint32_t>(32 * q) << 16) + d_cols +
                              f.d * BN + fg * kCols;
       uint16_t* gst = reinterpret_cast<uint16_t*>(sm_a) + (fg % kFixGroups) * 16 * kTileN;
 #pragma unroll 1
@@ -1577,12 +1603,12 @@ __global__ void __launch_bounds__((Cfg<FMT, BN, KU, PAIR, GATED>::kThreads), 1)
       int rows_here = kCols;
       if constexpr (kStrided) rows_here = f.height - row_base;
       if (fg < kFixGroups && (GATED || !*abort_flag) &&
-          PETIT_CHECK(f.d >= 0 && f.d < C::kNumD && f.c_first >= 0 && f.c_first <= cta &&
+          PETIT_CHECK(f.d >= 0 && f.d < C::kMaxD && f.c_first >= 0 && f.c_first <= cta &&
                       cta <= f.c_last && f.c_last < P && f.first_slot >= 0 &&
                       f.first_slot < 2 * NS)) {
         const int q = warp & 3;
         const int r = 32 * q + lane;
-        const uint32_t tbase = tmem + (static_cast<uint32_t>(32 * q) << 16) + C::kDColBase +
+        const uint32_t tbase = tmem + (static_cast<uint32_t>(32 * q) << 16) + d_cols +
                                f.d * BN + row_base;
   #pragma unroll 1
         for (int c0 = 0; c0 < rows_here; c0 += kStep) {
@@ -2224,6 +2250,14 @@ GemmPlan plan_gated(const int64_t* row_off, int num_groups, int64_t n, int64_t k
   if (num_groups == 1 && !pl.use_bounds &&
       ((codes > int64_t(64) << 20 && activation_tiles >= 2) || (codes > int64_t(48) << 20 && activation_tiles >= 8)))
     pl.spread = static_cast<int>(pl.tile_base[num_groups] / pl.num_ctas);
+  // Two accumulators where a range has more tiles to overlap (2 us each) than the third
+  // A-buffer saves (0.07 us a unit).  Us with one and with two: 8 experts of 100 rows
+  // through 28672 x 4096 152 and 142, of 96 rows through 4096 x 1024 13.5 and 12.2; 90
+  // rows through 28672 x 4096 25.0 and 26.8, 128 rows through 57344 x 8192 74 and 77.
+  if (pl.bn == 128 && pl.pair && pl.ku == 2) {
+    const int64_t per_tile = pl.k_stages / pl.ku, a_range = pl.units / pl.num_ctas;
+    pl.two_sums = 27 * (a_range - per_tile) > a_range * per_tile;
+  }
   lay_workspace(pl);
   return pl;
 }

@@ -18,6 +18,7 @@ cudaError_t launch_gated(const GemmPlan& pl, const GemmArgs& a, const GatedArgs&
   prm.act = g.act;
   prm.a_rows = pl.a_rows;
   prm.spread = pl.spread;
+  prm.two_sums = pl.two_sums;
   for (int i = 0; i < pl.num_groups; ++i) {
     prm.group_up[i] = g.group_up[i];
     prm.height[i] = pl.height[i];

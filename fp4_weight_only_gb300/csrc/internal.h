@@ -63,6 +63,7 @@ struct GemmPlan {
   int32_t height[kMaxGroups];
   int32_t a_rows;
   int32_t spread;   // whole tiles a range that are dealt out num_ctas apart (0: none)
+  int32_t two_sums;   // 1: two accumulators, for pairs of 128 rows and two chunks a unit
 };
 
 // pair_cap: CTA pairs that can be resident at once (pair_capacity()), 0 to

@@ -121,3 +121,27 @@ def test_tiles_dealt_out_to_ranges(cuda_lib, fmt, m, k):
             ws = cuda_lib.Workspace()
             checked = one(a, "silu", workspace=ws)
             assert ws.status() == 0 and torch.equal(checked.double(), got)
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("n,sizes", [(2048, [100, 0, 128, 33, 97, 100, 64, 128, 120]),    # pairs, many tiles a range
+                                     (7168, [90]), (1088, [100, 128, 100, 0, 96, 128])])  # pairs, few; no pairs
+def test_accumulators_in_turn(cuda_lib, fmt, n, sizes):
+    k, scales = 1024, SCALES[fmt]
+    mats = [matrices(cuda_lib, n, k, fmt, 90 + 2 * i, scales) for i in range(2)]   # (experts take one of two in turn)
+    rep = torch.cat([mats[e % 2][0] for e in range(len(sizes))])
+    off = [0]
+    for s in sizes:
+        off.append(off[-1] + s)
+    a = activations(off[-1], k, fmt, 3)
+    ws = cuda_lib.Workspace()
+    torch.cuda.synchronize()
+    call = lambda: cuda_lib.moe_gated_gemm(a, rep, off, n, fmt, [scales] * len(sizes), "silu", ws)  # noqa: E731
+    y = call()
+    for e, (lo, hi) in enumerate(zip(off, off[1:])):
+        if lo < hi:
+            check(y[lo:hi], a[lo:hi], *mats[e % 2][1:], scales, "silu", f"expert {e}")
+    assert all(torch.equal(call(), y) for _ in range(20)) and ws.status() == 0
+    with cuda_lib.bounds_checked():
+        ws = cuda_lib.Workspace()
+        assert torch.equal(call(), y) and ws.status() == 0
